@@ -1,0 +1,150 @@
+// act.h -- activations, their derivatives, and the finding of a row block's group.
+#pragma once
+#include "device_common.h"
+#include "ops.h"
+
+namespace muon {
+
+// act(z) in float32.  Each is z times a factor in [0, 1]; the tanh form of
+// gelu uses (1 + tanh u) / 2 = sigmoid(2 u), which keeps its relative
+// accuracy where tanh u nears -1.  NaN stays NaN.
+__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + __expf(-v)); }
+constexpr float kGeluC = 0.7978845608028654f, kGeluA = 0.044715f;  // sqrt(2 / pi); the cubic term
+__device__ __forceinline__ float act_f(float z, int act) {
+  switch (act) {
+    case MUON_ACT_RELU: return z <= 0.f ? 0.f : z;
+    case MUON_ACT_SILU: return z * sigmoid_f(z);
+    case MUON_ACT_GELU: return z * (0.5f + 0.5f * erff(z * 0.7071067811865476f));
+    case MUON_ACT_GELU_TANH: return z * sigmoid_f(2.f * kGeluC * (z + kGeluA * z * z * z));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case MUON_ACT_RELU: return z <= 0.f ? 0.f : 1.f;
+    case MUON_ACT_SILU: {
+      const float q = sigmoid_f(z);
+      return q + z * q * (1.f - q);
+    }
+    case MUON_ACT_GELU:
+      return 0.5f + 0.5f * erff(z * 0.7071067811865476f) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    case MUON_ACT_GELU_TANH: {
+      const float q = sigmoid_f(2.f * kGeluC * (z + kGeluA * z * z * z));
+      return q + z * q * (1.f - q) * 2.f * kGeluC * (1.f + 3.f * kGeluA * z * z);
+    }
+    default: return 1.f;
+  }
+}
+
+// Orders this wave's LDS accesses: lanes exchange values through LDS that no
+// other wave touches (the LDS itself serves a wave's accesses in order).
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Row range [lo, hi) of group e; group `groups` is the rows past the last
+// one.  The first group starts at row 0, and offsets are clamped into
+// [0, rows], so whatever they hold, every row read or written lies inside
+// the tensors.
+__device__ __forceinline__ void group_range(const int32_t* offsets, int groups, int64_t rows, int e, int& lo, int& hi) {
+  const int r = (int)rows;
+  lo = e == 0 ? 0 : min(max(offsets[e], 0), r);
+  hi = e == groups ? r : max(lo, min(offsets[e + 1], r));
+}
+
+// The group of row block `mt` when every group's rows are cut into blocks of
+// BM: each lane counts its share of the groups' blocks, a wave-wide prefix
+// sum finds the lane whose share holds mt.  Results are uniform over the
+// wave.  False: there are fewer blocks.
+template <int BM>
+__device__ __forceinline__ bool find_group(const int32_t* offsets, int groups, int64_t rows, int mt, int& e, int& row0,
+                                           int& end) {
+  const int lane = threadIdx.x & 63;
+  const int per = (groups + 64) / 64;  // groups + 1 ranges over 64 lanes
+  const int e0 = lane * per, e1 = min(e0 + per, groups + 1);
+  int cnt = 0;
+  for (int i = e0; i < e1; ++i) {
+    int lo, hi;
+    group_range(offsets, groups, rows, i, lo, hi);
+    cnt += (hi - lo + BM - 1) / BM;
+  }
+  int incl = cnt;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += v;
+  }
+  int left = mt - (incl - cnt);  // blocks of this lane's share ahead of mt
+  const uint64_t hit = __ballot(left >= 0 && left < cnt);
+  if (hit == 0) return false;
+  int fe = 0, f0 = 0, f1 = 0;
+  if (left >= 0 && left < cnt) {
+    for (int i = e0; i < e1; ++i) {
+      int lo, hi;
+      group_range(offsets, groups, rows, i, lo, hi);
+      const int c = (hi - lo + BM - 1) / BM;
+      if (left < c) {
+        fe = i;
+        f0 = lo + left * BM;
+        f1 = hi;
+        break;
+      }
+      left -= c;
+    }
+  }
+  const int src = __builtin_ctzll(hit);
+  e = __builtin_amdgcn_readlane(fe, src);
+  row0 = __builtin_amdgcn_readlane(f0, src);
+  end = __builtin_amdgcn_readlane(f1, src);
+  return true;
+}
+
+// Eight consecutive elements as float32 (vec: 16-byte pieces; otherwise one
+// by one, n of them inside the row, the others zero).
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    if (vec) {
+      const u32x4_t w = *reinterpret_cast<const MUON_GLOBAL u32x4_t*>(as_global(p));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+      return;
+    }
+  } else {
+    if (vec) {
+      const MUON_GLOBAL f32x4_t* q = reinterpret_cast<const MUON_GLOBAL f32x4_t*>(as_global(p));
+      const f32x4_t a = q[0], b = q[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? x_to_f32(p[i]) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&v)[8]) {
+  if (vec) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<MUON_GLOBAL u32x4_t*>(as_global(p)) =
+          u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    } else {
+      MUON_GLOBAL f32x4_t* q = reinterpret_cast<MUON_GLOBAL f32x4_t*>(as_global(p));
+      q[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+      q[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = cvt_x<T>(v[i]);
+}
+
+}  // namespace muon

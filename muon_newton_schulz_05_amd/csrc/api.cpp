@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "../../include/muon.h"
+#include "error.h"
 #include "kernels.h"
 #include "planner.h"
 
@@ -39,6 +40,16 @@ struct TimedLaunch {
 };
 
 }  // namespace
+
+int muon::set_error(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return code;
+}
 
 struct muon_plan {
   uint32_t magic = kPlanMagic;

@@ -1,0 +1,419 @@
+// gemm.h -- the tiled matrix product behind the linear and expert layers:
+// C[i][j] = sum_k A[i][k] B[j][k], with either operand contiguous along k or
+// along its rows, over groups of rows or of the contraction, and bias,
+// activation and residual in the epilogue.
+//
+// A workgroup owns a BM x BN tile of C; each of its waves owns a block of
+// 32 x 32 matrix-core products.  Operand k-slices of 128 bytes a row (64
+// bf16 or 32 float32 values) go from memory straight into LDS, NS stages
+// deep, with one barrier a slice.  What is out of range (rows past the
+// group, the contraction's tail) is given an offset past the buffer
+// descriptor's end, for which the load writes zeros to LDS.
+//
+//  - An operand contiguous along k sits in LDS as rows of 128 bytes; the
+//    16-byte chunk c of row r at slot c ^ (r / 2 mod 8), so that 16 lanes
+//    reading one chunk of 16 rows touch 16 distinct 16-byte bank groups.
+//  - An operand contiguous along its rows sits as k-rows.  bf16: fragments
+//    are read by ds_read_b64_tr_b16, which hands lane i of 16 the column i of
+//    a 4 x 16 block (four k of one row of the operand); k-rows k .. k + 3 of one
+//    64-byte block are kept in distinct banks by chunk ^ 4 (k mod 4).
+//    float32: 32 lanes read 32 consecutive values, no transposition.
+#pragma once
+#include "act.h"
+#include "device_common.h"
+#include "ops.h"
+
+namespace muon {
+namespace {
+
+#define LDS_PTR __attribute__((address_space(3)))
+
+constexpr uint32_t kNoLoad = 0x80000000u;     // an offset past every descriptor's end
+constexpr uint32_t kRecords = 0x7fffffffu;
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// 16 bytes a lane from base + off (zeros past the descriptor's end) to 1 KB of
+// LDS, lane l at byte 16 l.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, char* dst) {
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, kRecords, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void LDS_PTR*)dst, 16, off, 0, 0, 0);
+}
+// Wait until at most N of this wave's loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <typename T> struct Mma;
+template <> struct Mma<uint16_t> {
+  typedef bf16x8_t Frag;  // eight k of one row: k = 16 s + 8 (lane / 32) + 0..7
+  static __device__ __forceinline__ f32x16_t mul(Frag a, Frag b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct Mma<float> {
+  typedef f32x4_t Frag;   // four k of one row: k = 8 s + 4 (lane / 32) + 0..3
+  static __device__ __forceinline__ f32x16_t mul(Frag a, Frag b, f32x16_t c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+  }
+};
+
+// One operand's tile: R rows x one k-slice.
+template <typename T, int R, bool TR, int NW, bool DIRECT>
+struct Panel {
+  static constexpr int EPC = 16 / sizeof(T);          // elements of a 16-byte chunk
+  static constexpr int BK = 128 / sizeof(T);          // k of a slice
+  static constexpr int RB = TR ? R * (int)sizeof(T) : 128;  // bytes of an LDS row
+  static constexpr int CPR = RB / 16;                 // its chunks
+  static constexpr int BYTES = R * 128;
+  static constexpr int LI = BYTES / 1024 / NW;        // 1 KB loads a wave and slice
+  static_assert(BYTES % (1024 * NW) == 0, "whole loads");
+  typedef typename Mma<T>::Frag Frag;
+
+  static __device__ __forceinline__ int swz(int row) {
+    if (!TR) return (row >> 1) & 7;
+    if (sizeof(T) == 4) return (((row >> 2) & 1) << 3) & (CPR - 1);
+    if (CPR == 8) return ((row >> 1) & 1) << 2;
+    return ((row & 3) << 2) & (CPR - 1);
+  }
+
+  const char* base;     // first element of this tile at k = 0 of the group
+  int64_t ld;           // bytes from one row (k-row when TR) to the next
+  uint32_t off[LI];     // this lane's offsets; kNoLoad outside the tile's rows
+  int left[LI];         // not DIRECT: elements of the chunk inside the rows (TR) or 1 / 0
+  u32x4_t reg[DIRECT ? 1 : LI];
+
+  static __device__ __forceinline__ int slot(int u, int wave, int lane) { return (wave + NW * u) * 64 + lane; }
+  static __device__ __forceinline__ int lrow(int s) { return s / CPR; }
+  static __device__ __forceinline__ int chunk(int s) { return (s % CPR) ^ swz(s / CPR); }
+
+  // rows: rows of the operand inside the tile (at most R).
+  __device__ __forceinline__ void init(const char* p, int64_t ld_bytes, int rows, int wave, int lane) {
+    base = p;
+    ld = ld_bytes;
+#pragma unroll
+    for (int u = 0; u < LI; ++u) {
+      const int s = slot(u, wave, lane), r = lrow(s), c = chunk(s);
+      if constexpr (DIRECT) {
+        const bool ok = TR ? c * EPC < rows : r < rows;
+        off[u] = ok ? (uint32_t)(r * (int)ld_bytes + c * 16) : kNoLoad;
+      } else {
+        left[u] = TR ? min(EPC, rows - c * EPC) : (r < rows ? 1 : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ const char* at(int kt) const { return base + (TR ? (int64_t)kt * BK * ld : (int64_t)kt * 128); }
+
+  // DIRECT: slice kt into LDS; k_left: elements of the contraction from this
+  // slice on.
+  __device__ __forceinline__ void issue(int kt, int k_left, char* st, int wave, int lane) {
+    const char* p = at(kt);
+    if (k_left >= BK) {
+#pragma unroll
+      for (int u = 0; u < LI; ++u) load_to_lds(p, off[u], st + (wave + NW * u) * 1024);
+    } else {
+#pragma unroll
+      for (int u = 0; u < LI; ++u) {
+        const int s = slot(u, wave, lane);
+        const int kk = TR ? lrow(s) : chunk(s) * EPC;
+        load_to_lds(p, kk < k_left ? off[u] : kNoLoad, st + (wave + NW * u) * 1024);
+      }
+    }
+  }
+  // Otherwise: slice kt into registers (any alignment; a chunk that is only
+  // partly inside is taken element by element), then from there to LDS.
+  __device__ __forceinline__ void fetch(int kt, int k_left, int wave, int lane) {
+#pragma unroll
+    for (int u = 0; u < LI; ++u) {
+      const int s = slot(u, wave, lane), r = lrow(s), c = chunk(s);
+      const int n = TR ? (r < k_left ? left[u] : 0) : (left[u] ? min(EPC, k_left - c * EPC) : 0);
+      const char* p = at(kt) + (int64_t)r * ld + c * 16;
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (n >= EPC) {
+        __builtin_memcpy(&v, p, 16);
+      } else {
+        const T* q = reinterpret_cast<const T*>(p);
+#pragma unroll
+        for (int i = 0; i < EPC; ++i)
+          if (i < n) {
+            if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(q[i]);
+            else v[i / 2] |= (uint32_t)q[i] << (16 * (i & 1));
+          }
+      }
+      reg[u] = v;
+    }
+  }
+  __device__ __forceinline__ void put(char* st, int wave, int lane) const {
+#pragma unroll
+    for (int u = 0; u < LI; ++u) *reinterpret_cast<u32x4_t*>(st + (wave + NW * u) * 1024 + lane * 16) = reg[u];
+  }
+
+  // The fragment of substep s (16 bf16 or 8 float32 of k) for rows
+  // r0 .. r0 + 31 of the tile (r0 a multiple of 32).
+  static __device__ __forceinline__ Frag frag(const char* st, int r0, int s, int lane) {
+    if constexpr (!TR) {
+      const int r = r0 + (lane & 31);
+      return *reinterpret_cast<const Frag*>(st + r * 128 + (((2 * s + (lane >> 5)) ^ swz(r)) << 4));
+    } else if constexpr (sizeof(T) == 2) {
+      const int g = lane >> 4, i = lane & 15;
+      const int k = 16 * s + 8 * (g >> 1) + (i >> 2);
+      const int c = (r0 >> 3) + 2 * (g & 1) + ((i & 3) >> 1);
+      const char* p = st + k * RB + ((c ^ swz(k)) << 4) + (i & 1) * 8;
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4_t LDS_PTR*)p);
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4_t LDS_PTR*)(p + 4 * RB));
+      typedef short s16x8_t __attribute__((ext_vector_type(8)));
+      const s16x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(Frag, v);
+    } else {
+      const int c = (r0 + (lane & 31)) >> 2;
+      Frag v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = 8 * s + 4 * (lane >> 5) + j;
+        v[j] = *reinterpret_cast<const float*>(st + k * RB + ((c ^ swz(k)) << 4) + (lane & 3) * 4);
+      }
+      return v;
+    }
+  }
+};
+
+// z = v + bias (stored where asked), y = act(z) + res, eight columns of one row.
+template <typename T>
+__device__ __forceinline__ void finish8(const GemmArgs& g, float (&v)[8], const float (&bias)[8], int64_t e, int64_t row,
+                                        int col, int n) {
+  const bool vec = g.vec != 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += bias[i];
+  const int64_t at = e * g.sc + row * g.ldc + col;
+  if (g.z) store8(static_cast<T*>(g.z) + at, n, vec, v);
+  if (g.act != MUON_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], g.act);
+  }
+  if (g.res) {
+    float r[8];
+    load8(static_cast<const T*>(g.res) + row * g.ldr + col, n, vec, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += r[i];
+  }
+  store8(static_cast<T*>(g.c) + at, n, vec, v);
+}
+
+// Workgroups go to the 8 XCDs round robin: block b of n takes the place in
+// which each XCD walks one contiguous stretch.
+__device__ __forceinline__ int xcd_place(int b, int n) {
+  const int x = b & 7, q = n >> 3, r = n & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+// Tile t of a tiles_m x tiles_n grid, walked down stripes of 4 row tiles:
+// the 32 tiles an XCD runs at once share 4 row and 8 column panels in its L2.
+__device__ __forceinline__ void stripe(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per = 4 * tiles_n, s = t / per, w = min(4, tiles_m - 4 * s), u = t - s * per;
+  tn = u / w;
+  tm = 4 * s + u - tn * w;
+}
+
+template <typename T, int BM, int BN, int WGM, int WGN, int NS, bool TA, bool TB, bool DIRECT, int MINB>
+__global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
+  constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 32, FN = WN / 32;
+  typedef Panel<T, BM, TA, NW, DIRECT> PA;
+  typedef Panel<T, BN, TB, NW, DIRECT> PB;
+  typedef typename Mma<T>::Frag Frag;
+  constexpr int BK = PA::BK, STAGE = PA::BYTES + PB::BYTES;
+  constexpr int STRIDE = WN * 4 + 32;  // bytes of a staged epilogue row: rows r and r + 4 fall on opposite bank halves
+  constexpr int LDS = NS * STAGE > NW * 32 * STRIDE ? NS * STAGE : NW * 32 * STRIDE;
+  __shared__ __attribute__((aligned(1024))) char lds[LDS];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WGN, wn = wave % WGN;
+
+  // ---- which tile
+  constexpr bool GK = TA && TB;  // groups divide the contraction
+  const int tiles = g.tiles_m * g.tiles_n;
+  int b = blockIdx.x, split = 0, e = 0, tm, tn;
+  if (g.splits > 1) {
+    split = b / tiles;
+    b -= split * tiles;
+  }
+  if (GK && g.offsets) {
+    e = b / tiles;
+    b -= e * tiles;
+  }
+  stripe(xcd_place(b, tiles), g.tiles_m, g.tiles_n, tm, tn);
+  int64_t row0 = (int64_t)tm * BM, end = g.m, k0 = 0, k1 = g.k;
+  if (g.offsets) {
+    int lo, hi;
+    if (GK) {
+      group_range(g.offsets, g.groups, g.k, e, lo, hi);
+      k0 = lo;
+      k1 = hi;
+    } else {
+      if (!find_group<BM>(g.offsets, g.groups, g.m, tm, e, lo, hi)) return;  // uniform, before any barrier
+      row0 = lo;
+      end = hi;
+      if (e == g.groups) k1 = 0;  // rows past the last group: zeros
+    }
+  }
+  if (g.splits > 1) {
+    k0 = (int64_t)split * g.k_per;
+    k1 = min(k0 + g.k_per, k1);
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int rows_a = (int)min((int64_t)BM, end - row0), rows_b = (int)min((int64_t)BN, g.n - (int64_t)tn * BN);
+  const int64_t kk = max((int64_t)0, k1 - k0);
+  const int nk = (int)((kk + BK - 1) / BK);
+  PA pa;
+  PB pb;
+  {
+    const int64_t ra = GK ? (int64_t)tm * BM : row0, cb = (int64_t)tn * BN;
+    const T* A = static_cast<const T*>(g.a) + (TA ? k0 * g.lda + ra : ra * g.lda + k0);
+    const T* B = static_cast<const T*>(g.b) + (GK || k1 == 0 ? 0 : e * g.sb) + (TB ? k0 * g.ldb + cb : cb * g.ldb + k0);
+    pa.init(reinterpret_cast<const char*>(A), g.lda * (int64_t)sizeof(T), rows_a, wave, lane);
+    pb.init(reinterpret_cast<const char*>(B), g.ldb * (int64_t)sizeof(T), rows_b, wave, lane);
+  }
+
+  f32x16_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x16_t{};
+
+  auto multiply = [&](const char* st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      Frag af[FM], bf[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) af[i] = PA::frag(st, wm * WM + 32 * i, s, lane);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) bf[j] = PB::frag(st + PA::BYTES, wn * WN + 32 * j, s, lane);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(af[i], bf[j], acc[i][j]);
+    }
+  };
+
+  if constexpr (DIRECT) {
+    constexpr int L = PA::LI + PB::LI;
+    auto issue = [&](int kt, char* fill) __attribute__((always_inline)) {
+      const int k_left = (int)min((int64_t)BK, kk - (int64_t)kt * BK);
+      pa.issue(kt, k_left, fill, wave, lane);
+      pb.issue(kt, k_left, fill + PA::BYTES, wave, lane);
+    };
+#pragma unroll
+    for (int p = 0; p < NS - 1; ++p)
+      if (p < nk) issue(p, lds + p * STAGE);
+    int stage = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+      // Slices kt + 1 .. kt + NS - 2 may stay in flight; the barrier then says
+      // that slice kt is whole and that slice kt - 1 has been read by all.
+      static_assert(NS <= 4 && 2 * L < 64, "waits");
+      const int fly = min(NS - 2, nk - 1 - kt);
+      if (fly <= 0) wait_loads<0>();
+      else if (fly == 1) wait_loads<L>();
+      else wait_loads<2 * L>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      // The stage being filled and the one being read are never the same:
+      // __restrict says so, or the compiler would wait for the loads in
+      // flight ahead of every transposing read.
+      auto step = [&](char* __restrict fill, const char* __restrict st) __attribute__((always_inline)) {
+        if (kt + NS - 1 < nk) issue(kt + NS - 1, fill);
+        multiply(st);
+      };
+      step(lds + (stage == 0 ? NS - 1 : stage - 1) * STAGE, lds + stage * STAGE);
+      stage = stage == NS - 1 ? 0 : stage + 1;
+    }
+  } else {
+    auto fetch = [&](int kt) {
+      const int k_left = (int)min((int64_t)BK, kk - (int64_t)kt * BK);
+      pa.fetch(kt, k_left, wave, lane);
+      pb.fetch(kt, k_left, wave, lane);
+    };
+    if (nk > 0) fetch(0);
+    for (int kt = 0; kt < nk; ++kt) {
+      char* st = lds + (kt & 1) * STAGE;  // last read at slice kt - 2, a barrier ago
+      pa.put(st, wave, lane);
+      pb.put(st + PA::BYTES, wave, lane);
+      if (kt + 1 < nk) fetch(kt + 1);
+      __syncthreads();
+      multiply(st);
+    }
+  }
+  __syncthreads();  // every wave is done with the operand stages
+
+  // ---- epilogue: 32 rows at a time through this wave's own staging, so that
+  // a row of C leaves as whole 16-byte pieces.  Register 4 q + u of a block is
+  // row 8 q + 4 (lane / 32) + u, column lane mod 32.
+  constexpr int LPR = WN / 8, RPP = 64 / LPR;
+  char* stg = lds + wave * 32 * STRIDE;
+  const int col = tn * BN + wn * WN + 8 * (lane % LPR);
+  const int n = (int)min((int64_t)8, g.n - col);
+  float bias[8] = {};
+  if (g.bias && n > 0 && !g.part && !(!GK && e == g.groups && g.offsets))
+    load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n, g.vec != 0, bias);
+  const int64_t crow0 = GK ? (int64_t)tm * BM : row0;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int lr = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        *reinterpret_cast<float*>(stg + lr * STRIDE + (32 * j + (lane & 31)) * 4) = acc[i][j][r];
+      }
+    wave_fence();
+#pragma unroll
+    for (int p = 0; p < 32 / RPP; ++p) {
+      const int lr = p * RPP + lane / LPR;
+      const f32x4_t* q = reinterpret_cast<const f32x4_t*>(stg + lr * STRIDE + (lane % LPR) * 32);
+      const f32x4_t x = q[0], y = q[1];
+      float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      const int64_t row = crow0 + wm * WM + 32 * i + lr;
+      if (row < end && n > 0) {
+        if (g.part) store8(g.part + ((int64_t)split * g.m + row) * g.n + col, n, g.n % 8 == 0, v);
+        else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);
+      }
+    }
+    wave_fence();
+  }
+}
+
+// Joins a split contraction: the partials of an entry are added in split
+// order, then the epilogue runs as in the kernel above.
+template <typename T>
+__global__ __launch_bounds__(256) void k_gemm_join(GemmArgs g) {
+  const int64_t per = (g.n + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= per * g.m) return;
+  const int64_t row = i / per;
+  const int col = (int)(i - row * per) * 8, n = (int)min((int64_t)8, g.n - col);
+  float v[8] = {}, bias[8] = {};
+  for (int s = 0; s < g.splits; ++s) {
+    float p[8];
+    load8(g.part + ((int64_t)s * g.m + row) * g.n + col, n, g.n % 8 == 0, p);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += p[k];
+  }
+  if (g.bias) load8(static_cast<const T*>(g.bias) + col, n, g.vec != 0, bias);
+  finish8<T>(g, v, bias, 0, row, col, n);
+}
+
+template <typename T, int BM, int BN, int WGM, int WGN, int NS, bool DIRECT, int MINB>
+hipError_t launch_tile(const GemmArgs& g, bool ta, bool tb, hipStream_t s) {
+  const int64_t blocks = (int64_t)g.tiles_m * g.tiles_n * g.splits * (ta && tb && g.offsets ? g.groups : 1);
+  if (blocks <= 0) return hipSuccess;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks), block(64 * WGM * WGN);
+  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, NS, true, true, DIRECT, MINB>), grid, block, 0, s, g);
+  else if (tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, NS, false, true, DIRECT, MINB>), grid, block, 0, s, g);
+  else if (!ta) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, NS, false, false, DIRECT, MINB>), grid, block, 0, s, g);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace muon

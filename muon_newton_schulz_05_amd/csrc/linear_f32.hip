@@ -1,0 +1,131 @@
+// linear_f32.hip -- the float32 products of the layer operators, the joining
+// of split contractions, and the activation's gradient.
+#include "gemm.h"
+
+namespace muon {
+
+hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, bool direct, int tile, hipStream_t s) {
+  if (!direct) return launch_tile<float, 128, 128, 2, 2, 2, false, 1>(g, ta, tb, s);
+  if (tile == kTileRows32) return launch_tile<float, 32, 128, 1, 4, 4, true, 1>(g, ta, tb, s);
+  return launch_tile<float, 128, 128, 2, 2, 2, true, 1>(g, ta, tb, s);
+}
+
+int gemm_tile_m(int tile) { return tile == kTile256 ? 256 : tile == kTileRows32 ? 32 : 128; }
+int gemm_tile_n(int tile) { return tile == kTile256 ? 256 : 128; }
+
+hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, bool direct, int tile, hipStream_t s) {
+  return dtype == MUON_BF16 ? launch_gemm_bf16(g, ta, tb, direct, tile, s)
+                            : launch_gemm_f32(g, ta, tb, direct, tile, s);
+}
+
+hipError_t launch_gemm_join(const GemmArgs& g, int dtype, hipStream_t s) {
+  const int64_t blocks = ((g.n + 7) / 8 * g.m + 255) / 256;
+  if (blocks <= 0) return hipSuccess;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (dtype == MUON_BF16) hipLaunchKernelGGL((k_gemm_join<uint16_t>), dim3((unsigned)blocks), dim3(256), 0, s, g);
+  else hipLaunchKernelGGL((k_gemm_join<float>), dim3((unsigned)blocks), dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+
+namespace {
+
+// dz = dy act'(z) for one block of kActGradRows rows of one group and 512
+// columns, and that block's column sums, in float32 before any rounding.
+// Each lane holds 8 columns and each of the 4 waves every fourth row; the waves'
+// sums meet in LDS in wave order.  Bound by memory: it reads dy and z and
+// writes dz once.
+template <typename T>
+__global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int cols = (int)((a.n + 511) / 512);
+  const int blk = blockIdx.x / cols, cb = blockIdx.x - blk * cols;
+  int e = 0, lo = 0, hi = 0;
+  if (a.offsets) {
+    if (!find_group<kActGradRows>(a.offsets, a.groups, a.rows, blk, e, lo, hi)) return;
+    hi = min(hi, lo + kActGradRows);
+  } else {
+    lo = blk * kActGradRows;
+    hi = (int)min((int64_t)lo + kActGradRows, a.rows);
+  }
+  const int64_t col = (int64_t)cb * 512 + lane * 8;
+  const int n = (int)min((int64_t)8, a.n - col);
+  const bool vec = a.vec != 0;
+  float sum[8] = {};
+  // Rows past the last group: their gradient is zero.
+  const bool dead = a.offsets && e == a.groups;
+  if (n > 0) {
+    for (int r = lo + wave; r < hi; r += 4) {
+      float v[8], z[8];
+      load8(static_cast<const T*>(a.dy) + (int64_t)r * a.lddy + col, n, vec, v);
+      if (a.z) {
+        load8(static_cast<const T*>(a.z) + (int64_t)r * a.ldz + col, n, vec, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], a.act);
+      }
+      if (dead) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      }
+      if (a.dz) store8(static_cast<T*>(a.dz) + (int64_t)r * a.lddz + col, n, vec, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    }
+  }
+  if (!a.db || dead) return;  // uniform over the workgroup
+  __shared__ float part[4][512];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[wave][lane * 8 + i] = sum[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 512; c += 256) {
+    const int64_t cc = (int64_t)cb * 512 + c;
+    if (cc < a.n) a.part[(int64_t)blk * a.n + cc] = (part[0][c] + part[1][c]) + (part[2][c] + part[3][c]);
+  }
+}
+
+// db: the blocks' sums of each group, in block order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_col_join(ActGradArgs a, int blocks) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int e = blockIdx.y;
+  if (c >= a.n) return;
+  int b0 = 0, b1 = blocks;
+  if (a.offsets) {
+    for (int i = 0; i <= e; ++i) {
+      int lo, hi;
+      group_range(a.offsets, a.groups, a.rows, i, lo, hi);
+      const int k = (hi - lo + kActGradRows - 1) / kActGradRows;
+      if (i < e) b0 += k;
+      else b1 = min(b0 + k, blocks);
+    }
+  }
+  float s = 0.f;
+  for (int b = b0; b < b1; ++b) s += a.part[(int64_t)b * a.n + c];
+  store_from_f32(a.db, (int64_t)e * a.n + c, sizeof(T) == 2, s);
+}
+
+}  // namespace
+
+int64_t act_grad_blocks(int64_t rows, int32_t groups, bool grouped) {
+  return group_blocks(rows, groups, grouped, kActGradRows);
+}
+
+hipError_t launch_act_grad(const ActGradArgs& a, int dtype, hipStream_t s) {
+  const int64_t blocks = act_grad_blocks(a.rows, a.groups, a.offsets != nullptr);
+  const int64_t cols = (a.n + 511) / 512;
+  if (cols <= 0) return hipSuccess;
+  if (blocks * cols > 0x7fffffff || a.groups > 65535) return hipErrorInvalidValue;
+  if (blocks > 0) {
+    const dim3 grid((unsigned)(cols * blocks));
+    if (dtype == MUON_BF16) hipLaunchKernelGGL((k_act_grad<uint16_t>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_act_grad<float>), grid, dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!a.db) return hipSuccess;
+  const dim3 grid((unsigned)((a.n + 255) / 256), (unsigned)a.groups);
+  if (dtype == MUON_BF16) hipLaunchKernelGGL((k_col_join<uint16_t>), grid, dim3(256), 0, s, a, (int)blocks);
+  else hipLaunchKernelGGL((k_col_join<float>), grid, dim3(256), 0, s, a, (int)blocks);
+  return hipGetLastError();
+}
+
+}  // namespace muon

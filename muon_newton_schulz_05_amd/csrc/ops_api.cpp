@@ -1,0 +1,438 @@
+// ops_api.cpp -- the C ABI of the layer operators (include/muon_ops.h): argument
+// checks, the choice of tile and split, and the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/muon_ops.h"
+#include "error.h"
+#include "ops.h"
+
+namespace {
+
+using muon::set_error;
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int kCus = 256;
+
+int bad(const char* what) { return set_error(MUON_ERR_INVALID_ARGUMENT, "%s", what); }
+int hip_result(hipError_t e, const char* what) {
+  if (e == hipSuccess) return set_error(MUON_OK, "%s", "");
+  return set_error(MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int elem(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+
+int check_desc(const muon_linear_desc_t* d) {
+  if (!d) return bad("desc is null");
+  if (d->dtype != MUON_F32 && d->dtype != MUON_BF16) return bad("dtype must be MUON_F32 or MUON_BF16");
+  if (d->act < MUON_ACT_NONE || d->act > MUON_ACT_GELU_TANH) return bad("unknown activation");
+  if (d->groups < 0 || d->groups > 65535) return bad("groups outside [0, 65535]");
+  if (d->w_layout != 0 && d->w_layout != 1) return bad("w_layout must be 0 or 1");
+  if (d->rows < 0 || d->k < 0 || d->n < 0 || d->rows > kMaxDim || d->k > kMaxDim || d->n > kMaxDim)
+    return bad("a size is negative or over 2^31 - 1");
+  if (d->ldx < 0 || d->ldw < 0 || d->w_stride < 0 || d->ldr < 0 || d->ldg < 0) return bad("a stride is negative");
+  return MUON_OK;
+}
+
+// An operand of a product: may it be loaded by aligned 16-byte pieces with
+// 32-bit offsets inside a tile?  rows contiguous along k: whole pieces along k;
+// contiguous along its rows (t): whole pieces along them.
+bool direct(const void* p, int64_t ld, int64_t group_stride, bool t, int64_t rows, int64_t k, int tile_rows, int es) {
+  const int64_t piece = 16 / es;
+  if (!aligned(p, 16) || ld % piece != 0 || group_stride % piece != 0) return false;
+  if ((t ? rows : k) % piece != 0) return false;
+  return ld * es * (t ? 128 / es : tile_rows) < (int64_t(1) << 31) - 4096;
+}
+
+struct Product {
+  muon::GemmArgs g{};
+  int tile = muon::kTile128;
+  bool direct = false;
+  uint64_t ws = 0;
+};
+
+// The tile and the split of a product.  Grouped products are not split: their
+// tiles already number at least the experts with rows.
+void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int groups) {
+  muon::GemmArgs& g = p->g;
+  const bool gk = ta && tb, grouped = groups > 0;
+  auto tiles = [&](int t) {
+    const int64_t bm = muon::gemm_tile_m(t), bn = muon::gemm_tile_n(t);
+    const int64_t tm = gk ? (g.m + bm - 1) / bm : muon::group_blocks(g.m, groups, grouped, bm);
+    return tm * ((g.n + bn - 1) / bn) * (gk && grouped ? groups : 1);
+  };
+  p->direct = aligned_ops;
+  p->tile = muon::kTile128;
+  if (aligned_ops) {
+    const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
+    if (m_each <= 32) p->tile = muon::kTileRows32;
+    else if (dtype == MUON_BF16 && tiles(muon::kTile256) >= kCus && m_each >= 256 && g.n >= 256) p->tile = muon::kTile256;
+  }
+  const int64_t bm = muon::gemm_tile_m(p->tile), bn = muon::gemm_tile_n(p->tile);
+  g.tiles_m = (int32_t)(gk ? (g.m + bm - 1) / bm : muon::group_blocks(g.m, groups, grouped, bm));
+  g.tiles_n = (int32_t)((g.n + bn - 1) / bn);
+  g.groups = grouped ? groups : 1;
+  g.splits = 1;
+  g.k_per = g.k;
+  const int64_t t = tiles(p->tile);
+  if (!grouped && t > 0 && t < kCus && g.k >= 1024) {
+    // Splits of at least 512 of the contraction, until the card is full.
+    int64_t s = std::min<int64_t>((2 * kCus + t - 1) / t, g.k / 512);
+    s = std::min<int64_t>(s, 64);
+    if (s > 1) {
+      g.k_per = ((g.k + s - 1) / s + 63) / 64 * 64;
+      g.splits = (int32_t)((g.k + g.k_per - 1) / g.k_per);
+      p->ws = (uint64_t)g.splits * g.m * g.n * 4;
+    }
+  }
+}
+
+int run_product(Product* p, int dtype, bool ta, bool tb, void* ws, uint64_t ws_bytes, void* stream, const char* what) {
+  muon::GemmArgs& g = p->g;
+  if (g.m == 0 || g.n == 0) return set_error(MUON_OK, "%s", "");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (g.splits > 1) {
+    if (ws_bytes < p->ws || !ws) return bad("the workspace is smaller than muon_linear_workspace says");
+    if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
+    g.part = static_cast<float*>(ws);
+  }
+  hipError_t e = muon::launch_gemm(g, dtype, ta, tb, p->direct, p->tile, s);
+  if (e == hipSuccess && g.splits > 1) e = muon::launch_gemm_join(g, dtype, s);
+  return hip_result(e, what);
+}
+
+// The three products of a layer as C = A B^T; `ops_aligned` decides the loads.
+Product forward_product(const muon_linear_desc_t* d, const void* x, const void* w, bool* tb) {
+  Product p;
+  p.g.a = x;
+  p.g.b = w;
+  p.g.lda = d->ldx;
+  p.g.ldb = d->ldw;
+  p.g.sb = d->groups > 0 ? d->w_stride : 0;
+  p.g.m = d->rows;
+  p.g.n = d->n;
+  p.g.k = d->k;
+  *tb = d->w_layout == 0;
+  const int es = elem(d->dtype);
+  const bool ok = direct(x, d->ldx, 0, false, d->rows, d->k, 256, es) &&
+                  direct(w, d->ldw, p.g.sb, *tb, d->n, d->k, 256, es);
+  plan_product(&p, d->dtype, false, *tb, ok, d->groups);
+  return p;
+}
+Product input_product(const muon_linear_desc_t* d, const void* dz, const void* w, bool* tb) {
+  Product p;
+  p.g.a = dz;
+  p.g.b = w;
+  p.g.lda = d->ldg;
+  p.g.ldb = d->ldw;
+  p.g.sb = d->groups > 0 ? d->w_stride : 0;
+  p.g.m = d->rows;
+  p.g.n = d->k;
+  p.g.k = d->n;
+  *tb = d->w_layout == 1;
+  const int es = elem(d->dtype);
+  const bool ok = direct(dz, d->ldg, 0, false, d->rows, d->n, 256, es) &&
+                  direct(w, d->ldw, p.g.sb, *tb, d->k, d->n, 256, es);
+  plan_product(&p, d->dtype, false, *tb, ok, d->groups);
+  return p;
+}
+Product weight_product(const muon_linear_desc_t* d, const void* x, const void* dz) {
+  Product p;
+  const bool t = d->w_layout == 1;  // dW^T = dz^T x
+  p.g.a = t ? dz : x;
+  p.g.b = t ? x : dz;
+  p.g.lda = t ? d->ldg : d->ldx;
+  p.g.ldb = t ? d->ldx : d->ldg;
+  p.g.m = t ? d->n : d->k;
+  p.g.n = t ? d->k : d->n;
+  p.g.k = d->rows;
+  p.g.sc = p.g.m * p.g.n;
+  const int es = elem(d->dtype);
+  const bool ok = direct(p.g.a, p.g.lda, 0, true, p.g.m, p.g.k, 256, es) &&
+                  direct(p.g.b, p.g.ldb, 0, true, p.g.n, p.g.k, 256, es);
+  plan_product(&p, d->dtype, true, true, ok, d->groups);
+  return p;
+}
+
+// Outputs of eight columns as 16-byte pieces.
+bool vec_rows(int64_t n, const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && n % 8 == 0 && ld % 8 == 0); }
+
+int check_offsets(const muon_linear_desc_t* d, const int32_t* offsets) {
+  if (d->groups > 0 && !offsets) return bad("offsets is null");
+  if (d->groups == 0 && offsets) return bad("offsets given, but groups is 0");
+  if (!aligned(offsets, 4)) return bad("offsets is not 4-byte aligned");
+  return MUON_OK;
+}
+int check_ptr(const muon_linear_desc_t* d, const void* p, int64_t count, const char* name) {
+  if (count > 0 && !p) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is null", name);
+  if (!aligned(p, elem(d->dtype))) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", name);
+  return MUON_OK;
+}
+#define MUON_TRY(x)                   \
+  do {                                \
+    const int rc_ = (x);              \
+    if (rc_ != MUON_OK) return rc_;   \
+  } while (0)
+
+int check_move(const muon_move_desc_t* d) {
+  if (!d) return bad("desc is null");
+  if (d->dtype != MUON_F32 && d->dtype != MUON_BF16) return bad("dtype must be MUON_F32 or MUON_BF16");
+  if (d->top < 1 || d->tokens < 0 || d->h < 0 || d->h > kMaxDim) return bad("top, tokens or h out of range");
+  if (d->tokens > kMaxDim / d->top) return bad("tokens * top is over 2^31 - 1");
+  if (d->experts < 1 || d->experts > MUON_ROUTE_MAX_EXPERTS) return bad("experts outside [1, 1024]");
+  if (d->ldx < 0 || d->ldg < 0 || d->ldr < 0) return bad("a stride is negative");
+  return MUON_OK;
+}
+int check_rows(const muon_move_desc_t* d, const void* p, const char* name) {
+  if (d->tokens > 0 && d->h > 0 && !p) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is null", name);
+  if (!aligned(p, elem(d->dtype))) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", name);
+  return MUON_OK;
+}
+int check_ints(const muon_move_desc_t* d, const void* p, const char* name) {
+  if (d->tokens > 0 && !p) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is null", name);
+  if (!aligned(p, 4)) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is not 4-byte aligned", name);
+  return MUON_OK;
+}
+muon::MoveArgs move_args(const muon_move_desc_t* d) {
+  muon::MoveArgs a{};
+  a.experts = d->experts;
+  a.top = d->top;
+  a.tokens = d->tokens;
+  a.h = d->h;
+  a.ldx = d->ldx;
+  a.ldg = d->ldg;
+  a.ldr = d->ldr;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_linear_workspace(const muon_linear_desc_t* d, int32_t op, uint64_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  *bytes = 0;
+  MUON_TRY(check_desc(d));
+  if (op == MUON_LINEAR_GRAD_ACT) {
+    *bytes = (uint64_t)muon::act_grad_blocks(d->rows, d->groups, d->groups > 0) * d->n * 4;
+    return set_error(MUON_OK, "%s", "");
+  }
+  if (op < 0 || op > MUON_LINEAR_GRAD_WEIGHT) return bad("unknown operation");
+  // The plan depends on the pointers' alignment: the larger of both answers.
+  const void* probes[2] = {nullptr, reinterpret_cast<const void*>(uintptr_t(8))};
+  for (const void* q : probes) {
+    bool tb;
+    const Product p = op == MUON_LINEAR_FORWARD      ? forward_product(d, q, q, &tb)
+                      : op == MUON_LINEAR_GRAD_INPUT ? input_product(d, q, q, &tb)
+                                                     : weight_product(d, q, q);
+    *bytes = std::max(*bytes, p.ws);
+  }
+  return set_error(MUON_OK, "%s", "");
+}
+
+int muon_linear_forward(const muon_linear_desc_t* d, const int32_t* offsets, const void* x, const void* w,
+                        const void* bias, const void* residual, void* y, void* z, void* ws, uint64_t ws_bytes,
+                        void* stream) {
+  MUON_TRY(check_desc(d));
+  MUON_TRY(check_offsets(d, offsets));
+  MUON_TRY(check_ptr(d, x, d->rows * d->k, "x"));
+  MUON_TRY(check_ptr(d, w, d->k * d->n, "w"));
+  MUON_TRY(check_ptr(d, bias, 0, "bias"));
+  MUON_TRY(check_ptr(d, residual, 0, "residual"));
+  MUON_TRY(check_ptr(d, y, d->rows * d->n, "y"));
+  MUON_TRY(check_ptr(d, z, 0, "z"));
+  if (d->groups > 0 && residual) return bad("a grouped layer takes no residual");
+  bool tb;
+  Product p = forward_product(d, x, w, &tb);
+  p.g.offsets = offsets;
+  p.g.c = y;
+  p.g.z = z;
+  p.g.bias = bias;
+  p.g.res = residual;
+  p.g.ldc = d->n;
+  p.g.ldr = d->ldr;
+  p.g.sbias = d->n;
+  p.g.act = d->act;
+  p.g.vec = vec_rows(d->n, y, d->n) && vec_rows(d->n, z, d->n) && vec_rows(d->n, bias, d->n) &&
+            vec_rows(d->n, residual, d->ldr);
+  return run_product(&p, d->dtype, false, tb, ws, ws_bytes, stream, "muon_linear_forward");
+}
+
+int muon_linear_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const void* dy, const void* z, void* dz,
+                         void* db, void* ws, uint64_t ws_bytes, void* stream) {
+  MUON_TRY(check_desc(d));
+  MUON_TRY(check_offsets(d, offsets));
+  MUON_TRY(check_ptr(d, dy, d->rows * d->n, "dy"));
+  MUON_TRY(check_ptr(d, z, d->act != MUON_ACT_NONE ? d->rows * d->n : 0, "z"));
+  MUON_TRY(check_ptr(d, dz, 0, "dz"));
+  MUON_TRY(check_ptr(d, db, 0, "db"));
+  if (!dz && !db) return set_error(MUON_OK, "%s", "");
+  muon::ActGradArgs a{};
+  a.dy = dy;
+  a.z = d->act != MUON_ACT_NONE ? z : nullptr;
+  a.dz = dz;
+  a.db = db;
+  a.rows = d->rows;
+  a.n = d->n;
+  a.lddy = d->ldg;
+  a.ldz = d->n;
+  a.lddz = d->n;
+  a.offsets = offsets;
+  a.groups = std::max(d->groups, 1);
+  a.act = d->act;
+  a.vec = vec_rows(d->n, dy, d->ldg) && vec_rows(d->n, a.z, d->n) && vec_rows(d->n, dz, d->n);
+  if (db) {
+    const uint64_t need = (uint64_t)muon::act_grad_blocks(d->rows, a.groups, offsets != nullptr) * d->n * 4;
+    if (need > ws_bytes || (need && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
+    if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
+    a.part = static_cast<float*>(ws);
+  }
+  return hip_result(muon::launch_act_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_linear_grad_act");
+}
+
+int muon_linear_grad_input(const muon_linear_desc_t* d, const int32_t* offsets, const void* dz, const void* w, void* dx,
+                           void* ws, uint64_t ws_bytes, void* stream) {
+  MUON_TRY(check_desc(d));
+  MUON_TRY(check_offsets(d, offsets));
+  MUON_TRY(check_ptr(d, dz, d->rows * d->n, "dz"));
+  MUON_TRY(check_ptr(d, w, d->k * d->n, "w"));
+  MUON_TRY(check_ptr(d, dx, d->rows * d->k, "dx"));
+  bool tb;
+  Product p = input_product(d, dz, w, &tb);
+  p.g.offsets = offsets;
+  p.g.c = dx;
+  p.g.ldc = d->k;
+  p.g.vec = vec_rows(d->k, dx, d->k);
+  return run_product(&p, d->dtype, false, tb, ws, ws_bytes, stream, "muon_linear_grad_input");
+}
+
+int muon_linear_grad_weight(const muon_linear_desc_t* d, const int32_t* offsets, const void* x, const void* dz, void* dw,
+                            void* ws, uint64_t ws_bytes, void* stream) {
+  MUON_TRY(check_desc(d));
+  MUON_TRY(check_offsets(d, offsets));
+  MUON_TRY(check_ptr(d, x, d->rows * d->k, "x"));
+  MUON_TRY(check_ptr(d, dz, d->rows * d->n, "dz"));
+  MUON_TRY(check_ptr(d, dw, d->k * d->n, "dw"));
+  Product p = weight_product(d, x, dz);
+  p.g.offsets = offsets;
+  p.g.c = dw;
+  p.g.ldc = p.g.n;
+  p.g.vec = vec_rows(p.g.n, dw, p.g.n) && p.g.sc % 8 == 0;
+  return run_product(&p, d->dtype, true, true, ws, ws_bytes, stream, "muon_linear_grad_weight");
+}
+
+int muon_route_workspace(int64_t entries, int32_t experts, uint64_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  *bytes = 0;
+  if (entries < 0 || entries > kMaxDim) return bad("entries out of range");
+  if (experts < 1 || experts > MUON_ROUTE_MAX_EXPERTS) return bad("experts outside [1, 1024]");
+  *bytes = (uint64_t)((entries + muon::kRouteBlock - 1) / muon::kRouteBlock) * experts * 4;
+  return set_error(MUON_OK, "%s", "");
+}
+
+int muon_route(const void* ids, int32_t ids_bytes, int64_t tokens, int32_t top, int32_t experts, int32_t* offsets,
+               int32_t* order, int32_t* position, void* ws, uint64_t ws_bytes, void* stream) {
+  if (ids_bytes != 4 && ids_bytes != 8) return bad("ids_bytes must be 4 or 8");
+  if (tokens < 0 || top < 1 || tokens > kMaxDim / top) return bad("tokens or top out of range");
+  const int64_t entries = tokens * top;
+  uint64_t need = 0;
+  MUON_TRY(muon_route_workspace(entries, experts, &need));
+  if (!offsets) return bad("offsets is null");
+  if (entries > 0 && (!ids || !order || !position)) return bad("ids, order or position is null");
+  if (!aligned(ids, ids_bytes) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(position, 4))
+    return bad("a pointer is not aligned to its elements");
+  if (need > ws_bytes || (need && !ws)) return bad("the workspace is smaller than muon_route_workspace says");
+  if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
+  muon::RouteArgs a{ids, ids_bytes == 8, experts, top, entries, order, position, offsets, static_cast<int32_t*>(ws)};
+  return hip_result(muon::launch_route(a, static_cast<hipStream_t>(stream)), "muon_route");
+}
+
+int muon_dispatch(const muon_move_desc_t* d, const int32_t* offsets, const int32_t* position, const void* x, void* xs,
+                  void* stream) {
+  MUON_TRY(check_move(d));
+  MUON_TRY(check_ints(d, offsets, "offsets"));
+  MUON_TRY(check_ints(d, position, "position"));
+  MUON_TRY(check_rows(d, x, "x"));
+  MUON_TRY(check_rows(d, xs, "xs"));
+  muon::MoveArgs a = move_args(d);
+  a.offsets = offsets;
+  a.position = position;
+  a.x = x;
+  a.out = xs;
+  a.vec = vec_rows(d->h, x, d->ldx) && vec_rows(d->h, xs, d->h);
+  return hip_result(muon::launch_dispatch(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_dispatch");
+}
+
+int muon_dispatch_grad(const muon_move_desc_t* d, const int32_t* position, const void* dxs, void* dx, void* stream) {
+  MUON_TRY(check_move(d));
+  MUON_TRY(check_ints(d, position, "position"));
+  MUON_TRY(check_rows(d, dxs, "dxs"));
+  MUON_TRY(check_rows(d, dx, "dx"));
+  muon::MoveArgs a = move_args(d);
+  a.position = position;
+  a.x = dxs;
+  a.out = dx;
+  a.vec = vec_rows(d->h, dxs, d->ldx) && vec_rows(d->h, dx, d->h);
+  return hip_result(muon::launch_gather_sum(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_dispatch_grad");
+}
+
+int muon_combine(const muon_move_desc_t* d, const int32_t* position, const float* weights, const void* ys,
+                 const void* residual, void* y, void* stream) {
+  MUON_TRY(check_move(d));
+  MUON_TRY(check_ints(d, position, "position"));
+  MUON_TRY(check_ints(d, weights, "weights"));
+  MUON_TRY(check_rows(d, ys, "ys"));
+  MUON_TRY(check_rows(d, y, "y"));
+  if (!aligned(residual, elem(d->dtype))) return bad("residual is not aligned to its elements");
+  muon::MoveArgs a = move_args(d);
+  a.position = position;
+  a.w = weights;
+  a.x = ys;
+  a.res = residual;
+  a.out = y;
+  a.vec = vec_rows(d->h, ys, d->ldx) && vec_rows(d->h, residual, d->ldr) && vec_rows(d->h, y, d->h);
+  return hip_result(muon::launch_gather_sum(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_combine");
+}
+
+int muon_combine_grad(const muon_move_desc_t* d, const int32_t* offsets, const int32_t* position, const float* weights,
+                      const void* ys, const void* dy, void* dys, float* dweights, void* stream) {
+  MUON_TRY(check_move(d));
+  MUON_TRY(check_ints(d, offsets, "offsets"));
+  MUON_TRY(check_ints(d, position, "position"));
+  MUON_TRY(check_ints(d, weights, "weights"));
+  MUON_TRY(check_rows(d, dy, "dy"));
+  if (dweights) MUON_TRY(check_rows(d, ys, "ys"));
+  if (!aligned(dys, elem(d->dtype)) || !aligned(dweights, 4)) return bad("a pointer is not aligned to its elements");
+  if (!dys && !dweights) return set_error(MUON_OK, "%s", "");
+  muon::MoveArgs a = move_args(d);
+  a.offsets = offsets;
+  a.position = position;
+  a.w = weights;
+  a.x = dweights ? ys : nullptr;
+  a.g = dy;
+  a.out = dys;
+  a.dw = dweights;
+  a.vec = vec_rows(d->h, a.x, d->ldx) && vec_rows(d->h, dy, d->ldg) && vec_rows(d->h, dys, d->h);
+  return hip_result(muon::launch_combine_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_combine_grad");
+}
+
+int muon_dropout(int32_t dtype, int64_t n, const void* x, const void* residual, void* y, double p, uint64_t seed,
+                 uint64_t offset, const uint64_t* state, void* stream) {
+  if (dtype != MUON_F32 && dtype != MUON_BF16) return bad("dtype must be MUON_F32 or MUON_BF16");
+  if (n < 0 || n > (int64_t(1) << 40)) return bad("n out of range");
+  if (!(p >= 0.0 && p < 1.0)) return bad("p outside [0, 1)");
+  const uint32_t drop = (uint32_t)std::nearbyint(p * 65536.0);
+  if (drop >= 65536u) return bad("p rounds to 1 (of 65536 steps)");
+  if (n > 0 && (!x || !y)) return bad("x or y is null");
+  const uintptr_t es = (uintptr_t)elem(dtype);
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(y, es) || !aligned(state, 8))
+    return bad("a pointer is not aligned to its elements");
+  muon::DropoutArgs a{x, residual, y, n, seed, offset, state, drop, 0};
+  a.vec = aligned(x, 16) && aligned(residual, 16) && aligned(y, 16);
+  return hip_result(muon::launch_dropout(a, dtype, static_cast<hipStream_t>(stream)), "muon_dropout");
+}
+
+}  // extern "C"

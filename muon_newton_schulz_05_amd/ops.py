@@ -1,0 +1,592 @@
+"""Layer operators on torch tensors: the forward and backward passes whose gradients a ``MuonPlan`` steps on.
+
+Everything runs in the HIP kernels behind the C ABI of ``include/muon_ops.h``;
+this module checks arguments, allocates outputs and workspaces from torch's
+caching allocator on the current stream, and ties the calls to autograd.
+
+* ``linear``: act(x W + b) + residual, and ``expert_linear``, the same over rows
+  grouped by expert with a weight [E, K, N];
+* ``route``, ``dispatch``, ``combine``: entries sorted by expert, rows moved there
+  and back with weights;
+* ``dropout``: from a counter-based generator, the mask never stored.
+
+Tensors are float32 or bfloat16, on one GPU, on the current torch stream.  Rows
+may be strided; a tensor whose last dimension is not contiguous is copied
+first.  The ``*_forward`` and ``*_backward`` functions are the same passes without
+autograd, for code that captures them into a HIP graph.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import NamedTuple
+
+import torch
+
+from .binding import MUON_BF16, MUON_F32, MUON_OK, MuonError, load_library, muon_last_error
+
+MUON_ROUTE_MAX_EXPERTS = 1024
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+EXPORTED_OPS = ("muon_linear_workspace", "muon_linear_forward", "muon_linear_grad_act", "muon_linear_grad_input",
+                "muon_linear_grad_weight", "muon_route_workspace", "muon_route", "muon_dispatch",
+                "muon_dispatch_grad", "muon_combine", "muon_combine_grad", "muon_dropout")
+
+_FORWARD, _GRAD_ACT, _GRAD_INPUT, _GRAD_WEIGHT = range(4)
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("w_layout", ctypes.c_int32), ("rows", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldg", ctypes.c_int64)]
+
+
+class MoveDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("experts", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("tokens", ctypes.c_int64), ("h", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldg", ctypes.c_int64), ("ldr", ctypes.c_int64)]
+
+
+_ops = None
+
+
+def load_ops():
+    """libmuon.so with the signatures of include/muon_ops.h; raises if it is not built."""
+    global _ops
+    if _ops is not None:
+        return _ops
+    lib = load_library()
+    P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
+    D, M, UP = ctypes.POINTER(LinearDesc), ctypes.POINTER(MoveDesc), ctypes.POINTER(U64)
+    sig = {
+        "muon_linear_workspace": [D, I32, UP],
+        "muon_linear_forward": [D, P, P, P, P, P, P, P, P, U64, P],
+        "muon_linear_grad_act": [D, P, P, P, P, P, P, U64, P],
+        "muon_linear_grad_input": [D, P, P, P, P, P, U64, P],
+        "muon_linear_grad_weight": [D, P, P, P, P, P, U64, P],
+        "muon_route_workspace": [I64, I32, UP],
+        "muon_route": [P, I32, I64, I32, I32, P, P, P, P, U64, P],
+        "muon_dispatch": [M, P, P, P, P, P],
+        "muon_dispatch_grad": [M, P, P, P, P],
+        "muon_combine": [M, P, P, P, P, P, P],
+        "muon_combine_grad": [M, P, P, P, P, P, P, P, P],
+        "muon_dropout": [I32, I64, P, P, P, ctypes.c_double, U64, U64, P, P],
+    }
+    for name, args in sig.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = ctypes.c_int
+    _ops = lib
+    return lib
+
+
+def _check(rc, where):
+    if rc != MUON_OK:
+        raise MuonError(rc, where, muon_last_error())
+
+
+# ------------------------------------------------------------------ helpers
+
+
+def _dtype(t, what):
+    if t.dtype is torch.bfloat16:
+        return MUON_BF16
+    if t.dtype is torch.float32:
+        return MUON_F32
+    raise TypeError(f"{what} is {t.dtype}: float32 or bfloat16 is supported")
+
+
+def _same(x, **others):
+    for name, t in others.items():
+        if t is None:
+            continue
+        if t.dtype is not x.dtype:
+            raise TypeError(f"{name} is {t.dtype}, x is {x.dtype}")
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, x is on {x.device}")
+
+
+def _gpu(t, what):
+    if t.device.type != "cuda":
+        raise ValueError(f"{what} must live on a GPU")
+
+
+def _rows(t):
+    """t with contiguous rows (last dimension of stride 1, no negative strides)."""
+    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor with contiguous rows."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """The device of a tensor made current, and its current stream."""
+
+    def __init__(self, t):
+        self.dev = t.device
+
+    def __enter__(self):
+        self.guard = None
+        if self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation {name!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+# ------------------------------------------------------------------ linear layers
+
+
+class _Weight:
+    """A weight [.., K, N] with either of its last two dimensions contiguous."""
+
+    def __init__(self, w):
+        k, n = w.shape[-2:]
+        if w.stride(-1) == 1 and (k <= 1 or w.stride(-2) >= n):
+            self.t, self.layout = w, 0
+        elif w.stride(-2) == 1 and (n <= 1 or w.stride(-1) >= k):
+            self.t, self.layout = w, 1
+        else:
+            self.t, self.layout = w.contiguous(), 0
+        w = self.t
+        self.ld = (w.stride(-2) if k > 1 else max(n, 1)) if self.layout == 0 else (w.stride(-1) if n > 1 else max(k, 1))
+        self.step = w.stride(0) if w.dim() == 3 else 0
+
+
+def _desc(x, w, act, groups):
+    k, n = w.t.shape[-2:]
+    return LinearDesc(_dtype(x, "x"), act, groups, w.layout, x.shape[0], k, n, _ld(x), w.ld, w.step, n, n)
+
+
+def _workspace(lib, d, op, x):
+    need = ctypes.c_uint64(0)
+    _check(lib.muon_linear_workspace(ctypes.byref(d), op, ctypes.byref(need)), "muon_linear_workspace")
+    if need.value == 0:
+        return None, 0
+    return torch.empty(need.value, dtype=torch.uint8, device=x.device), need.value
+
+
+def _check_linear(x, weight, bias, residual, offsets):
+    grouped = offsets is not None
+    _gpu(x, "x")
+    _dtype(x, "x")
+    if weight.dim() != (3 if grouped else 2):
+        raise ValueError(f"weight has {weight.dim()} dimensions, expected {3 if grouped else 2}")
+    if x.dim() < 1 or (grouped and x.dim() != 2):
+        raise ValueError("x must be [rows, K]" if grouped else "x must have at least one dimension")
+    k, n = weight.shape[-2:]
+    if x.shape[-1] != k:
+        raise ValueError(f"x has {x.shape[-1]} columns, the weight takes {k}")
+    _same(x, weight=weight, bias=bias, residual=residual)
+    want = (weight.shape[0], n) if grouped else (n,)
+    if bias is not None and tuple(bias.shape) != want:
+        raise ValueError(f"bias has shape {tuple(bias.shape)}, expected {want}")
+    if residual is not None and tuple(residual.shape) != (*x.shape[:-1], n):
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {(*x.shape[:-1], n)}")
+    if grouped:
+        e = weight.shape[0]
+        if not 1 <= e <= 65535:
+            raise ValueError(f"{e} experts: 1 to 65535 are supported")
+        if offsets.dtype is not torch.int32 or tuple(offsets.shape) != (e + 1,) or not offsets.is_contiguous():
+            raise ValueError(f"offsets must be a contiguous int32 tensor of {e + 1} values")
+        if offsets.device != x.device:
+            raise ValueError(f"offsets is on {offsets.device}, x is on {x.device}")
+
+
+def _forward(x, w, bias, residual, offsets, act, keep_z):
+    """y and, where asked and the activation has a slope, z; x and residual 2-D with contiguous rows."""
+    lib = load_ops()
+    d = _desc(x, w, act, 0 if offsets is None else w.t.shape[0])
+    y = torch.empty((d.rows, d.n), dtype=x.dtype, device=x.device)
+    z = torch.empty_like(y) if keep_z and act else None
+    if residual is not None:
+        d.ldr = _ld(residual)
+    with _On(x) as stream:
+        ws, size = _workspace(lib, d, _FORWARD, x)
+        _check(lib.muon_linear_forward(ctypes.byref(d), _ptr(offsets), x.data_ptr(), w.t.data_ptr(), _ptr(bias),
+                                       _ptr(residual), y.data_ptr(), _ptr(z), _ptr(ws), size, stream),
+               "muon_linear_forward")
+    return y, z
+
+
+def _backward(dy, x, w, z, offsets, act, need_x, need_w, need_b):
+    lib = load_ops()
+    groups = 0 if offsets is None else w.t.shape[0]
+    d = _desc(x, w, act, groups)
+    d.ldg = _ld(dy)
+    dz = dy
+    dx = dw = db = None
+    with _On(x) as stream:
+        if need_b or act:
+            store = act != 0 and (need_x or need_w)
+            if store:
+                dz = torch.empty((d.rows, d.n), dtype=x.dtype, device=x.device)
+            if need_b:
+                db = torch.empty((max(groups, 1), d.n), dtype=x.dtype, device=x.device)
+                ws, size = _workspace(lib, d, _GRAD_ACT, x)
+            else:
+                ws, size = None, 0
+            if store or need_b:
+                _check(lib.muon_linear_grad_act(ctypes.byref(d), _ptr(offsets), dy.data_ptr(), _ptr(z),
+                                                dz.data_ptr() if store else None, _ptr(db), _ptr(ws), size, stream),
+                       "muon_linear_grad_act")
+            if store:
+                d.ldg = d.n
+            if db is not None and groups == 0:
+                db = db[0]
+        if need_x:
+            dx = torch.empty((d.rows, d.k), dtype=x.dtype, device=x.device)
+            ws, size = _workspace(lib, d, _GRAD_INPUT, x)
+            _check(lib.muon_linear_grad_input(ctypes.byref(d), _ptr(offsets), dz.data_ptr(), w.t.data_ptr(),
+                                              dx.data_ptr(), _ptr(ws), size, stream), "muon_linear_grad_input")
+        if need_w:
+            lead = () if groups == 0 else (groups,)
+            shape = (*lead, d.k, d.n) if w.layout == 0 else (*lead, d.n, d.k)
+            dw = torch.empty(shape, dtype=x.dtype, device=x.device)
+            ws, size = _workspace(lib, d, _GRAD_WEIGHT, x)
+            _check(lib.muon_linear_grad_weight(ctypes.byref(d), _ptr(offsets), x.data_ptr(), dz.data_ptr(),
+                                               dw.data_ptr(), _ptr(ws), size, stream), "muon_linear_grad_weight")
+            if w.layout == 1:
+                dw = dw.transpose(-1, -2)
+    return dx, dw, db
+
+
+def _flat(t, cols):
+    if t is None:
+        return None
+    return _rows(t if t.dim() == 2 else t.reshape(math.prod(t.shape[:-1]), cols))
+
+
+def linear_forward(x, weight, bias=None, activation="none", residual=None, offsets=None, keep_z=False):
+    """``linear`` (or, with ``offsets``, ``expert_linear``) without autograd.
+
+    Returns (y, z); z, the value ahead of the activation, is None unless
+    ``keep_z`` and the activation is not "none"."""
+    act = _activation(activation)
+    _check_linear(x, weight, bias, residual, offsets)
+    k, n = weight.shape[-2:]
+    y, z = _forward(_flat(x, k), _Weight(weight), None if bias is None else bias.contiguous(), _flat(residual, n),
+                    offsets, act, keep_z)
+    return y.view(*x.shape[:-1], n), z
+
+
+def linear_backward(dy, x, weight, z=None, activation="none", offsets=None, needs=(True, True, True)):
+    """(dx, dW, db) of ``linear_forward`` for the gradient dy; needs: which of them are computed.
+
+    z is what ``linear_forward(..., keep_z=True)`` returned (not used by "none").  The residual's gradient is dy."""
+    act = _activation(activation)
+    _check_linear(x, weight, None, dy, offsets)
+    if act and (z is None or z.dtype is not x.dtype or not z.is_contiguous() or z.numel() != dy.numel()):
+        raise ValueError("z must be the tensor that linear_forward(..., keep_z=True) returned")
+    k, n = weight.shape[-2:]
+    dx, dw, db = _backward(_flat(dy, n), _flat(x, k), _Weight(weight), z, offsets, act, *needs)
+    return None if dx is None else dx.view(x.shape), dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, offsets, act):
+        k, n = weight.shape[-2:]
+        x2 = _flat(x, k)
+        w = _Weight(weight)
+        y, z = _forward(x2, w, None if bias is None else bias.contiguous(), _flat(residual, n), offsets, act, True)
+        ctx.save_for_backward(x2, w.t, z, offsets)
+        ctx.act, ctx.x_shape = act, x.shape
+        return y.view(*x.shape[:-1], n)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, wt, z, offsets = ctx.saved_tensors
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        dx = dw = db = None
+        if need_x or need_w or need_b:
+            dx, dw, db = _backward(_flat(dy, wt.shape[-1]), x, _Weight(wt), z, offsets, ctx.act, need_x, need_w,
+                                   need_b)
+            if dx is not None:
+                dx = dx.view(ctx.x_shape)
+        return dx, dw, db, dy if need_r else None, None, None
+
+
+def _tracked(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def linear(x, weight, bias=None, *, activation="none", residual=None):
+    """act(x W + b) + residual.
+
+    x [..., K], weight [K, N] (or the transposed view of a [N, K] tensor, read
+    in place), bias [N], residual [..., N].  activation: "none", "relu", "silu",
+    "gelu" or "gelu_tanh".  Differentiable in every tensor (once); for
+    the gradient, z = x W + b is kept in x's type."""
+    if not _tracked(x, weight, bias, residual):
+        return linear_forward(x, weight, bias, activation, residual)[0]
+    _check_linear(x, weight, bias, residual, None)
+    return _Linear.apply(x, weight, bias, residual, None, _activation(activation))
+
+
+def expert_linear(x, weight, offsets, bias=None, *, activation="none"):
+    """act(x_p W[e] + b[e]) for the rows p = offsets[e] .. offsets[e + 1] of every expert e.
+
+    x [rows, K], weight [E, K, N] (its last two dimensions in either order in
+    memory), offsets [E + 1] int32 on the GPU as ``route`` gives them, bias
+    [E, N].  Rows past offsets[E] give zero and get a zero gradient.  The weight's
+    gradient [E, K, N] is zero for an expert without rows."""
+    if not _tracked(x, weight, bias):
+        return linear_forward(x, weight, bias, activation, None, offsets)[0]
+    _check_linear(x, weight, bias, None, offsets)
+    return _Linear.apply(x, weight, bias, None, offsets, _activation(activation))
+
+
+# ------------------------------------------------------------------ experts: there and back
+
+
+class Routing(NamedTuple):
+    """Entries (token, choice) sorted by expert.
+
+    offsets [E + 1]: first sorted row of each expert, and the number routed;
+    order [tokens * top]: flat entry of each sorted row, -1 past the routed ones;
+    position [tokens, top]: sorted row of each entry, -1 where it is not routed.
+    All int32 on the GPU."""
+    offsets: torch.Tensor
+    order: torch.Tensor
+    position: torch.Tensor
+
+
+def route(expert_ids, n_experts):
+    """Sorts the entries of expert_ids [tokens, top] (int64 or int32) by expert, stably.
+
+    An id outside [0, n_experts) (-1, say) is not routed."""
+    _gpu(expert_ids, "expert_ids")
+    if expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
+        raise ValueError("expert_ids must be [tokens, top] with top >= 1")
+    if expert_ids.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"expert_ids is {expert_ids.dtype}: int64 or int32 is supported")
+    lib = load_ops()
+    ids = expert_ids.contiguous()
+    tokens, top = ids.shape
+    need = ctypes.c_uint64(0)
+    _check(lib.muon_route_workspace(tokens * top, n_experts, ctypes.byref(need)), "muon_route_workspace")
+    # One allocation holds the three results and the workspace, each 16-byte aligned.
+    e4, p4 = (n_experts + 1 + 3) // 4 * 4, (tokens * top + 3) // 4 * 4
+    buf = torch.empty(e4 + 2 * p4 + need.value // 4, dtype=torch.int32, device=ids.device)
+    at, end = buf.data_ptr(), tokens * top
+    with _On(ids) as stream:
+        _check(lib.muon_route(ids.data_ptr(), ids.element_size(), tokens, top, n_experts, at, at + 4 * e4,
+                              at + 4 * (e4 + p4), at + 4 * (e4 + 2 * p4), need.value, stream), "muon_route")
+    return Routing(buf[:n_experts + 1], buf[e4:e4 + end], buf[e4 + p4:e4 + p4 + end].view(tokens, top))
+
+
+def _move(routing, rows, h, dtype):
+    tokens, top = routing.position.shape
+    return MoveDesc(dtype, routing.offsets.shape[0] - 1, top, 0, tokens, h, h, h, h)
+
+
+def _check_routing(routing, t, rows, what):
+    _gpu(t, what)
+    _dtype(t, what)
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions")
+    if t.device != routing.position.device:
+        raise ValueError(f"{what} is on {t.device}, the routing is on {routing.position.device}")
+    if t.shape[0] != rows:
+        raise ValueError(f"{what} has {t.shape[0]} rows, expected {rows}")
+    p, o = routing.position, routing.offsets
+    if p.dim() != 2 or p.dtype is not torch.int32 or o.dtype is not torch.int32 or not p.is_contiguous() \
+            or not o.is_contiguous() or o.dim() != 1 or o.shape[0] < 2:
+        raise ValueError("routing must be what route() returned")
+
+
+def dispatch_forward(x, routing):
+    """``dispatch`` without autograd."""
+    tokens, top = routing.position.shape
+    _check_routing(routing, x, tokens, "x")
+    x = _rows(x)
+    d = _move(routing, tokens, x.shape[1], _dtype(x, "x"))
+    d.ldx = _ld(x)
+    xs = torch.empty((tokens * top, x.shape[1]), dtype=x.dtype, device=x.device)
+    with _On(x) as stream:
+        _check(load_ops().muon_dispatch(ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(),
+                                        x.data_ptr(), xs.data_ptr(), stream), "muon_dispatch")
+    return xs
+
+
+def dispatch_backward(dxs, routing):
+    """dx of ``dispatch``: each token's sum over its rows of dxs."""
+    tokens, top = routing.position.shape
+    _check_routing(routing, dxs, tokens * top, "dxs")
+    dxs = _rows(dxs)
+    d = _move(routing, tokens, dxs.shape[1], _dtype(dxs, "dxs"))
+    d.ldx = _ld(dxs)
+    dx = torch.empty((tokens, dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
+    with _On(dxs) as stream:
+        _check(load_ops().muon_dispatch_grad(ctypes.byref(d), routing.position.data_ptr(), dxs.data_ptr(),
+                                             dx.data_ptr(), stream), "muon_dispatch_grad")
+    return dx
+
+
+def _check_weights(routing, weights):
+    if weights.dtype is not torch.float32 or tuple(weights.shape) != tuple(routing.position.shape):
+        raise ValueError(f"weights must be float32 of shape {tuple(routing.position.shape)}")
+    if weights.device != routing.position.device:
+        raise ValueError(f"weights is on {weights.device}, the routing is on {routing.position.device}")
+
+
+def combine_forward(ys, routing, weights, residual=None):
+    """``combine`` without autograd (weights float32)."""
+    tokens, top = routing.position.shape
+    _check_routing(routing, ys, tokens * top, "ys")
+    _check_weights(routing, weights)
+    _same(ys, residual=residual)
+    h = ys.shape[1]
+    if residual is not None and tuple(residual.shape) != (tokens, h):
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {(tokens, h)}")
+    ys, w = _rows(ys), weights.contiguous()
+    residual = None if residual is None else _rows(residual)
+    d = _move(routing, tokens, h, _dtype(ys, "ys"))
+    d.ldx = _ld(ys)
+    if residual is not None:
+        d.ldr = _ld(residual)
+    y = torch.empty((tokens, h), dtype=ys.dtype, device=ys.device)
+    with _On(ys) as stream:
+        _check(load_ops().muon_combine(ctypes.byref(d), routing.position.data_ptr(), w.data_ptr(), ys.data_ptr(),
+                                       _ptr(residual), y.data_ptr(), stream), "muon_combine")
+    return y
+
+
+def combine_backward(dy, ys, routing, weights, needs=(True, True)):
+    """(dys, dweights) of ``combine``; needs: which of them are computed."""
+    tokens, top = routing.position.shape
+    _check_routing(routing, dy, tokens, "dy")
+    _check_routing(routing, ys, tokens * top, "ys")
+    _check_weights(routing, weights)
+    _same(ys, dy=dy)
+    if dy.shape[1] != ys.shape[1]:
+        raise ValueError(f"dy has {dy.shape[1]} columns, ys has {ys.shape[1]}")
+    dy, ys, w = _rows(dy), _rows(ys), weights.contiguous()
+    d = _move(routing, tokens, ys.shape[1], _dtype(ys, "ys"))
+    d.ldx, d.ldg = _ld(ys), _ld(dy)
+    dys = torch.empty((tokens * top, ys.shape[1]), dtype=ys.dtype, device=ys.device) if needs[0] else None
+    dw = torch.empty((tokens, top), dtype=torch.float32, device=ys.device) if needs[1] else None
+    with _On(ys) as stream:
+        _check(load_ops().muon_combine_grad(ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(),
+                                            w.data_ptr(), ys.data_ptr(), dy.data_ptr(), _ptr(dys), _ptr(dw), stream),
+               "muon_combine_grad")
+    return dys, dw
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, offsets, order, position):
+        ctx.save_for_backward(offsets, order, position)
+        return dispatch_forward(x, Routing(offsets, order, position))
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dxs):
+        return dispatch_backward(dxs, Routing(*ctx.saved_tensors)), None, None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ys, weights, residual, offsets, order, position):
+        ctx.save_for_backward(ys, weights, offsets, order, position)
+        return combine_forward(ys, Routing(offsets, order, position), weights, residual)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        ys, weights, *routing = ctx.saved_tensors
+        need_ys, need_w, need_r = ctx.needs_input_grad[:3]
+        dys = dw = None
+        if need_ys or need_w:
+            dys, dw = combine_backward(dy, ys, Routing(*routing), weights, (need_ys, need_w))
+        return dys, dw, dy if need_r else None, None, None, None
+
+
+def dispatch(x, routing):
+    """Rows of x [tokens, H] in sorted order: xs[position[t][j]] = x[t], [tokens * top, H].
+
+    Rows past the routed ones are zero.  Differentiable in x."""
+    return _Dispatch.apply(x, *routing) if _tracked(x) else dispatch_forward(x, routing)
+
+
+def combine(ys, routing, weights, residual=None):
+    """y[t] = sum_j weights[t][j] ys[position[t][j]] (+ residual[t]), [tokens, H].
+
+    Entries that were not routed add nothing.  weights [tokens, top] (bfloat16 is
+    taken as float32).  Differentiable in ys, weights and residual."""
+    if weights.dtype is torch.bfloat16:
+        weights = weights.float()
+    if not _tracked(ys, weights, residual):
+        return combine_forward(ys, routing, weights, residual)
+    return _Combine.apply(ys, weights, residual, *routing)
+
+
+# ------------------------------------------------------------------ dropout
+
+
+def dropout_forward(x, p, seed=0, offset=0, residual=None, state=None):
+    """``dropout`` without autograd.  The gradient of x is the same call on dy without a residual."""
+    _gpu(x, "x")
+    code = _dtype(x, "x")
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"p is {p}: 0 <= p < 1 is supported")
+    _same(x, residual=residual)
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
+    if state is not None and (state.dtype is not torch.int64 or state.numel() != 2 or state.device != x.device
+                              or not state.is_contiguous()):
+        raise ValueError("state must be two contiguous int64 values on x's device: seed, offset")
+    x = x.contiguous()
+    residual = None if residual is None else residual.contiguous()
+    y = torch.empty_like(x)
+    with _On(x) as stream:
+        _check(load_ops().muon_dropout(code, x.numel(), x.data_ptr(), _ptr(residual), y.data_ptr(), p,
+                                       seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, _ptr(state), stream),
+               "muon_dropout")
+    return y
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset, state):
+        # A copy: the mask of the gradient is this pass's, whatever the caller writes into state later.
+        ctx.state = None if state is None else state.clone()
+        ctx.p, ctx.seed, ctx.offset = p, seed, offset
+        return dropout_forward(x, p, seed, offset, residual, ctx.state)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        dx = dropout_forward(dy, ctx.p, ctx.seed, ctx.offset, None, ctx.state) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None, None
+
+
+def dropout(x, p, *, seed=0, offset=0, residual=None, state=None):
+    """x with each element zeroed with probability p and the others scaled by 1 / (1 - p), plus residual.
+
+    p is taken to the nearest of 65536 steps.  The mask follows from (seed,
+    offset) and an element's flat index alone: calls that must differ get another
+    seed or offset.  state: an int64 tensor [seed, offset] on the GPU used in
+    their place, which a captured graph reads at every replay.  Differentiable
+    in x and residual."""
+    if not _tracked(x, residual):
+        return dropout_forward(x, p, seed, offset, residual, state)
+    return _Dropout.apply(x, residual, p, seed, offset, state)
