@@ -4,14 +4,15 @@
 // activation and residual in the epilogue.
 //
 // A workgroup owns a BM x BN tile of C; each of its waves owns a block of
-// 32 x 32 matrix-core products.  Operand k-slices of 128 bytes a row (64
-// bf16 or 32 float32 values) go from memory straight into LDS, NS stages
+// 32 x 32 matrix-core products.  Operand k-slices of KB = 64 or 128 bytes
+// a row go from memory straight into LDS, NS stages
 // deep, with one barrier a slice.  What is out of range (rows past the
 // group, the contraction's tail) is given an offset past the buffer
 // descriptor's end, for which the load writes zeros to LDS.
 //
-//  - An operand contiguous along k sits in LDS as rows of 128 bytes; the
-//    16-byte chunk c of row r at slot c ^ (r / 2 mod 8), so that 16 lanes
+//  - An operand contiguous along k sits in LDS as rows of KB bytes; the
+//    16-byte chunk c of row r at slot c ^ (r / 2 mod 8) (KB = 128) or
+//    c ^ (r / 4 mod 4) (64), so that 16 lanes
 //    reading one chunk of 16 rows touch 16 distinct 16-byte bank groups.
 //  - An operand contiguous along its rows sits as k-rows.  bf16: fragments
 //    are read by ds_read_b64_tr_b16, which hands lane i of 16 the column i of
@@ -39,45 +40,70 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, char
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, kRecords, 0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void LDS_PTR*)dst, 16, off, 0, 0, 0);
 }
-// Wait until at most N of this wave's loads are in flight.
+// Wait until at most N of this wave's loads are in flight and its LDS reads are
+// done.  (The builtin, not inline asm: the compiler then knows that no LDS
+// read is pending and adds no wait of its own behind it.)
 template <int N>
 __device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  static_assert(N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt N, lgkmcnt 0, expcnt untouched
+  asm volatile("" ::: "memory");
+}
+// Scheduling of one substep: VM loads to LDS and RD fragment reads spread evenly
+// over MM matrix-core products, each ahead of its product.
+template <int RD, int VM, int MM, int Q = 0>
+__device__ __forceinline__ void interleave() {
+  if constexpr (Q < MM) {
+    constexpr int vm = ((Q + 1) * VM + MM - 1) / MM - (Q * VM + MM - 1) / MM;
+    constexpr int rd = ((Q + 1) * RD + MM - 1) / MM - (Q * RD + MM - 1) / MM;
+    if constexpr (vm > 0) __builtin_amdgcn_sched_group_barrier(0x010, vm, 0);
+    if constexpr (rd > 0) __builtin_amdgcn_sched_group_barrier(0x100, rd, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    interleave<RD, VM, MM, Q + 1>();
+  }
 }
 
+// Products of 16 x 16 blocks.  Against 32 x 32 x 16 the deeper contraction moves
+// fewer accumulator registers a product (8 of 32 against 16 of 40 registers
+// read and written a 32768 flops), which the card's power limit returns as clock.
 template <typename T> struct Mma;
 template <> struct Mma<uint16_t> {
-  typedef bf16x8_t Frag;  // eight k of one row: k = 16 s + 8 (lane / 32) + 0..7
-  static __device__ __forceinline__ f32x16_t mul(Frag a, Frag b, f32x16_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  static constexpr int N = 1;
+  typedef bf16x8_t Frag;  // eight k of one row: k = 32 s + 8 (lane / 16) + 0..7
+  static __device__ __forceinline__ f32x4_t mul(Frag a, Frag b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
 };
 template <> struct Mma<float> {
-  typedef f32x4_t Frag;   // four k of one row: k = 8 s + 4 (lane / 32) + 0..3
-  static __device__ __forceinline__ f32x16_t mul(Frag a, Frag b, f32x16_t c) {
+  static constexpr int N = 4;
+  typedef f32x4_t Frag;   // four k of one row: k = 16 s + 4 (lane / 16) + 0..3
+  static __device__ __forceinline__ f32x4_t mul(Frag a, Frag b, f32x4_t c) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
     return c;
   }
 };
 
 // One operand's tile: R rows x one k-slice.
+constexpr int KB = 128;  // bytes of a k-slice's row
+
 template <typename T, int R, bool TR, int NW, bool DIRECT>
 struct Panel {
   static constexpr int EPC = 16 / sizeof(T);          // elements of a 16-byte chunk
-  static constexpr int BK = 128 / sizeof(T);          // k of a slice
-  static constexpr int RB = TR ? R * (int)sizeof(T) : 128;  // bytes of an LDS row
+  static constexpr int BK = KB / sizeof(T);           // k of a slice
+  static constexpr int RB = TR ? R * (int)sizeof(T) : KB;  // bytes of an LDS row
   static constexpr int CPR = RB / 16;                 // its chunks
-  static constexpr int BYTES = R * 128;
+  static constexpr int BYTES = R * KB;
   static constexpr int LI = BYTES / 1024 / NW;        // 1 KB loads a wave and slice
+  static constexpr int READS = !TR ? 1 : sizeof(T) == 2 ? 2 : 4;  // LDS reads of a fragment
   static_assert(BYTES % (1024 * NW) == 0, "whole loads");
   typedef typename Mma<T>::Frag Frag;
 
   static __device__ __forceinline__ int swz(int row) {
     if (!TR) return (row >> 1) & 7;
-    if (sizeof(T) == 4) return (((row >> 2) & 1) << 3) & (CPR - 1);
-    if (CPR == 8) return ((row >> 1) & 1) << 2;
-    return ((row & 3) << 2) & (CPR - 1);
+    if (sizeof(T) == 4) return (((row >> 2) & 3) << 2) & (CPR - 1);
+    const int v = (row & 3) | (((row >> 3) & 1) << 2);  // eight k-rows read at once, 32 bytes of each
+    return CPR >= 16 ? v << 1 : CPR == 8 ? (v >> 1) << 1 : (v >> 2) << 1;
   }
 
   const char* base;     // first element of this tile at k = 0 of the group
@@ -105,22 +131,21 @@ struct Panel {
       }
     }
   }
-  __device__ __forceinline__ const char* at(int kt) const { return base + (TR ? (int64_t)kt * BK * ld : (int64_t)kt * 128); }
+  __device__ __forceinline__ const char* at(int kt) const { return base + (TR ? (int64_t)kt * BK * ld : (int64_t)kt * KB); }
 
   // DIRECT: slice kt into LDS; k_left: elements of the contraction from this
-  // slice on.
+  // slice on (none left: zeros).  Branchless, so that the loads and the
+  // products around them are scheduled as one block.
   __device__ __forceinline__ void issue(int kt, int k_left, char* st, int wave, int lane) {
     const char* p = at(kt);
-    if (k_left >= BK) {
+    // A lane's first k: in an operand contiguous along k the swizzle of rows
+    // 1024 / KB NW u apart is the same, so one value serves every load.
+    static_assert(NW * (1024 / KB) % 16 == 0, "swizzle");
+    const int s0 = slot(0, wave, lane), k0 = TR ? lrow(s0) : chunk(s0) * EPC;
 #pragma unroll
-      for (int u = 0; u < LI; ++u) load_to_lds(p, off[u], st + (wave + NW * u) * 1024);
-    } else {
-#pragma unroll
-      for (int u = 0; u < LI; ++u) {
-        const int s = slot(u, wave, lane);
-        const int kk = TR ? lrow(s) : chunk(s) * EPC;
-        load_to_lds(p, kk < k_left ? off[u] : kNoLoad, st + (wave + NW * u) * 1024);
-      }
+    for (int u = 0; u < LI; ++u) {
+      const int kk = TR ? k0 + u * (NW * 64 / CPR) : k0;
+      load_to_lds(p, kk < k_left ? off[u] : kNoLoad, st + (wave + NW * u) * 1024);
     }
   }
   // Otherwise: slice kt into registers (any alignment; a chunk that is only
@@ -151,16 +176,16 @@ struct Panel {
     for (int u = 0; u < LI; ++u) *reinterpret_cast<u32x4_t*>(st + (wave + NW * u) * 1024 + lane * 16) = reg[u];
   }
 
-  // The fragment of substep s (16 bf16 or 8 float32 of k) for rows
-  // r0 .. r0 + 31 of the tile (r0 a multiple of 32).
+  // The fragment of substep s (32 bf16 or 16 float32 of k) for rows
+  // r0 .. r0 + 15 of the tile (r0 a multiple of 16).
   static __device__ __forceinline__ Frag frag(const char* st, int r0, int s, int lane) {
+    const int g = lane >> 4, i = lane & 15;
     if constexpr (!TR) {
-      const int r = r0 + (lane & 31);
-      return *reinterpret_cast<const Frag*>(st + r * 128 + (((2 * s + (lane >> 5)) ^ swz(r)) << 4));
+      const int r = r0 + i;
+      return *reinterpret_cast<const Frag*>(st + r * KB + (((4 * s + g) ^ swz(r)) << 4));
     } else if constexpr (sizeof(T) == 2) {
-      const int g = lane >> 4, i = lane & 15;
-      const int k = 16 * s + 8 * (g >> 1) + (i >> 2);
-      const int c = (r0 >> 3) + 2 * (g & 1) + ((i & 3) >> 1);
+      const int k = 32 * s + 8 * g + (i >> 2);
+      const int c = (r0 >> 3) + ((i & 3) >> 1);
       const char* p = st + k * RB + ((c ^ swz(k)) << 4) + (i & 1) * 8;
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4_t LDS_PTR*)p);
       const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4_t LDS_PTR*)(p + 4 * RB));
@@ -168,12 +193,12 @@ struct Panel {
       const s16x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       return __builtin_bit_cast(Frag, v);
     } else {
-      const int c = (r0 + (lane & 31)) >> 2;
+      const int c = (r0 + i) >> 2;
       Frag v;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = 8 * s + 4 * (lane >> 5) + j;
-        v[j] = *reinterpret_cast<const float*>(st + k * RB + ((c ^ swz(k)) << 4) + (lane & 3) * 4);
+        const int k = 16 * s + 4 * g + j;
+        v[j] = *reinterpret_cast<const float*>(st + k * RB + ((c ^ swz(k)) << 4) + (i & 3) * 4);
       }
       return v;
     }
@@ -218,12 +243,12 @@ __device__ __forceinline__ void stripe(int t, int tiles_m, int tiles_n, int& tm,
 
 template <typename T, int BM, int BN, int WGM, int WGN, int NS, bool TA, bool TB, bool DIRECT, int MINB>
 __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
-  constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 32, FN = WN / 32;
+  constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
   typedef Panel<T, BM, TA, NW, DIRECT> PA;
   typedef Panel<T, BN, TB, NW, DIRECT> PB;
   typedef typename Mma<T>::Frag Frag;
-  constexpr int BK = PA::BK, STAGE = PA::BYTES + PB::BYTES;
-  constexpr int STRIDE = WN * 4 + 32;  // bytes of a staged epilogue row: rows r and r + 4 fall on opposite bank halves
+  constexpr int BK = PA::BK, SUB = KB / 64, STAGE = PA::BYTES + PB::BYTES;
+  constexpr int STRIDE = WN * 4 + 16;  // bytes of a staged epilogue row: rows 4 apart fall on distinct bank quarters
   constexpr int LDS = NS * STAGE > NW * 32 * STRIDE ? NS * STAGE : NW * 32 * STRIDE;
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
 
@@ -276,58 +301,69 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
     pb.init(reinterpret_cast<const char*>(B), g.ldb * (int64_t)sizeof(T), rows_b, wave, lane);
   }
 
-  f32x16_t acc[FM][FN];
+  f32x4_t acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x16_t{};
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{};
 
-  auto multiply = [&](const char* st) __attribute__((always_inline)) {
+  // Fragments of two substeps: one being read while the other is multiplied.
+  Frag af[2][FM] = {}, bf[2][FN] = {};
+  auto read = [&](const char* st, int s) __attribute__((always_inline)) {
+    af[s & 1][0] = PA::frag(st, wm * WM, s, lane);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      Frag af[FM], bf[FN];
+    for (int j = 0; j < FN; ++j) bf[s & 1][j] = PB::frag(st + PA::BYTES, wn * WN + 16 * j, s, lane);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) af[i] = PA::frag(st, wm * WM + 32 * i, s, lane);
+    for (int i = 1; i < FM; ++i) af[s & 1][i] = PA::frag(st, wm * WM + 16 * i, s, lane);
+  };
+  auto multiply = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) bf[j] = PB::frag(st + PA::BYTES, wn * WN + 32 * j, s, lane);
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(af[i], bf[j], acc[i][j]);
-    }
+      for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(af[s & 1][i], bf[s & 1][j], acc[i][j]);
   };
 
   if constexpr (DIRECT) {
     constexpr int L = PA::LI + PB::LI;
     auto issue = [&](int kt, char* fill) __attribute__((always_inline)) {
-      const int k_left = (int)min((int64_t)BK, kk - (int64_t)kt * BK);
+      const int k_left = (int)max((int64_t)0, min((int64_t)BK, kk - (int64_t)kt * BK));
       pa.issue(kt, k_left, fill, wave, lane);
       pb.issue(kt, k_left, fill + PA::BYTES, wave, lane);
     };
+    if (nk > 0) {
 #pragma unroll
-    for (int p = 0; p < NS - 1; ++p)
-      if (p < nk) issue(p, lds + p * STAGE);
+      for (int p = 0; p < NS - 1; ++p) issue(p, lds + p * STAGE);
+    }
     int stage = 0;
     for (int kt = 0; kt < nk; ++kt) {
-      // Slices kt + 1 .. kt + NS - 2 may stay in flight; the barrier then says
-      // that slice kt is whole and that slice kt - 1 has been read by all.
-      static_assert(NS <= 4 && 2 * L < 64, "waits");
-      const int fly = min(NS - 2, nk - 1 - kt);
-      if (fly <= 0) wait_loads<0>();
-      else if (fly == 1) wait_loads<L>();
-      else wait_loads<2 * L>();
+      // Slices kt + 1 .. kt + NS - 2 stay in flight; the barrier then says that
+      // slice kt is whole and that slice kt - 1 has been read by all.
+      static_assert((NS - 2) * L < 64, "waits");
+      wait_loads<(NS - 2) * L>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       // The stage being filled and the one being read are never the same:
       // __restrict says so, or the compiler would wait for the loads in
       // flight ahead of every transposing read.
       auto step = [&](char* __restrict fill, const char* __restrict st) __attribute__((always_inline)) {
-        if (kt + NS - 1 < nk) issue(kt + NS - 1, fill);
-        multiply(st);
+        issue(kt + NS - 1, fill);
+        // A slice's last substep is multiplied behind the next barrier, so the
+        // matrix cores have work while the first fragments are read.  (Ahead of
+        // the first slice these are products of zeros.)
+        constexpr int RD = PA::READS * FM + PB::READS * FN, MM = FM * FN * Mma<T>::N;
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+          read(st, s);
+          multiply(s + 1);  // of the other parity: substep s - 1
+          if (s == 0) interleave<RD, L, MM>();
+          else interleave<RD, 0, MM>();
+        }
       };
       step(lds + (stage == 0 ? NS - 1 : stage - 1) * STAGE, lds + stage * STAGE);
       stage = stage == NS - 1 ? 0 : stage + 1;
     }
+    if (nk > 0) multiply(SUB - 1);
+    wait_loads<0>();
   } else {
     auto fetch = [&](int kt) {
       const int k_left = (int)min((int64_t)BK, kk - (int64_t)kt * BK);
@@ -341,14 +377,18 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
       pb.put(st + PA::BYTES, wave, lane);
       if (kt + 1 < nk) fetch(kt + 1);
       __syncthreads();
-      multiply(st);
+#pragma unroll
+      for (int s = 0; s < SUB; ++s) {
+        read(st, s);
+        multiply(s);
+      }
     }
   }
   __syncthreads();  // every wave is done with the operand stages
 
   // ---- epilogue: 32 rows at a time through this wave's own staging, so that
-  // a row of C leaves as whole 16-byte pieces.  Register 4 q + u of a block is
-  // row 8 q + 4 (lane / 32) + u, column lane mod 32.
+  // a row of C leaves as whole 16-byte pieces.  Register u of a block is row
+  // 4 (lane / 16) + u, column lane mod 16.
   constexpr int LPR = WN / 8, RPP = 64 / LPR;
   char* stg = lds + wave * 32 * STRIDE;
   const int col = tn * BN + wn * WN + 8 * (lane % LPR);
@@ -358,14 +398,16 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
     load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n, g.vec != 0, bias);
   const int64_t crow0 = GK ? (int64_t)tm * BM : row0;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  for (int i = 0; i < WM / 32; ++i) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int lr = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        *reinterpret_cast<float*>(stg + lr * STRIDE + (32 * j + (lane & 31)) * 4) = acc[i][j][r];
-      }
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int lr = 16 * ii + 4 * (lane >> 4) + u;
+          *reinterpret_cast<float*>(stg + lr * STRIDE + (16 * j + (lane & 15)) * 4) = acc[2 * i + ii][j][u];
+        }
     wave_fence();
 #pragma unroll
     for (int p = 0; p < 32 / RPP; ++p) {
