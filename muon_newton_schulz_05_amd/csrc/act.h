@@ -8,13 +8,31 @@ namespace muon {
 // act(z) in float32.  Each is z times a factor in [0, 1]; the tanh form of
 // gelu uses (1 + tanh u) / 2 = sigmoid(2 u), which keeps its relative
 // accuracy where tanh u nears -1.  NaN stays NaN.
-__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + __expf(-v)); }
+__device__ __forceinline__ float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 constexpr float kGeluC = 0.7978845608028654f, kGeluA = 0.044715f;  // sqrt(2 / pi); the cubic term
+
+// The normal distribution function by Abramowitz and Stegun 7.1.26
+// (erfc(x) = t (a1 + .. + a5 t^4) e^-x^2 with t = 1 / (1 + p x), within 1.5e-7),
+// x = |z| / sqrt 2; e = e^(-z^2 / 2), which the slope needs as well.  A
+// library erf took 2.5 times as long, all of it exposed behind the products.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.7071067811865476f, 1.f));
+  e = __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.4426950408889634f));
+  float p = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  p = fmaf(t, p, 0.5f * 1.421413741f);
+  p = fmaf(t, p, 0.5f * -0.284496736f);
+  p = fmaf(t, p, 0.5f * 0.254829592f);
+  const float q = t * p * e;
+  return z < 0.f ? q : 1.f - q;
+}
 __device__ __forceinline__ float act_f(float z, int act) {
   switch (act) {
     case MUON_ACT_RELU: return z <= 0.f ? 0.f : z;
     case MUON_ACT_SILU: return z * sigmoid_f(z);
-    case MUON_ACT_GELU: return z * (0.5f + 0.5f * erff(z * 0.7071067811865476f));
+    case MUON_ACT_GELU: {
+      float e;
+      return z * normal_cdf(z, e);
+    }
     case MUON_ACT_GELU_TANH: return z * sigmoid_f(2.f * kGeluC * (z + kGeluA * z * z * z));
     default: return z;
   }
@@ -26,8 +44,11 @@ __device__ __forceinline__ float act_slope(float z, int act) {
       const float q = sigmoid_f(z);
       return q + z * q * (1.f - q);
     }
-    case MUON_ACT_GELU:
-      return 0.5f + 0.5f * erff(z * 0.7071067811865476f) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    case MUON_ACT_GELU: {
+      float e;
+      const float c = normal_cdf(z, e);
+      return fmaf(z * 0.3989422804014327f, e, c);
+    }
     case MUON_ACT_GELU_TANH: {
       const float q = sigmoid_f(2.f * kGeluC * (z + kGeluA * z * z * z));
       return q + z * q * (1.f - q) * 2.f * kGeluC * (1.f + 3.f * kGeluA * z * z);
@@ -57,9 +78,8 @@ __device__ __forceinline__ void group_range(const int32_t* offsets, int groups, 
 // BM: each lane counts its share of the groups' blocks, a wave-wide prefix
 // sum finds the lane whose share holds mt.  Results are uniform over the
 // wave.  False: there are fewer blocks.
-template <int BM>
-__device__ __forceinline__ bool find_group(const int32_t* offsets, int groups, int64_t rows, int mt, int& e, int& row0,
-                                           int& end) {
+__device__ __forceinline__ bool find_group(const int32_t* offsets, int groups, int64_t rows, int BM, int mt, int& e,
+                                           int& row0, int& end) {
   const int lane = threadIdx.x & 63;
   const int per = (groups + 64) / 64;  // groups + 1 ranges over 64 lanes
   const int e0 = lane * per, e1 = min(e0 + per, groups + 1);
@@ -100,45 +120,42 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int groups, i
   return true;
 }
 
-// Eight consecutive elements as float32 (vec: 16-byte pieces; otherwise one
-// by one, n of them inside the row, the others zero).
+// Eight consecutive elements as float32, n of them inside the row (the others
+// are zero).  Whole groups move as 16-byte accesses at any alignment of
+// their elements, which the hardware splits where it has to.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    if (vec) {
-      const u32x4_t w = *reinterpret_cast<const MUON_GLOBAL u32x4_t*>(as_global(p));
+__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      u32x4_t w;
+      __builtin_memcpy(&w, as_global(p), 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = bf16_lo(w[i]);
         v[2 * i + 1] = bf16_hi(w[i]);
       }
-      return;
-    }
-  } else {
-    if (vec) {
-      const MUON_GLOBAL f32x4_t* q = reinterpret_cast<const MUON_GLOBAL f32x4_t*>(as_global(p));
-      const f32x4_t a = q[0], b = q[1];
+    } else {
+      f32x4_t w[2];
+      __builtin_memcpy(&w[0], as_global(p), 16);
+      __builtin_memcpy(&w[1], as_global(p + 4), 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
-      }
-      return;
+      for (int i = 0; i < 8; ++i) v[i] = w[i >> 2][i & 3];
     }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = i < n ? x_to_f32(p[i]) : 0.f;
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&v)[8]) {
-  if (vec) {
+__device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<MUON_GLOBAL u32x4_t*>(as_global(p)) =
-          u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      const u32x4_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      __builtin_memcpy(as_global(p), &w, 16);
     } else {
-      MUON_GLOBAL f32x4_t* q = reinterpret_cast<MUON_GLOBAL f32x4_t*>(as_global(p));
-      q[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-      q[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+      const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+      __builtin_memcpy(as_global(p), &a, 16);
+      __builtin_memcpy(as_global(p + 4), &b, 16);
     }
     return;
   }

@@ -33,11 +33,10 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a) {
   const int64_t blk = (int64_t)blockIdx.x * 256 + threadIdx.x, i0 = blk * 8;
   if (i0 >= a.n) return;
   const int n = (int)min((int64_t)8, a.n - i0);
-  const bool vec = a.vec != 0 && n == 8;
   const uint64_t seed = a.state ? a.state[0] : a.seed, offset = a.state ? a.state[1] : a.offset;
   float v[8], r[8] = {};
-  load8(static_cast<const T*>(a.x) + i0, n, vec, v);
-  if (a.res) load8(static_cast<const T*>(a.res) + i0, n, vec, r);
+  load8(static_cast<const T*>(a.x) + i0, n, v);
+  if (a.res) load8(static_cast<const T*>(a.res) + i0, n, r);
   const u32x4_t w = philox((uint64_t)blk, offset, seed);
   const float scale = 65536.f / (float)(65536u - a.drop);
 #pragma unroll
@@ -46,7 +45,7 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a) {
     // A dropped element is zero whatever it held, infinities and NaN too.
     v[i] = (u >= a.drop ? v[i] * scale : 0.f) + r[i];
   }
-  store8(static_cast<T*>(a.y) + i0, n, vec, v);
+  store8(static_cast<T*>(a.y) + i0, n, v);
 }
 
 }  // namespace

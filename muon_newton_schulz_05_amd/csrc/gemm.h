@@ -20,6 +20,8 @@
 //    64-byte block are kept in distinct banks by chunk ^ 4 (k mod 4).
 //    float32: 32 lanes read 32 consecutive values, no transposition.
 #pragma once
+#include <type_traits>
+
 #include "act.h"
 #include "device_common.h"
 #include "ops.h"
@@ -49,17 +51,18 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt N, lgkmcnt 0, expcnt untouched
   asm volatile("" ::: "memory");
 }
-// Scheduling of one substep: VM loads to LDS and RD fragment reads spread evenly
-// over MM matrix-core products, each ahead of its product.
-template <int RD, int VM, int MM, int Q = 0>
+// Scheduling of one substep: RD fragment reads spread evenly over MM matrix-core
+// products and VM loads to LDS over the first SV of them, each ahead of its
+// product.
+template <int RD, int VM, int SV, int MM, int Q = 0>
 __device__ __forceinline__ void interleave() {
   if constexpr (Q < MM) {
-    constexpr int vm = ((Q + 1) * VM + MM - 1) / MM - (Q * VM + MM - 1) / MM;
+    constexpr int vm = Q < SV ? ((Q + 1) * VM + SV - 1) / SV - (Q * VM + SV - 1) / SV : 0;
     constexpr int rd = ((Q + 1) * RD + MM - 1) / MM - (Q * RD + MM - 1) / MM;
     if constexpr (vm > 0) __builtin_amdgcn_sched_group_barrier(0x010, vm, 0);
     if constexpr (rd > 0) __builtin_amdgcn_sched_group_barrier(0x100, rd, 0);
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    interleave<RD, VM, MM, Q + 1>();
+    interleave<RD, VM, SV, MM, Q + 1>();
   }
 }
 
@@ -209,22 +212,21 @@ struct Panel {
 template <typename T>
 __device__ __forceinline__ void finish8(const GemmArgs& g, float (&v)[8], const float (&bias)[8], int64_t e, int64_t row,
                                         int col, int n) {
-  const bool vec = g.vec != 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] += bias[i];
   const int64_t at = e * g.sc + row * g.ldc + col;
-  if (g.z) store8(static_cast<T*>(g.z) + at, n, vec, v);
+  if (g.z) store8(static_cast<T*>(g.z) + at, n, v);
   if (g.act != MUON_ACT_NONE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], g.act);
   }
   if (g.res) {
     float r[8];
-    load8(static_cast<const T*>(g.res) + row * g.ldr + col, n, vec, r);
+    load8(static_cast<const T*>(g.res) + row * g.ldr + col, n, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += r[i];
   }
-  store8(static_cast<T*>(g.c) + at, n, vec, v);
+  store8(static_cast<T*>(g.c) + at, n, v);
 }
 
 // Workgroups go to the 8 XCDs round robin: block b of n takes the place in
@@ -254,7 +256,12 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WGN, wn = wave % WGN;
+  // Waves w and w + 4 share a SIMD.  With 2 x 4 of them, each SIMD gets one wave
+  // of the tile's upper and one of its lower half, and one of its left and one of
+  // its right half, so that a tile with half of its rows or columns outside
+  // C leaves every SIMD half its work.
+  const int wm = NW == 8 && WGM == 2 ? (wave & 1) ^ (wave >> 2) : wave / WGN;
+  const int wn = NW == 8 && WGM == 2 ? (wave >> 1) & 3 : wave % WGN;
 
   // ---- which tile
   constexpr bool GK = TA && TB;  // groups divide the contraction
@@ -277,7 +284,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
       k0 = lo;
       k1 = hi;
     } else {
-      if (!find_group<BM>(g.offsets, g.groups, g.m, tm, e, lo, hi)) return;  // uniform, before any barrier
+      if (!find_group(g.offsets, g.groups, g.m, BM, tm, e, lo, hi)) return;  // uniform, before any barrier
       row0 = lo;
       end = hi;
       if (e == g.groups) k1 = 0;  // rows past the last group: zeros
@@ -307,6 +314,9 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{};
 
+  // A wave whose rows or columns all lie outside C multiplies nothing.
+  const bool idle = wm * WM >= rows_a || wn * WN >= rows_b;
+
   // Fragments of two substeps: one being read while the other is multiplied.
   Frag af[2][FM] = {}, bf[2][FN] = {};
   auto read = [&](const char* st, int s) __attribute__((always_inline)) {
@@ -334,35 +344,44 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
 #pragma unroll
       for (int p = 0; p < NS - 1; ++p) issue(p, lds + p * STAGE);
     }
-    int stage = 0;
-    for (int kt = 0; kt < nk; ++kt) {
-      // Slices kt + 1 .. kt + NS - 2 stay in flight; the barrier then says that
-      // slice kt is whole and that slice kt - 1 has been read by all.
-      static_assert((NS - 2) * L < 64, "waits");
-      wait_loads<(NS - 2) * L>();
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      // The stage being filled and the one being read are never the same:
-      // __restrict says so, or the compiler would wait for the loads in
-      // flight ahead of every transposing read.
-      auto step = [&](char* __restrict fill, const char* __restrict st) __attribute__((always_inline)) {
-        issue(kt + NS - 1, fill);
-        // A slice's last substep is multiplied behind the next barrier, so the
-        // matrix cores have work while the first fragments are read.  (Ahead of
-        // the first slice these are products of zeros.)
-        constexpr int RD = PA::READS * FM + PB::READS * FN, MM = FM * FN * Mma<T>::N;
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-          read(st, s);
-          multiply(s + 1);  // of the other parity: substep s - 1
-          if (s == 0) interleave<RD, L, MM>();
-          else interleave<RD, 0, MM>();
-        }
-      };
-      step(lds + (stage == 0 ? NS - 1 : stage - 1) * STAGE, lds + stage * STAGE);
-      stage = stage == NS - 1 ? 0 : stage + 1;
-    }
-    if (nk > 0) multiply(SUB - 1);
+    auto run = [&](auto idle_tag) __attribute__((always_inline)) {
+      constexpr bool IDLE = decltype(idle_tag)::value;
+      int stage = 0;
+      for (int kt = 0; kt < nk; ++kt) {
+        // Slices kt + 1 .. kt + NS - 2 stay in flight; the barrier then says that
+        // slice kt is whole and that slice kt - 1 has been read by all.
+        static_assert((NS - 2) * L < 64, "waits");
+        wait_loads<(NS - 2) * L>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // The stage being filled and the one being read are never the same:
+        // __restrict says so, or the compiler would wait for the loads in
+        // flight ahead of every transposing read.
+        auto step = [&](char* __restrict fill, const char* __restrict st) __attribute__((always_inline)) {
+          issue(kt + NS - 1, fill);
+          if constexpr (IDLE) return;
+          // A slice's last substep is multiplied behind the next barrier, so the
+          // matrix cores have work while the first fragments are read.  (Ahead of
+          // the first slice these are products of zeros.)
+          constexpr int RD = PA::READS * FM + PB::READS * FN, MM = FM * FN * Mma<T>::N;
+  #pragma unroll
+          for (int s = 0; s < SUB; ++s) {
+            read(st, s);
+            multiply(s + 1);  // of the other parity: substep s - 1
+            // The loads go out over the first half of the products: at 8192^3
+            // 1416 / 1419 / 1411 TFLOP/s (forward, dx, dW) against 1388 / 1392 /
+            // 1345 over all of them and 1407 / 1371 / 1406 over the first quarter.
+            if (s == 0) interleave<RD, L, MM / 2, MM>();
+            else interleave<RD, 0, 1, MM>();
+          }
+        };
+        step(lds + (stage == 0 ? NS - 1 : stage - 1) * STAGE, lds + stage * STAGE);
+        stage = stage == NS - 1 ? 0 : stage + 1;
+      }
+      if (!IDLE && nk > 0) multiply(SUB - 1);
+    };
+    if (NW == 8 && idle) run(std::true_type{});
+    else run(std::false_type{});
     wait_loads<0>();
   } else {
     auto fetch = [&](int kt) {
@@ -395,7 +414,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
   const int n = (int)min((int64_t)8, g.n - col);
   float bias[8] = {};
   if (g.bias && n > 0 && !g.part && !(!GK && e == g.groups && g.offsets))
-    load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n, g.vec != 0, bias);
+    load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n, bias);
   const int64_t crow0 = GK ? (int64_t)tm * BM : row0;
 #pragma unroll
   for (int i = 0; i < WM / 32; ++i) {
@@ -417,7 +436,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
       float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
       const int64_t row = crow0 + wm * WM + 32 * i + lr;
       if (row < end && n > 0) {
-        if (g.part) store8(g.part + ((int64_t)split * g.m + row) * g.n + col, n, g.n % 8 == 0, v);
+        if (g.part) store8(g.part + ((int64_t)split * g.m + row) * g.n + col, n, v);
         else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);
       }
     }
@@ -436,11 +455,11 @@ __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs g) {
   float v[8] = {}, bias[8] = {};
   for (int s = 0; s < g.splits; ++s) {
     float p[8];
-    load8(g.part + ((int64_t)s * g.m + row) * g.n + col, n, g.n % 8 == 0, p);
+    load8(g.part + ((int64_t)s * g.m + row) * g.n + col, n, p);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += p[k];
   }
-  if (g.bias) load8(static_cast<const T*>(g.bias) + col, n, g.vec != 0, bias);
+  if (g.bias) load8(static_cast<const T*>(g.bias) + col, n, bias);
   finish8<T>(g, v, bias, 0, row, col, n);
 }
 

@@ -5,13 +5,17 @@
 namespace muon {
 
 hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, bool direct, int tile, hipStream_t s) {
-  if (!direct) return launch_tile<float, 128, 128, 2, 2, 2, false, 1>(g, ta, tb, s);
+  if (!direct) {
+    if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 2, false, 1>(g, ta, tb, s);
+    return launch_tile<float, 128, 128, 2, 2, 2, false, 1>(g, ta, tb, s);
+  }
+  if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 2, true, 1>(g, ta, tb, s);
   if (tile == kTileRows32) return launch_tile<float, 32, 128, 1, 4, 4, true, 1>(g, ta, tb, s);
   return launch_tile<float, 128, 128, 2, 2, 2, true, 1>(g, ta, tb, s);
 }
 
-int gemm_tile_m(int tile) { return tile == kTile256 ? 256 : tile == kTileRows32 ? 32 : 128; }
-int gemm_tile_n(int tile) { return tile == kTile256 ? 256 : 128; }
+int gemm_tile_m(int tile) { return tile == kTile256 || tile == kTile256x128 ? 256 : tile == kTileRows32 ? 32 : tile == kTile64 ? 64 : 128; }
+int gemm_tile_n(int tile) { return tile == kTile256 ? 256 : tile == kTile64 ? 64 : 128; }
 
 hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, bool direct, int tile, hipStream_t s) {
   return dtype == MUON_BF16 ? launch_gemm_bf16(g, ta, tb, direct, tile, s)
@@ -29,7 +33,7 @@ hipError_t launch_gemm_join(const GemmArgs& g, int dtype, hipStream_t s) {
 
 namespace {
 
-// dz = dy act'(z) for one block of kActGradRows rows of one group and 512
+// dz = dy act'(z) for one block of a.block rows of one group and 512
 // columns, and that block's column sums, in float32 before any rounding.
 // Each lane holds 8 columns and each of the 4 waves every fourth row; the waves'
 // sums meet in LDS in wave order.  Bound by memory: it reads dy and z and
@@ -41,24 +45,23 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
   const int blk = blockIdx.x / cols, cb = blockIdx.x - blk * cols;
   int e = 0, lo = 0, hi = 0;
   if (a.offsets) {
-    if (!find_group<kActGradRows>(a.offsets, a.groups, a.rows, blk, e, lo, hi)) return;
-    hi = min(hi, lo + kActGradRows);
+    if (!find_group(a.offsets, a.groups, a.rows, a.block, blk, e, lo, hi)) return;
+    hi = min(hi, lo + a.block);
   } else {
-    lo = blk * kActGradRows;
-    hi = (int)min((int64_t)lo + kActGradRows, a.rows);
+    lo = blk * a.block;
+    hi = (int)min((int64_t)lo + a.block, a.rows);
   }
   const int64_t col = (int64_t)cb * 512 + lane * 8;
   const int n = (int)min((int64_t)8, a.n - col);
-  const bool vec = a.vec != 0;
   float sum[8] = {};
   // Rows past the last group: their gradient is zero.
   const bool dead = a.offsets && e == a.groups;
   if (n > 0) {
     for (int r = lo + wave; r < hi; r += 4) {
       float v[8], z[8];
-      load8(static_cast<const T*>(a.dy) + (int64_t)r * a.lddy + col, n, vec, v);
+      load8(static_cast<const T*>(a.dy) + (int64_t)r * a.lddy + col, n, v);
       if (a.z) {
-        load8(static_cast<const T*>(a.z) + (int64_t)r * a.ldz + col, n, vec, z);
+        load8(static_cast<const T*>(a.z) + (int64_t)r * a.ldz + col, n, z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], a.act);
       }
@@ -66,7 +69,7 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
       }
-      if (a.dz) store8(static_cast<T*>(a.dz) + (int64_t)r * a.lddz + col, n, vec, v);
+      if (a.dz) store8(static_cast<T*>(a.dz) + (int64_t)r * a.lddz + col, n, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += v[i];
     }
@@ -82,35 +85,66 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
   }
 }
 
-// db: the blocks' sums of each group, in block order.
+// db: the blocks' sums of each group.  64 columns a workgroup; its four waves
+// take every fourth block each, eight loads in flight, and meet in LDS: the
+// order of the sum is fixed.
 template <typename T>
 __global__ __launch_bounds__(256) void k_col_join(ActGradArgs a, int blocks) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   const int e = blockIdx.y;
-  if (c >= a.n) return;
   int b0 = 0, b1 = blocks;
   if (a.offsets) {
-    for (int i = 0; i <= e; ++i) {
+    // Blocks of the groups ahead of e, counted by the wave's lanes.
+    int before = 0, mine = 0;
+    for (int i = lane; i <= e; i += 64) {
       int lo, hi;
       group_range(a.offsets, a.groups, a.rows, i, lo, hi);
-      const int k = (hi - lo + kActGradRows - 1) / kActGradRows;
-      if (i < e) b0 += k;
-      else b1 = min(b0 + k, blocks);
+      const int k = (hi - lo + a.block - 1) / a.block;
+      if (i < e) before += k;
+      else mine = k;
     }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      before += __shfl_xor(before, d, 64);
+      mine += __shfl_xor(mine, d, 64);
+    }
+    b0 = min(before, blocks);
+    b1 = min(before + mine, blocks);
   }
   float s = 0.f;
-  for (int b = b0; b < b1; ++b) s += a.part[(int64_t)b * a.n + c];
-  store_from_f32(a.db, (int64_t)e * a.n + c, sizeof(T) == 2, s);
+  if (c < a.n) {
+    const float* p = a.part + c;
+    int b = b0 + wave;
+    for (; b + 28 < b1; b += 32) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = p[(int64_t)(b + 4 * u) * a.n];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+    for (; b < b1; b += 4) s += p[(int64_t)b * a.n];
+  }
+  __shared__ float part[4][64];
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < a.n)
+    store_from_f32(a.db, (int64_t)e * a.n + c, sizeof(T) == 2,
+                   (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
 }
 
 }  // namespace
 
-int64_t act_grad_blocks(int64_t rows, int32_t groups, bool grouped) {
-  return group_blocks(rows, groups, grouped, kActGradRows);
+// 64 rows a block; 16 where that would leave most of the card without one.
+int act_grad_block(int64_t rows, int64_t n) { return (rows + 63) / 64 * ((n + 511) / 512) < 1024 ? 16 : 64; }
+int64_t act_grad_blocks(int64_t rows, int64_t n, int32_t groups, bool grouped) {
+  return group_blocks(rows, groups, grouped, act_grad_block(rows, n));
 }
 
-hipError_t launch_act_grad(const ActGradArgs& a, int dtype, hipStream_t s) {
-  const int64_t blocks = act_grad_blocks(a.rows, a.groups, a.offsets != nullptr);
+hipError_t launch_act_grad(const ActGradArgs& args, int dtype, hipStream_t s) {
+  ActGradArgs a = args;
+  a.block = act_grad_block(a.rows, a.n);
+  const int64_t blocks = act_grad_blocks(a.rows, a.n, a.groups, a.offsets != nullptr);
   const int64_t cols = (a.n + 511) / 512;
   if (cols <= 0) return hipSuccess;
   if (blocks * cols > 0x7fffffff || a.groups > 65535) return hipErrorInvalidValue;
@@ -122,7 +156,7 @@ hipError_t launch_act_grad(const ActGradArgs& a, int dtype, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!a.db) return hipSuccess;
-  const dim3 grid((unsigned)((a.n + 255) / 256), (unsigned)a.groups);
+  const dim3 grid((unsigned)((a.n + 63) / 64), (unsigned)a.groups);
   if (dtype == MUON_BF16) hipLaunchKernelGGL((k_col_join<uint16_t>), grid, dim3(256), 0, s, a, (int)blocks);
   else hipLaunchKernelGGL((k_col_join<float>), grid, dim3(256), 0, s, a, (int)blocks);
   return hipGetLastError();

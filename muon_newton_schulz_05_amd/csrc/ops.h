@@ -28,7 +28,6 @@ struct GemmArgs {
   const void* res;         // null, or rows of ldr elements
   int64_t ldc, sc, ldr, sbias;
   int32_t act;
-  int32_t vec;             // C, z, res and bias take 16-byte accesses of 8 columns
   // split contraction: part != null stores float32 partials [splits][m][n]
   float* part;
   int32_t splits;
@@ -36,7 +35,7 @@ struct GemmArgs {
   int32_t tiles_m, tiles_n;
 };
 
-enum GemmTile { kTile128 = 0, kTile256, kTileRows32, kNumTiles };
+enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTileRows32, kTile64 };
 int gemm_tile_m(int tile);
 int gemm_tile_n(int tile);
 // direct: the operands may be loaded by aligned 16-byte pieces (gemm_direct).
@@ -54,10 +53,10 @@ struct ActGradArgs {
   float* part;             // column sums of one row block, [blocks][n]
   int64_t rows, n, lddy, ldz, lddz;
   const int32_t* offsets;
-  int32_t groups, act, vec;
+  int32_t groups, act;
+  int32_t block;           // rows of one block (launch_act_grad sets it)
 };
-constexpr int kActGradRows = 64;  // rows of one block
-int64_t act_grad_blocks(int64_t rows, int32_t groups, bool grouped);
+int64_t act_grad_blocks(int64_t rows, int64_t n, int32_t groups, bool grouped);
 hipError_t launch_act_grad(const ActGradArgs& a, int dtype, hipStream_t s);
 
 // Most row blocks that `rows` rows in up to `groups` groups (and the rows
@@ -90,7 +89,7 @@ struct MoveArgs {
   const float* w;          // weights [tokens][top]
   const int32_t* position;
   const int32_t* offsets;
-  int32_t experts, top, vec;
+  int32_t experts, top;
   int64_t tokens, h, ldx, ldg, ldr;
 };
 hipError_t launch_dispatch(const MoveArgs& a, int dtype, hipStream_t s);
@@ -105,7 +104,6 @@ struct DropoutArgs {
   uint64_t seed, offset;
   const uint64_t* state;   // null, or {seed, offset} on the device
   uint32_t drop;           // of 65536
-  int32_t vec;
 };
 hipError_t launch_dropout(const DropoutArgs& a, int dtype, hipStream_t s);
 

@@ -54,8 +54,23 @@ struct Product {
   uint64_t ws = 0;
 };
 
-// The tile and the split of a product.  Grouped products are not split: their
-// tiles already number at least the experts with rows.
+// The tile and the split of a product, by how many tiles there are for the
+// card's 256 compute units (times in us, bf16, forward / dx / dW):
+//  - 256 x 256 has the best rate (1400 TFLOP/s at 8192^3) once every unit has a
+//    tile: 4096^3 takes 110 / 105 / 106, with 256 x 128 120 / 120 / 131, with
+//    128 x 128 132 / 148 / 140.
+//  - 256 x 128 where only it fills the card: 2048 x 16384 x 4096 forward 224, with
+//    128 x 128 256, with 256 x 256 split four ways 248.
+//  - 128 x 128 down to half a card of tiles (2048^3: 30 / 31 / 29, with 256 x 128
+//    50), then 64 x 64.  float32 products are bound by their lower matrix rate,
+//    not by operand traffic, and take 64 x 64 until 128 x 128 fills the card four
+//    times over (1024^3: 25 against 47; 4096^3: 1017 against 987).
+//  - 32 x 128 for at most 32 rows (a group), where time goes to reading B, and for
+//    grouped products whose 64-tiles leave units idle ([24, 10240] experts over
+//    8192 rows, dx: 52, with 64 x 64 75, with 128 x 128 104).
+// A dense product whose tiles do not fill the card is split along the
+// contraction, at least 512 of it each, and joined.  Grouped products are not:
+// their tiles already number at least the groups with rows.
 void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int groups) {
   muon::GemmArgs& g = p->g;
   const bool gk = ta && tb, grouped = groups > 0;
@@ -64,12 +79,21 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int
     const int64_t tm = gk ? (g.m + bm - 1) / bm : muon::group_blocks(g.m, groups, grouped, bm);
     return tm * ((g.n + bn - 1) / bn) * (gk && grouped ? groups : 1);
   };
+  const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
+  const bool f32 = dtype == MUON_F32;
   p->direct = aligned_ops;
-  p->tile = muon::kTile128;
-  if (aligned_ops) {
-    const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
-    if (m_each <= 32) p->tile = muon::kTileRows32;
-    else if (dtype == MUON_BF16 && tiles(muon::kTile256) >= kCus && m_each >= 256 && g.n >= 256) p->tile = muon::kTile256;
+  if (!aligned_ops) {
+    p->tile = tiles(muon::kTile128) >= (f32 ? 4 : 2) * kCus ? muon::kTile128 : muon::kTile64;
+  } else if (m_each <= 32) {
+    p->tile = muon::kTileRows32;
+  } else if (!f32 && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
+    p->tile = muon::kTile256;
+  } else if (!f32 && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
+    p->tile = muon::kTile256x128;
+  } else if (tiles(muon::kTile128) >= (f32 ? 4 * kCus : kCus / 2)) {
+    p->tile = muon::kTile128;
+  } else {
+    p->tile = grouped && !gk && tiles(muon::kTile64) < kCus ? muon::kTileRows32 : muon::kTile64;
   }
   const int64_t bm = muon::gemm_tile_m(p->tile), bn = muon::gemm_tile_n(p->tile);
   g.tiles_m = (int32_t)(gk ? (g.m + bm - 1) / bm : muon::group_blocks(g.m, groups, grouped, bm));
@@ -79,7 +103,6 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int
   g.k_per = g.k;
   const int64_t t = tiles(p->tile);
   if (!grouped && t > 0 && t < kCus && g.k >= 1024) {
-    // Splits of at least 512 of the contraction, until the card is full.
     int64_t s = std::min<int64_t>((2 * kCus + t - 1) / t, g.k / 512);
     s = std::min<int64_t>(s, 64);
     if (s > 1) {
@@ -157,9 +180,6 @@ Product weight_product(const muon_linear_desc_t* d, const void* x, const void* d
   return p;
 }
 
-// Outputs of eight columns as 16-byte pieces.
-bool vec_rows(int64_t n, const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && n % 8 == 0 && ld % 8 == 0); }
-
 int check_offsets(const muon_linear_desc_t* d, const int32_t* offsets) {
   if (d->groups > 0 && !offsets) return bad("offsets is null");
   if (d->groups == 0 && offsets) return bad("offsets given, but groups is 0");
@@ -217,7 +237,7 @@ int muon_linear_workspace(const muon_linear_desc_t* d, int32_t op, uint64_t* byt
   *bytes = 0;
   MUON_TRY(check_desc(d));
   if (op == MUON_LINEAR_GRAD_ACT) {
-    *bytes = (uint64_t)muon::act_grad_blocks(d->rows, d->groups, d->groups > 0) * d->n * 4;
+    *bytes = (uint64_t)muon::act_grad_blocks(d->rows, d->n, std::max(d->groups, 1), d->groups > 0) * d->n * 4;
     return set_error(MUON_OK, "%s", "");
   }
   if (op < 0 || op > MUON_LINEAR_GRAD_WEIGHT) return bad("unknown operation");
@@ -256,8 +276,6 @@ int muon_linear_forward(const muon_linear_desc_t* d, const int32_t* offsets, con
   p.g.ldr = d->ldr;
   p.g.sbias = d->n;
   p.g.act = d->act;
-  p.g.vec = vec_rows(d->n, y, d->n) && vec_rows(d->n, z, d->n) && vec_rows(d->n, bias, d->n) &&
-            vec_rows(d->n, residual, d->ldr);
   return run_product(&p, d->dtype, false, tb, ws, ws_bytes, stream, "muon_linear_forward");
 }
 
@@ -283,9 +301,8 @@ int muon_linear_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, co
   a.offsets = offsets;
   a.groups = std::max(d->groups, 1);
   a.act = d->act;
-  a.vec = vec_rows(d->n, dy, d->ldg) && vec_rows(d->n, a.z, d->n) && vec_rows(d->n, dz, d->n);
   if (db) {
-    const uint64_t need = (uint64_t)muon::act_grad_blocks(d->rows, a.groups, offsets != nullptr) * d->n * 4;
+    const uint64_t need = (uint64_t)muon::act_grad_blocks(d->rows, d->n, a.groups, offsets != nullptr) * d->n * 4;
     if (need > ws_bytes || (need && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
     if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
     a.part = static_cast<float*>(ws);
@@ -305,7 +322,6 @@ int muon_linear_grad_input(const muon_linear_desc_t* d, const int32_t* offsets, 
   p.g.offsets = offsets;
   p.g.c = dx;
   p.g.ldc = d->k;
-  p.g.vec = vec_rows(d->k, dx, d->k);
   return run_product(&p, d->dtype, false, tb, ws, ws_bytes, stream, "muon_linear_grad_input");
 }
 
@@ -320,7 +336,6 @@ int muon_linear_grad_weight(const muon_linear_desc_t* d, const int32_t* offsets,
   p.g.offsets = offsets;
   p.g.c = dw;
   p.g.ldc = p.g.n;
-  p.g.vec = vec_rows(p.g.n, dw, p.g.n) && p.g.sc % 8 == 0;
   return run_product(&p, d->dtype, true, true, ws, ws_bytes, stream, "muon_linear_grad_weight");
 }
 
@@ -362,7 +377,6 @@ int muon_dispatch(const muon_move_desc_t* d, const int32_t* offsets, const int32
   a.position = position;
   a.x = x;
   a.out = xs;
-  a.vec = vec_rows(d->h, x, d->ldx) && vec_rows(d->h, xs, d->h);
   return hip_result(muon::launch_dispatch(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_dispatch");
 }
 
@@ -375,7 +389,6 @@ int muon_dispatch_grad(const muon_move_desc_t* d, const int32_t* position, const
   a.position = position;
   a.x = dxs;
   a.out = dx;
-  a.vec = vec_rows(d->h, dxs, d->ldx) && vec_rows(d->h, dx, d->h);
   return hip_result(muon::launch_gather_sum(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_dispatch_grad");
 }
 
@@ -393,7 +406,6 @@ int muon_combine(const muon_move_desc_t* d, const int32_t* position, const float
   a.x = ys;
   a.res = residual;
   a.out = y;
-  a.vec = vec_rows(d->h, ys, d->ldx) && vec_rows(d->h, residual, d->ldr) && vec_rows(d->h, y, d->h);
   return hip_result(muon::launch_gather_sum(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_combine");
 }
 
@@ -415,7 +427,6 @@ int muon_combine_grad(const muon_move_desc_t* d, const int32_t* offsets, const i
   a.g = dy;
   a.out = dys;
   a.dw = dweights;
-  a.vec = vec_rows(d->h, a.x, d->ldx) && vec_rows(d->h, dy, d->ldg) && vec_rows(d->h, dys, d->h);
   return hip_result(muon::launch_combine_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_combine_grad");
 }
 
@@ -430,8 +441,7 @@ int muon_dropout(int32_t dtype, int64_t n, const void* x, const void* residual, 
   const uintptr_t es = (uintptr_t)elem(dtype);
   if (!aligned(x, es) || !aligned(residual, es) || !aligned(y, es) || !aligned(state, 8))
     return bad("a pointer is not aligned to its elements");
-  muon::DropoutArgs a{x, residual, y, n, seed, offset, state, drop, 0};
-  a.vec = aligned(x, 16) && aligned(residual, 16) && aligned(y, 16);
+  const muon::DropoutArgs a{x, residual, y, n, seed, offset, state, drop};
   return hip_result(muon::launch_dropout(a, dtype, static_cast<hipStream_t>(stream)), "muon_dropout");
 }
 

@@ -224,19 +224,18 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_dispatch(MoveArgs a) {
   const Piece p = my_piece(a);
   if (!p.in) return;
-  const bool vec = a.vec != 0;
   float v[8];
-  load8(static_cast<const T*>(a.x) + p.token * a.ldx + p.col, p.n, vec, v);
+  load8(static_cast<const T*>(a.x) + p.token * a.ldx + p.col, p.n, v);
   const int all = routed_rows(a);
   T* out = static_cast<T*>(a.out);
   for (int j = 0; j < a.top; ++j) {
     const int64_t r = row_at(a, p.token, j);
-    if (r >= 0) store8(out + r * a.h + p.col, p.n, vec, v);
+    if (r >= 0) store8(out + r * a.h + p.col, p.n, v);
   }
   const float zero[8] = {};
   for (int j = 0; j < a.top; ++j) {
     const int64_t r = p.token * a.top + j;
-    if (r >= all) store8(out + r * a.h + p.col, p.n, vec, zero);
+    if (r >= all) store8(out + r * a.h + p.col, p.n, zero);
   }
 }
 
@@ -245,7 +244,6 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_gather_sum(MoveArgs a) {
   const Piece p = my_piece(a);
   if (!p.in) return;
-  const bool vec = a.vec != 0;
   float sum[8] = {};
   constexpr int U = 4;  // rows in flight
   for (int j0 = 0; j0 < a.top; j0 += U) {
@@ -258,7 +256,7 @@ __global__ __launch_bounds__(256) void k_gather_sum(MoveArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (r[u] >= 0) load8(static_cast<const T*>(a.x) + r[u] * a.ldx + p.col, p.n, vec, v[u]);
+      if (r[u] >= 0) load8(static_cast<const T*>(a.x) + r[u] * a.ldx + p.col, p.n, v[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (r[u] >= 0) {
@@ -268,11 +266,11 @@ __global__ __launch_bounds__(256) void k_gather_sum(MoveArgs a) {
   }
   if (a.res) {
     float v[8];
-    load8(static_cast<const T*>(a.res) + p.token * a.ldr + p.col, p.n, vec, v);
+    load8(static_cast<const T*>(a.res) + p.token * a.ldr + p.col, p.n, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] += v[i];
   }
-  store8(static_cast<T*>(a.out) + p.token * a.h + p.col, p.n, vec, sum);
+  store8(static_cast<T*>(a.out) + p.token * a.h + p.col, p.n, sum);
 }
 
 // One wave a token: dys[position[t][j]] = w[t][j] dy[t] and
@@ -283,7 +281,6 @@ __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (t >= a.tokens) return;
-  const bool vec = a.vec != 0;
   const int all = routed_rows(a);
   constexpr int U = 4;
   T* out = static_cast<T*>(a.out);
@@ -298,11 +295,11 @@ __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
     for (int64_t c = lane * 8; c < a.h; c += kCols) {
       const int n = (int)min((int64_t)8, a.h - c);
       float d[8], v[U][8];
-      load8(static_cast<const T*>(a.g) + t * a.ldg + c, n, vec, d);
+      load8(static_cast<const T*>(a.g) + t * a.ldg + c, n, d);
       if (a.dw) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (r[u] >= 0) load8(static_cast<const T*>(a.x) + r[u] * a.ldx + c, n, vec, v[u]);
+          if (r[u] >= 0) load8(static_cast<const T*>(a.x) + r[u] * a.ldx + c, n, v[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (r[u] >= 0) {
@@ -317,7 +314,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = w[u] * d[i];
-            store8(out + r[u] * a.h + c, n, vec, o);
+            store8(out + r[u] * a.h + c, n, o);
           }
       }
     }
@@ -334,7 +331,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
   for (int j = 0; j < a.top; ++j) {
     const int64_t r = t * a.top + j;
     if (r < all) continue;
-    for (int64_t c = lane * 8; c < a.h; c += kCols) store8(out + r * a.h + c, (int)min((int64_t)8, a.h - c), vec, zero);
+    for (int64_t c = lane * 8; c < a.h; c += kCols) store8(out + r * a.h + c, (int)min((int64_t)8, a.h - c), zero);
   }
 }
 

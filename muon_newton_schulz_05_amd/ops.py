@@ -126,22 +126,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The device of a tensor made current, and its current stream."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, t):
-        self.dev = t.device
 
-    def __enter__(self):
-        self.guard = None
-        if self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(name, t, *args):
+    """The C function on t's device and current stream."""
+    index = t.get_device()
+    f = getattr(_ops or load_ops(), name)
+    if index == torch.cuda.current_device():
+        rc = f(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, _raw_stream(index))
+    if rc != MUON_OK:
+        raise MuonError(rc, name, muon_last_error())
 
 
 def _activation(name):
@@ -153,38 +152,67 @@ def _activation(name):
 # ------------------------------------------------------------------ linear layers
 
 
-class _Weight:
-    """A weight [.., K, N] with either of its last two dimensions contiguous."""
+class _Plan:
+    """Descriptor and workspace sizes of a layer: what follows from shapes, strides and types alone."""
 
-    def __init__(self, w):
+    def __init__(self, x, w, act, grouped):
         k, n = w.shape[-2:]
+        groups = w.shape[0] if grouped else 0
         if w.stride(-1) == 1 and (k <= 1 or w.stride(-2) >= n):
-            self.t, self.layout = w, 0
-        elif w.stride(-2) == 1 and (n <= 1 or w.stride(-1) >= k):
-            self.t, self.layout = w, 1
+            layout, ld = 0, w.stride(-2) if k > 1 else max(n, 1)
         else:
-            self.t, self.layout = w.contiguous(), 0
-        w = self.t
-        self.ld = (w.stride(-2) if k > 1 else max(n, 1)) if self.layout == 0 else (w.stride(-1) if n > 1 else max(k, 1))
-        self.step = w.stride(0) if w.dim() == 3 else 0
+            layout, ld = 1, w.stride(-1) if n > 1 else max(k, 1)
+        self.rows, self.k, self.n, self.groups, self.layout = x.shape[0], k, n, groups, layout
+        self.y_shape = (self.rows, n)
+        lead = (groups,) if grouped else ()
+        self.dw_shape = (*lead, k, n) if layout == 0 else (*lead, n, k)
+        self.args = [_dtype(x, "x"), act, groups, layout, self.rows, k, n, _ld(x), ld, w.stride(0) if grouped else 0]
+        self.descs = {}
+
+    def get(self, op, ld):
+        """(descriptor, workspace bytes) of one call whose residual or gradient rows are ld apart."""
+        got = self.descs.get((op, ld))
+        if got is None:
+            d = LinearDesc(*self.args, ld, ld)
+            need = ctypes.c_uint64(0)
+            _check(load_ops().muon_linear_workspace(ctypes.byref(d), op, ctypes.byref(need)), "muon_linear_workspace")
+            got = self.descs[(op, ld)] = (ctypes.byref(d), need.value)
+        return got
 
 
-def _desc(x, w, act, groups):
-    k, n = w.t.shape[-2:]
-    return LinearDesc(_dtype(x, "x"), act, groups, w.layout, x.shape[0], k, n, _ld(x), w.ld, w.step, n, n)
+_plans = {}
 
 
-def _workspace(lib, d, op, x):
-    need = ctypes.c_uint64(0)
-    _check(lib.muon_linear_workspace(ctypes.byref(d), op, ctypes.byref(need)), "muon_linear_workspace")
-    if need.value == 0:
-        return None, 0
-    return torch.empty(need.value, dtype=torch.uint8, device=x.device), need.value
+def _layout_ok(w):
+    k, n = w.shape[-2:]
+    return (w.stride(-1) == 1 and (k <= 1 or w.stride(-2) >= n)) or (w.stride(-2) == 1 and (n <= 1 or w.stride(-1) >= k))
+
+
+def _plan(x, w, act, grouped):
+    """The plan of x [rows, K] with contiguous rows and a weight with either of its last dimensions contiguous."""
+    key = (x.shape, x.stride(), w.shape, w.stride(), x.dtype, act, grouped)
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) >= 4096:
+            _plans.clear()
+        p = _plans[key] = _Plan(x, w, act, grouped)
+    return p
+
+
+def _workspace(size, x):
+    return torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+
+
+def _flat(t, cols):
+    if t is None:
+        return None
+    return _rows(t if t.dim() == 2 else t.reshape(math.prod(t.shape[:-1]), cols))
 
 
 def _check_linear(x, weight, bias, residual, offsets):
     grouped = offsets is not None
-    _gpu(x, "x")
+    if not x.is_cuda:
+        raise ValueError("x must live on a GPU")
     _dtype(x, "x")
     if weight.dim() != (3 if grouped else 2):
         raise ValueError(f"weight has {weight.dim()} dimensions, expected {3 if grouped else 2}")
@@ -195,15 +223,15 @@ def _check_linear(x, weight, bias, residual, offsets):
         raise ValueError(f"x has {x.shape[-1]} columns, the weight takes {k}")
     _same(x, weight=weight, bias=bias, residual=residual)
     want = (weight.shape[0], n) if grouped else (n,)
-    if bias is not None and tuple(bias.shape) != want:
+    if bias is not None and bias.shape != want:
         raise ValueError(f"bias has shape {tuple(bias.shape)}, expected {want}")
-    if residual is not None and tuple(residual.shape) != (*x.shape[:-1], n):
+    if residual is not None and residual.shape != (*x.shape[:-1], n):
         raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {(*x.shape[:-1], n)}")
     if grouped:
         e = weight.shape[0]
         if not 1 <= e <= 65535:
             raise ValueError(f"{e} experts: 1 to 65535 are supported")
-        if offsets.dtype is not torch.int32 or tuple(offsets.shape) != (e + 1,) or not offsets.is_contiguous():
+        if offsets.dtype is not torch.int32 or offsets.shape != (e + 1,) or not offsets.is_contiguous():
             raise ValueError(f"offsets must be a contiguous int32 tensor of {e + 1} values")
         if offsets.device != x.device:
             raise ValueError(f"offsets is on {offsets.device}, x is on {x.device}")
@@ -211,66 +239,45 @@ def _check_linear(x, weight, bias, residual, offsets):
 
 def _forward(x, w, bias, residual, offsets, act, keep_z):
     """y and, where asked and the activation has a slope, z; x and residual 2-D with contiguous rows."""
-    lib = load_ops()
-    d = _desc(x, w, act, 0 if offsets is None else w.t.shape[0])
-    y = torch.empty((d.rows, d.n), dtype=x.dtype, device=x.device)
+    p = _plan(x, w, act, offsets is not None)
+    d, size = p.get(_FORWARD, _ld(residual) if residual is not None else p.n)
+    y = torch.empty(p.y_shape, dtype=x.dtype, device=x.device)
     z = torch.empty_like(y) if keep_z and act else None
-    if residual is not None:
-        d.ldr = _ld(residual)
-    with _On(x) as stream:
-        ws, size = _workspace(lib, d, _FORWARD, x)
-        _check(lib.muon_linear_forward(ctypes.byref(d), _ptr(offsets), x.data_ptr(), w.t.data_ptr(), _ptr(bias),
-                                       _ptr(residual), y.data_ptr(), _ptr(z), _ptr(ws), size, stream),
-               "muon_linear_forward")
+    ws = _workspace(size, x)
+    _call("muon_linear_forward", x, d, _ptr(offsets), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
+          y.data_ptr(), _ptr(z), _ptr(ws), size)
     return y, z
 
 
 def _backward(dy, x, w, z, offsets, act, need_x, need_w, need_b):
-    lib = load_ops()
-    groups = 0 if offsets is None else w.t.shape[0]
-    d = _desc(x, w, act, groups)
-    d.ldg = _ld(dy)
-    dz = dy
+    p = _plan(x, w, act, offsets is not None)
+    dz, ld, off = dy, _ld(dy), _ptr(offsets)
     dx = dw = db = None
-    with _On(x) as stream:
-        if need_b or act:
-            store = act != 0 and (need_x or need_w)
-            if store:
-                dz = torch.empty((d.rows, d.n), dtype=x.dtype, device=x.device)
-            if need_b:
-                db = torch.empty((max(groups, 1), d.n), dtype=x.dtype, device=x.device)
-                ws, size = _workspace(lib, d, _GRAD_ACT, x)
-            else:
-                ws, size = None, 0
-            if store or need_b:
-                _check(lib.muon_linear_grad_act(ctypes.byref(d), _ptr(offsets), dy.data_ptr(), _ptr(z),
-                                                dz.data_ptr() if store else None, _ptr(db), _ptr(ws), size, stream),
-                       "muon_linear_grad_act")
-            if store:
-                d.ldg = d.n
-            if db is not None and groups == 0:
-                db = db[0]
-        if need_x:
-            dx = torch.empty((d.rows, d.k), dtype=x.dtype, device=x.device)
-            ws, size = _workspace(lib, d, _GRAD_INPUT, x)
-            _check(lib.muon_linear_grad_input(ctypes.byref(d), _ptr(offsets), dz.data_ptr(), w.t.data_ptr(),
-                                              dx.data_ptr(), _ptr(ws), size, stream), "muon_linear_grad_input")
-        if need_w:
-            lead = () if groups == 0 else (groups,)
-            shape = (*lead, d.k, d.n) if w.layout == 0 else (*lead, d.n, d.k)
-            dw = torch.empty(shape, dtype=x.dtype, device=x.device)
-            ws, size = _workspace(lib, d, _GRAD_WEIGHT, x)
-            _check(lib.muon_linear_grad_weight(ctypes.byref(d), _ptr(offsets), x.data_ptr(), dz.data_ptr(),
-                                               dw.data_ptr(), _ptr(ws), size, stream), "muon_linear_grad_weight")
-            if w.layout == 1:
-                dw = dw.transpose(-1, -2)
+    store = act != 0 and (need_x or need_w)
+    if store or need_b:
+        d, size = p.get(_GRAD_ACT, ld)
+        if store:
+            dz = torch.empty(p.y_shape, dtype=x.dtype, device=x.device)
+        if need_b:
+            db = torch.empty((p.groups, p.n) if p.groups else (p.n,), dtype=x.dtype, device=x.device)
+        ws = _workspace(size, x) if need_b else None
+        _call("muon_linear_grad_act", x, d, off, dy.data_ptr(), _ptr(z), dz.data_ptr() if store else None, _ptr(db),
+              _ptr(ws), size)
+        if store:
+            ld = max(p.n, 1)
+    if need_x:
+        d, size = p.get(_GRAD_INPUT, ld)
+        dx = torch.empty((p.rows, p.k), dtype=x.dtype, device=x.device)
+        ws = _workspace(size, x)
+        _call("muon_linear_grad_input", x, d, off, dz.data_ptr(), w.data_ptr(), dx.data_ptr(), _ptr(ws), size)
+    if need_w:
+        d, size = p.get(_GRAD_WEIGHT, ld)
+        dw = torch.empty(p.dw_shape, dtype=x.dtype, device=x.device)
+        ws = _workspace(size, x)
+        _call("muon_linear_grad_weight", x, d, off, x.data_ptr(), dz.data_ptr(), dw.data_ptr(), _ptr(ws), size)
+        if p.layout == 1:
+            dw = dw.transpose(-1, -2)
     return dx, dw, db
-
-
-def _flat(t, cols):
-    if t is None:
-        return None
-    return _rows(t if t.dim() == 2 else t.reshape(math.prod(t.shape[:-1]), cols))
 
 
 def linear_forward(x, weight, bias=None, activation="none", residual=None, offsets=None, keep_z=False):
@@ -280,10 +287,17 @@ def linear_forward(x, weight, bias=None, activation="none", residual=None, offse
     ``keep_z`` and the activation is not "none"."""
     act = _activation(activation)
     _check_linear(x, weight, bias, residual, offsets)
+    return _prepared(x, weight, bias, residual, offsets, act, keep_z)[:2]
+
+
+def _prepared(x, weight, bias, residual, offsets, act, keep_z):
+    """The forward pass of checked arguments: y, z, and x and the weight as the kernels read them."""
     k, n = weight.shape[-2:]
-    y, z = _forward(_flat(x, k), _Weight(weight), None if bias is None else bias.contiguous(), _flat(residual, n),
-                    offsets, act, keep_z)
-    return y.view(*x.shape[:-1], n), z
+    x2 = _flat(x, k)
+    w = weight if _layout_ok(weight) else weight.contiguous()
+    b = bias if bias is None or bias.is_contiguous() else bias.contiguous()
+    y, z = _forward(x2, w, b, _flat(residual, n), offsets, act, keep_z)
+    return y if x.dim() == 2 else y.view(*x.shape[:-1], n), z, x2, w
 
 
 def linear_backward(dy, x, weight, z=None, activation="none", offsets=None, needs=(True, True, True)):
@@ -292,33 +306,31 @@ def linear_backward(dy, x, weight, z=None, activation="none", offsets=None, need
     z is what ``linear_forward(..., keep_z=True)`` returned (not used by "none").  The residual's gradient is dy."""
     act = _activation(activation)
     _check_linear(x, weight, None, dy, offsets)
-    if act and (z is None or z.dtype is not x.dtype or not z.is_contiguous() or z.numel() != dy.numel()):
+    if act and (z is None or z.dtype is not x.dtype or z.device != x.device or not z.is_contiguous()
+                or z.numel() != dy.numel()):
         raise ValueError("z must be the tensor that linear_forward(..., keep_z=True) returned")
     k, n = weight.shape[-2:]
-    dx, dw, db = _backward(_flat(dy, n), _flat(x, k), _Weight(weight), z, offsets, act, *needs)
+    w = weight if _layout_ok(weight) else weight.contiguous()
+    dx, dw, db = _backward(_flat(dy, n), _flat(x, k), w, z, offsets, act, *needs)
     return None if dx is None else dx.view(x.shape), dw, db
 
 
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, offsets, act):
-        k, n = weight.shape[-2:]
-        x2 = _flat(x, k)
-        w = _Weight(weight)
-        y, z = _forward(x2, w, None if bias is None else bias.contiguous(), _flat(residual, n), offsets, act, True)
-        ctx.save_for_backward(x2, w.t, z, offsets)
+        y, z, x2, w = _prepared(x, weight, bias, residual, offsets, act, True)
+        ctx.save_for_backward(x2, w, z, offsets)
         ctx.act, ctx.x_shape = act, x.shape
-        return y.view(*x.shape[:-1], n)
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, wt, z, offsets = ctx.saved_tensors
+        x, w, z, offsets = ctx.saved_tensors
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
         dx = dw = db = None
         if need_x or need_w or need_b:
-            dx, dw, db = _backward(_flat(dy, wt.shape[-1]), x, _Weight(wt), z, offsets, ctx.act, need_x, need_w,
-                                   need_b)
+            dx, dw, db = _backward(_flat(dy, w.shape[-1]), x, w, z, offsets, ctx.act, need_x, need_w, need_b)
             if dx is not None:
                 dx = dx.view(ctx.x_shape)
         return dx, dw, db, dy if need_r else None, None, None
@@ -369,6 +381,9 @@ class Routing(NamedTuple):
     position: torch.Tensor
 
 
+_route_sizes = {}
+
+
 def route(expert_ids, n_experts):
     """Sorts the entries of expert_ids [tokens, top] (int64 or int32) by expert, stably.
 
@@ -378,18 +393,21 @@ def route(expert_ids, n_experts):
         raise ValueError("expert_ids must be [tokens, top] with top >= 1")
     if expert_ids.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"expert_ids is {expert_ids.dtype}: int64 or int32 is supported")
-    lib = load_ops()
     ids = expert_ids.contiguous()
     tokens, top = ids.shape
-    need = ctypes.c_uint64(0)
-    _check(lib.muon_route_workspace(tokens * top, n_experts, ctypes.byref(need)), "muon_route_workspace")
+    need = _route_sizes.get((tokens * top, n_experts))
+    if need is None:
+        got = ctypes.c_uint64(0)
+        _check(load_ops().muon_route_workspace(tokens * top, n_experts, ctypes.byref(got)), "muon_route_workspace")
+        if len(_route_sizes) >= 4096:
+            _route_sizes.clear()
+        need = _route_sizes[(tokens * top, n_experts)] = got.value
     # One allocation holds the three results and the workspace, each 16-byte aligned.
     e4, p4 = (n_experts + 1 + 3) // 4 * 4, (tokens * top + 3) // 4 * 4
-    buf = torch.empty(e4 + 2 * p4 + need.value // 4, dtype=torch.int32, device=ids.device)
+    buf = torch.empty(e4 + 2 * p4 + need // 4, dtype=torch.int32, device=ids.device)
     at, end = buf.data_ptr(), tokens * top
-    with _On(ids) as stream:
-        _check(lib.muon_route(ids.data_ptr(), ids.element_size(), tokens, top, n_experts, at, at + 4 * e4,
-                              at + 4 * (e4 + p4), at + 4 * (e4 + 2 * p4), need.value, stream), "muon_route")
+    _call("muon_route", ids, ids.data_ptr(), ids.element_size(), tokens, top, n_experts, at, at + 4 * e4,
+          at + 4 * (e4 + p4), at + 4 * (e4 + 2 * p4), need)
     return Routing(buf[:n_experts + 1], buf[e4:e4 + end], buf[e4 + p4:e4 + p4 + end].view(tokens, top))
 
 
@@ -421,9 +439,8 @@ def dispatch_forward(x, routing):
     d = _move(routing, tokens, x.shape[1], _dtype(x, "x"))
     d.ldx = _ld(x)
     xs = torch.empty((tokens * top, x.shape[1]), dtype=x.dtype, device=x.device)
-    with _On(x) as stream:
-        _check(load_ops().muon_dispatch(ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(),
-                                        x.data_ptr(), xs.data_ptr(), stream), "muon_dispatch")
+    _call("muon_dispatch", x, ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(), x.data_ptr(),
+          xs.data_ptr())
     return xs
 
 
@@ -435,9 +452,7 @@ def dispatch_backward(dxs, routing):
     d = _move(routing, tokens, dxs.shape[1], _dtype(dxs, "dxs"))
     d.ldx = _ld(dxs)
     dx = torch.empty((tokens, dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
-    with _On(dxs) as stream:
-        _check(load_ops().muon_dispatch_grad(ctypes.byref(d), routing.position.data_ptr(), dxs.data_ptr(),
-                                             dx.data_ptr(), stream), "muon_dispatch_grad")
+    _call("muon_dispatch_grad", dxs, ctypes.byref(d), routing.position.data_ptr(), dxs.data_ptr(), dx.data_ptr())
     return dx
 
 
@@ -464,9 +479,8 @@ def combine_forward(ys, routing, weights, residual=None):
     if residual is not None:
         d.ldr = _ld(residual)
     y = torch.empty((tokens, h), dtype=ys.dtype, device=ys.device)
-    with _On(ys) as stream:
-        _check(load_ops().muon_combine(ctypes.byref(d), routing.position.data_ptr(), w.data_ptr(), ys.data_ptr(),
-                                       _ptr(residual), y.data_ptr(), stream), "muon_combine")
+    _call("muon_combine", ys, ctypes.byref(d), routing.position.data_ptr(), w.data_ptr(), ys.data_ptr(),
+          _ptr(residual), y.data_ptr())
     return y
 
 
@@ -484,10 +498,8 @@ def combine_backward(dy, ys, routing, weights, needs=(True, True)):
     d.ldx, d.ldg = _ld(ys), _ld(dy)
     dys = torch.empty((tokens * top, ys.shape[1]), dtype=ys.dtype, device=ys.device) if needs[0] else None
     dw = torch.empty((tokens, top), dtype=torch.float32, device=ys.device) if needs[1] else None
-    with _On(ys) as stream:
-        _check(load_ops().muon_combine_grad(ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(),
-                                            w.data_ptr(), ys.data_ptr(), dy.data_ptr(), _ptr(dys), _ptr(dw), stream),
-               "muon_combine_grad")
+    _call("muon_combine_grad", ys, ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(),
+          w.data_ptr(), ys.data_ptr(), dy.data_ptr(), _ptr(dys), _ptr(dw))
     return dys, dw
 
 
@@ -557,10 +569,8 @@ def dropout_forward(x, p, seed=0, offset=0, residual=None, state=None):
     x = x.contiguous()
     residual = None if residual is None else residual.contiguous()
     y = torch.empty_like(x)
-    with _On(x) as stream:
-        _check(load_ops().muon_dropout(code, x.numel(), x.data_ptr(), _ptr(residual), y.data_ptr(), p,
-                                       seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, _ptr(state), stream),
-               "muon_dropout")
+    _call("muon_dropout", x, code, x.numel(), x.data_ptr(), _ptr(residual), y.data_ptr(), p,
+          seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, _ptr(state))
     return y
 
 
