@@ -63,10 +63,11 @@ typedef enum {
   MUON_LINEAR_FORWARD = 0,
   MUON_LINEAR_GRAD_ACT = 1,
   MUON_LINEAR_GRAD_INPUT = 2,
-  MUON_LINEAR_GRAD_WEIGHT = 3
+  MUON_LINEAR_GRAD_WEIGHT = 3,
+  MUON_LINEAR_BACKWARD = 4
 } muon_linear_op_t;
 
-/* Workspace of one of the four calls below, for pointers that are 16-byte
+/* Workspace of one of the calls below, for pointers that are 16-byte
  * aligned or not (host only; 0 for many shapes). */
 int muon_linear_workspace(const muon_linear_desc_t* desc, int32_t op, uint64_t* bytes);
 
@@ -91,6 +92,12 @@ int muon_linear_grad_input(const muon_linear_desc_t* desc, const int32_t* offset
  * ([k, n], or [n, k] for 1); zero for an expert without rows. */
 int muon_linear_grad_weight(const muon_linear_desc_t* desc, const int32_t* offsets, const void* x, const void* dz,
                             void* dw, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* The three steps above in one call: dx, dw and db, each NULL where not wanted,
+ * from x, W, z and dy; dz stays in the workspace. */
+int muon_linear_backward(const muon_linear_desc_t* desc, const int32_t* offsets, const void* x, const void* w,
+                         const void* z, const void* dy, void* dx, void* dw, void* db, void* workspace,
+                         uint64_t workspace_bytes, void* stream);
 
 #define MUON_ROUTE_MAX_EXPERTS 1024
 

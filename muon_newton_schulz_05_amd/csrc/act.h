@@ -123,21 +123,31 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int groups, i
 // Eight consecutive elements as float32, n of them inside the row (the others
 // are zero).  Whole groups move as 16-byte accesses at any alignment of
 // their elements, which the hardware splits where it has to.
-template <typename T>
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));  // at any alignment of 16-bit elements
+template <typename T, bool NT = false>
+__device__ __forceinline__ u32x4_t load16(const T* p) {
+  const MUON_GLOBAL u32x4_any_t* q = (const MUON_GLOBAL u32x4_any_t*)as_global(p);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+template <bool NT = false, typename T>
+__device__ __forceinline__ void store16(T* p, u32x4_t w) {
+  MUON_GLOBAL u32x4_any_t* q = (MUON_GLOBAL u32x4_any_t*)as_global(p);
+  if constexpr (NT) __builtin_nontemporal_store(w, q);
+  else *q = w;
+}
+template <typename T, bool NT = false>
 __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
   if (n >= 8) {
     if constexpr (sizeof(T) == 2) {
-      u32x4_t w;
-      __builtin_memcpy(&w, as_global(p), 16);
+      const u32x4_t w = load16<T, NT>(p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = bf16_lo(w[i]);
         v[2 * i + 1] = bf16_hi(w[i]);
       }
     } else {
-      f32x4_t w[2];
-      __builtin_memcpy(&w[0], as_global(p), 16);
-      __builtin_memcpy(&w[1], as_global(p + 4), 16);
+      const f32x4_t w[2] = {__builtin_bit_cast(f32x4_t, load16<T, NT>(p)), __builtin_bit_cast(f32x4_t, load16<T, NT>(p + 4))};
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = w[i >> 2][i & 3];
     }
@@ -146,16 +156,15 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = i < n ? x_to_f32(p[i]) : 0.f;
 }
-template <typename T>
+template <typename T, bool NT = false>
 __device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
   if (n >= 8) {
     if constexpr (sizeof(T) == 2) {
-      const u32x4_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-      __builtin_memcpy(as_global(p), &w, 16);
+      store16<NT>(p, u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                             pack_bf16x2(v[6], v[7])});
     } else {
-      const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-      __builtin_memcpy(as_global(p), &a, 16);
-      __builtin_memcpy(as_global(p + 4), &b, 16);
+      store16<NT>(p, __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]}));
+      store16<NT>(p + 4, __builtin_bit_cast(u32x4_t, f32x4_t{v[4], v[5], v[6], v[7]}));
     }
     return;
   }

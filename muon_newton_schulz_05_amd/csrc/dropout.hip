@@ -28,11 +28,11 @@ __device__ __forceinline__ u32x4_t philox(uint64_t block, uint64_t offset, uint6
   return u32x4_t{c0, c1, c2, c3};
 }
 
-template <typename T>
+template <typename T, bool FULL>
 __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a) {
   const int64_t blk = (int64_t)blockIdx.x * 256 + threadIdx.x, i0 = blk * 8;
   if (i0 >= a.n) return;
-  const int n = (int)min((int64_t)8, a.n - i0);
+  const int n = FULL ? 8 : (int)min((int64_t)8, a.n - i0);
   const uint64_t seed = a.state ? a.state[0] : a.seed, offset = a.state ? a.state[1] : a.offset;
   float v[8], r[8] = {};
   load8(static_cast<const T*>(a.x) + i0, n, v);
@@ -54,8 +54,12 @@ hipError_t launch_dropout(const DropoutArgs& a, int dtype, hipStream_t s) {
   const int64_t blocks = ((a.n + 7) / 8 + 255) / 256;
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (dtype == MUON_BF16) hipLaunchKernelGGL((k_dropout<uint16_t>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_dropout<float>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  const bool full = a.n % 8 == 0;
+  const dim3 grid((unsigned)blocks), block(256);
+  if (dtype == MUON_BF16 && full) hipLaunchKernelGGL((k_dropout<uint16_t, true>), grid, block, 0, s, a);
+  else if (dtype == MUON_BF16) hipLaunchKernelGGL((k_dropout<uint16_t, false>), grid, block, 0, s, a);
+  else if (full) hipLaunchKernelGGL((k_dropout<float, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_dropout<float, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

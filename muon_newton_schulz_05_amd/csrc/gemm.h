@@ -36,11 +36,13 @@ constexpr uint32_t kRecords = 0x7fffffffu;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-// 16 bytes a lane from base + off (zeros past the descriptor's end) to 1 KB of
-// LDS, lane l at byte 16 l.
+// LB bytes a lane from base + off (zeros past the descriptor's end) to LDS, lane l
+// at byte LB l.
+template <int LB>
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, char* dst) {
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, kRecords, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void LDS_PTR*)dst, 16, off, 0, 0, 0);
+  if constexpr (LB == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void LDS_PTR*)dst, 16, off, 0, 0, 0);
+  else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void LDS_PTR*)dst, 4, off, 0, 0, 0);
 }
 // Wait until at most N of this wave's loads are in flight and its LDS reads are
 // done.  (The builtin, not inline asm: the compiler then knows that no LDS
@@ -73,33 +75,33 @@ template <typename T> struct Mma;
 template <> struct Mma<uint16_t> {
   static constexpr int N = 1;
   typedef bf16x8_t Frag;  // eight k of one row: k = 32 s + 8 (lane / 16) + 0..7
-  static __device__ __forceinline__ f32x4_t mul(Frag a, Frag b, f32x4_t c) {
+  static __device__ __forceinline__ f32x4_t mul(Frag a, Frag b, f32x4_t c, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
 };
 template <> struct Mma<float> {
   static constexpr int N = 4;
   typedef f32x4_t Frag;   // four k of one row: k = 16 s + 4 (lane / 16) + 0..3
-  static __device__ __forceinline__ f32x4_t mul(Frag a, Frag b, f32x4_t c) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
-    return c;
+  static __device__ __forceinline__ f32x4_t mul(Frag a, Frag b, f32x4_t c, int q) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a[q], b[q], c, 0, 0, 0);
   }
 };
 
 // One operand's tile: R rows x one k-slice.
 constexpr int KB = 128;  // bytes of a k-slice's row
 
-template <typename T, int R, bool TR, int NW, bool DIRECT>
+template <typename T, int R, bool TR, int NW, int LOADS, int PD>
 struct Panel {
+  static constexpr bool DIRECT = LOADS != kStaged;
+  static constexpr int LB = LOADS == kDirect4 ? 4 : 16;  // bytes a lane
   static constexpr int EPC = 16 / sizeof(T);          // elements of a 16-byte chunk
   static constexpr int BK = KB / sizeof(T);           // k of a slice
   static constexpr int RB = TR ? R * (int)sizeof(T) : KB;  // bytes of an LDS row
   static constexpr int CPR = RB / 16;                 // its chunks
   static constexpr int BYTES = R * KB;
-  static constexpr int LI = BYTES / 1024 / NW;        // 1 KB loads a wave and slice
+  static constexpr int LI = BYTES / (64 * LB) / NW;   // loads a wave and slice
   static constexpr int READS = !TR ? 1 : sizeof(T) == 2 ? 2 : 4;  // LDS reads of a fragment
-  static_assert(BYTES % (1024 * NW) == 0, "whole loads");
+  static_assert(BYTES % (64 * LB * NW) == 0, "whole loads");
   typedef typename Mma<T>::Frag Frag;
 
   static __device__ __forceinline__ int swz(int row) {
@@ -113,11 +115,14 @@ struct Panel {
   int64_t ld;           // bytes from one row (k-row when TR) to the next
   uint32_t off[LI];     // this lane's offsets; kNoLoad outside the tile's rows
   int left[LI];         // not DIRECT: elements of the chunk inside the rows (TR) or 1 / 0
-  u32x4_t reg[DIRECT ? 1 : LI];
+  u32x4_t reg[DIRECT ? 1 : PD][DIRECT ? 1 : LI];
 
-  static __device__ __forceinline__ int slot(int u, int wave, int lane) { return (wave + NW * u) * 64 + lane; }
-  static __device__ __forceinline__ int lrow(int s) { return s / CPR; }
-  static __device__ __forceinline__ int chunk(int s) { return (s % CPR) ^ swz(s / CPR); }
+  // Byte of the tile that load u fills in this lane; its 16-byte slot's row and
+  // chunk, and the element inside the chunk.
+  static __device__ __forceinline__ int place(int u, int wave, int lane) { return ((wave + NW * u) * 64 + lane) * LB; }
+  static __device__ __forceinline__ int lrow(int b) { return b / RB; }
+  static __device__ __forceinline__ int chunk(int b) { return (b % RB / 16) ^ swz(b / RB); }
+  static __device__ __forceinline__ int element(int b) { return LB == 16 ? 0 : b % 16 / (int)sizeof(T); }
 
   // rows: rows of the operand inside the tile (at most R).
   __device__ __forceinline__ void init(const char* p, int64_t ld_bytes, int rows, int wave, int lane) {
@@ -125,10 +130,10 @@ struct Panel {
     ld = ld_bytes;
 #pragma unroll
     for (int u = 0; u < LI; ++u) {
-      const int s = slot(u, wave, lane), r = lrow(s), c = chunk(s);
+      const int s = place(u, wave, lane), r = lrow(s), c = chunk(s);
       if constexpr (DIRECT) {
-        const bool ok = TR ? c * EPC < rows : r < rows;
-        off[u] = ok ? (uint32_t)(r * (int)ld_bytes + c * 16) : kNoLoad;
+        const bool ok = TR ? c * EPC + element(s) < rows : r < rows;
+        off[u] = ok ? (uint32_t)(r * (int)ld_bytes + c * 16 + element(s) * (int)sizeof(T)) : kNoLoad;
       } else {
         left[u] = TR ? min(EPC, rows - c * EPC) : (r < rows ? 1 : 0);
       }
@@ -141,22 +146,24 @@ struct Panel {
   // products around them are scheduled as one block.
   __device__ __forceinline__ void issue(int kt, int k_left, char* st, int wave, int lane) {
     const char* p = at(kt);
-    // A lane's first k: in an operand contiguous along k the swizzle of rows
-    // 1024 / KB NW u apart is the same, so one value serves every load.
-    static_assert(NW * (1024 / KB) % 16 == 0, "swizzle");
-    const int s0 = slot(0, wave, lane), k0 = TR ? lrow(s0) : chunk(s0) * EPC;
+    // A lane's first k.  In an operand contiguous along k the swizzle repeats every
+    // 16 rows: with 16-byte pieces one value serves every load, with 4-byte
+    // pieces every other one.
+    static_assert(TR ? NW * 64 * LB % RB == 0 : (LB == 4 ? 2 : 1) * NW * 64 * LB / KB % 16 == 0, "rows of a lane");
+    const int s0 = place(0, wave, lane), s1 = place(1, wave, lane);
+    const int k0 = TR ? lrow(s0) : chunk(s0) * EPC + element(s0), k1 = LB == 4 ? chunk(s1) * EPC + element(s1) : k0;
 #pragma unroll
     for (int u = 0; u < LI; ++u) {
-      const int kk = TR ? k0 + u * (NW * 64 / CPR) : k0;
-      load_to_lds(p, kk < k_left ? off[u] : kNoLoad, st + (wave + NW * u) * 1024);
+      const int kk = TR ? k0 + u * (NW * 64 * LB / RB) : u & 1 ? k1 : k0;
+      load_to_lds<LB>(p, kk < k_left ? off[u] : kNoLoad, st + (wave + NW * u) * 64 * LB);
     }
   }
   // Otherwise: slice kt into registers (any alignment; a chunk that is only
   // partly inside is taken element by element), then from there to LDS.
-  __device__ __forceinline__ void fetch(int kt, int k_left, int wave, int lane) {
+  __device__ __forceinline__ void fetch(int kt, int k_left, int slot_, int wave, int lane) {
 #pragma unroll
     for (int u = 0; u < LI; ++u) {
-      const int s = slot(u, wave, lane), r = lrow(s), c = chunk(s);
+      const int s = place(u, wave, lane), r = lrow(s), c = chunk(s);
       const int n = TR ? (r < k_left ? left[u] : 0) : (left[u] ? min(EPC, k_left - c * EPC) : 0);
       const char* p = at(kt) + (int64_t)r * ld + c * 16;
       u32x4_t v = {0u, 0u, 0u, 0u};
@@ -171,12 +178,12 @@ struct Panel {
             else v[i / 2] |= (uint32_t)q[i] << (16 * (i & 1));
           }
       }
-      reg[u] = v;
+      reg[slot_][u] = v;
     }
   }
-  __device__ __forceinline__ void put(char* st, int wave, int lane) const {
+  __device__ __forceinline__ void put(char* st, int slot_, int wave, int lane) const {
 #pragma unroll
-    for (int u = 0; u < LI; ++u) *reinterpret_cast<u32x4_t*>(st + (wave + NW * u) * 1024 + lane * 16) = reg[u];
+    for (int u = 0; u < LI; ++u) *reinterpret_cast<u32x4_t*>(st + (wave + NW * u) * 1024 + lane * 16) = reg[slot_][u];
   }
 
   // The fragment of substep s (32 bf16 or 16 float32 of k) for rows
@@ -243,19 +250,26 @@ __device__ __forceinline__ void stripe(int t, int tiles_m, int tiles_n, int& tm,
   tm = 4 * s + u - tn * w;
 }
 
-template <typename T, int BM, int BN, int WGM, int WGN, int NS, bool TA, bool TB, bool DIRECT, int MINB>
-__global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
+// WGM x WGN waves share a tile; WGK such sets of waves take every WGK-th k-slice
+// each, with stages of their own, and add up in the epilogue in set order.
+// PD: slices held in registers ahead of LDS where loads are not direct.
+template <typename T, int BM, int BN, int WGM, int WGN, int WGK, int NS, bool TA, bool TB, int LOADS>
+__global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
-  typedef Panel<T, BM, TA, NW, DIRECT> PA;
-  typedef Panel<T, BN, TB, NW, DIRECT> PB;
+  constexpr bool DIRECT = LOADS != kStaged;
+  constexpr int PD = DIRECT ? 1 : BM * BN <= 64 * 64 ? 4 : 2;
+  typedef Panel<T, BM, TA, NW, LOADS, PD> PA;
+  typedef Panel<T, BN, TB, NW, LOADS, PD> PB;
   typedef typename Mma<T>::Frag Frag;
   constexpr int BK = PA::BK, SUB = KB / 64, STAGE = PA::BYTES + PB::BYTES;
   constexpr int STRIDE = WN * 4 + 16;  // bytes of a staged epilogue row: rows 4 apart fall on distinct bank quarters
-  constexpr int LDS = NS * STAGE > NW * 32 * STRIDE ? NS * STAGE : NW * 32 * STRIDE;
+  constexpr int LDS = WGK * (NS * STAGE > NW * 32 * STRIDE ? NS * STAGE : NW * 32 * STRIDE);
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = wave_all % NW, set = wave_all / NW;
+  static_assert(WGK == 1 || (DIRECT && BM == 32), "sets of waves: direct loads, one strip of rows");
   // Waves w and w + 4 share a SIMD.  With 2 x 4 of them, each SIMD gets one wave
   // of the tile's upper and one of its lower half, and one of its left and one of
   // its right half, so that a tile with half of its rows or columns outside
@@ -327,27 +341,34 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
     for (int i = 1; i < FM; ++i) af[s & 1][i] = PA::frag(st, wm * WM + 16 * i, s, lane);
   };
   auto multiply = [&](int s) __attribute__((always_inline)) {
+    // A block's steps (four of float32) are apart by all the others: a product
+    // that waits for the one before it in its accumulator would idle the unit.
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int q = 0; q < Mma<T>::N; ++q)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(af[s & 1][i], bf[s & 1][j], acc[i][j]);
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(af[s & 1][i], bf[s & 1][j], acc[i][j], q);
   };
 
   if constexpr (DIRECT) {
     constexpr int L = PA::LI + PB::LI;
-    auto issue = [&](int kt, char* fill) __attribute__((always_inline)) {
+    char* stages = lds + set * NS * STAGE;
+    const int its = (nk + WGK - 1) / WGK;  // slices of a set (those past the end are zeros)
+    auto issue = [&](int it, char* fill) __attribute__((always_inline)) {
+      const int kt = it * WGK + set;
       const int k_left = (int)max((int64_t)0, min((int64_t)BK, kk - (int64_t)kt * BK));
       pa.issue(kt, k_left, fill, wave, lane);
       pb.issue(kt, k_left, fill + PA::BYTES, wave, lane);
     };
     if (nk > 0) {
 #pragma unroll
-      for (int p = 0; p < NS - 1; ++p) issue(p, lds + p * STAGE);
+      for (int p = 0; p < NS - 1; ++p) issue(p, stages + p * STAGE);
     }
     auto run = [&](auto idle_tag) __attribute__((always_inline)) {
       constexpr bool IDLE = decltype(idle_tag)::value;
       int stage = 0;
-      for (int kt = 0; kt < nk; ++kt) {
+      for (int kt = 0; kt < its; ++kt) {
         // Slices kt + 1 .. kt + NS - 2 stay in flight; the barrier then says that
         // slice kt is whole and that slice kt - 1 has been read by all.
         static_assert((NS - 2) * L < 64, "waits");
@@ -375,7 +396,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
             else interleave<RD, 0, 1, MM>();
           }
         };
-        step(lds + (stage == 0 ? NS - 1 : stage - 1) * STAGE, lds + stage * STAGE);
+        step(stages + (stage == 0 ? NS - 1 : stage - 1) * STAGE, stages + stage * STAGE);
         stage = stage == NS - 1 ? 0 : stage + 1;
       }
       if (!IDLE && nk > 0) multiply(SUB - 1);
@@ -384,22 +405,31 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
     else run(std::false_type{});
     wait_loads<0>();
   } else {
-    auto fetch = [&](int kt) {
+    auto fetch = [&](int kt, int q) __attribute__((always_inline)) {
       const int k_left = (int)min((int64_t)BK, kk - (int64_t)kt * BK);
-      pa.fetch(kt, k_left, wave, lane);
-      pb.fetch(kt, k_left, wave, lane);
+      pa.fetch(kt, k_left, q, wave, lane);
+      pb.fetch(kt, k_left, q, wave, lane);
     };
-    if (nk > 0) fetch(0);
-    for (int kt = 0; kt < nk; ++kt) {
-      char* st = lds + (kt & 1) * STAGE;  // last read at slice kt - 2, a barrier ago
-      pa.put(st, wave, lane);
-      pb.put(st + PA::BYTES, wave, lane);
-      if (kt + 1 < nk) fetch(kt + 1);
-      __syncthreads();
 #pragma unroll
-      for (int s = 0; s < SUB; ++s) {
-        read(st, s);
-        multiply(s);
+    for (int q = 0; q < PD; ++q)
+      if (q < nk) fetch(q, q);
+    for (int k0t = 0; k0t < nk; k0t += PD) {
+#pragma unroll
+      for (int q = 0; q < PD; ++q) {
+        const int kt = k0t + q;
+        if (kt >= nk) break;
+        char* st = lds + (q & 1) * STAGE;  // last read at slice kt - 2, a barrier ago
+        pa.put(st, q, wave, lane);
+        pb.put(st + PA::BYTES, q, wave, lane);
+        if (kt + PD < nk) fetch(kt + PD, q);
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0: this wave's part is in LDS; loads stay in flight
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+          read(st, s);
+          multiply(s);
+        }
       }
     }
   }
@@ -409,39 +439,59 @@ __global__ __launch_bounds__(64 * WGM * WGN, MINB) void k_gemm(GemmArgs g) {
   // a row of C leaves as whole 16-byte pieces.  Register u of a block is row
   // 4 (lane / 16) + u, column lane mod 16.
   constexpr int LPR = WN / 8, RPP = 64 / LPR;
-  char* stg = lds + wave * 32 * STRIDE;
+  char* stg = lds + wave_all * 32 * STRIDE;
   const int col = tn * BN + wn * WN + 8 * (lane % LPR);
-  const int n = (int)min((int64_t)8, g.n - col);
+  const int n_in = (int)min((int64_t)8, g.n - col);
   float bias[8] = {};
-  if (g.bias && n > 0 && !g.part && !(!GK && e == g.groups && g.offsets))
-    load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n, bias);
+  if (g.bias && n_in > 0 && !g.part && !(!GK && e == g.groups && g.offsets))
+    load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n_in, bias);
   const int64_t crow0 = GK ? (int64_t)tm * BM : row0;
+  // Where n is a multiple of 8 every piece is whole: no branch between the loads and
+  // stores of a strip.
+  auto strips = [&](auto full_tag) __attribute__((always_inline)) {
+    const int n = decltype(full_tag)::value ? 8 : n_in;
 #pragma unroll
-  for (int i = 0; i < WM / 32; ++i) {
+    for (int i = 0; i < WM / 32; ++i) {
 #pragma unroll
-    for (int ii = 0; ii < 2; ++ii)
+      for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int lr = 16 * ii + 4 * (lane >> 4) + u;
-          *reinterpret_cast<float*>(stg + lr * STRIDE + (16 * j + (lane & 15)) * 4) = acc[2 * i + ii][j][u];
+          for (int u = 0; u < 4; ++u) {
+            const int lr = 16 * ii + 4 * (lane >> 4) + u;
+            *reinterpret_cast<float*>(stg + lr * STRIDE + (16 * j + (lane & 15)) * 4) = acc[2 * i + ii][j][u];
+          }
+      if constexpr (WGK > 1) __syncthreads();
+      else wave_fence();
+      // One wave reads its strip back; with several sets, each set takes its share
+      // of the 32 rows and adds the sets' values in order.
+      constexpr int ROWS = 32 / WGK;
+#pragma unroll
+      for (int p = 0; p < (ROWS + RPP - 1) / RPP; ++p) {
+        const int pr = p * RPP + lane / LPR, lr = set * ROWS + pr;
+        float v[8] = {};
+#pragma unroll
+        for (int q = 0; q < WGK; ++q) {
+          const char* from = WGK == 1 ? stg : lds + (q * NW + wave) * 32 * STRIDE;
+          const f32x4_t* src = reinterpret_cast<const f32x4_t*>(from + min(lr, 31) * STRIDE + (lane % LPR) * 32);
+          const f32x4_t x = src[0], y = src[1];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            v[c] += x[c];
+            v[4 + c] += y[c];
+          }
         }
-    wave_fence();
-#pragma unroll
-    for (int p = 0; p < 32 / RPP; ++p) {
-      const int lr = p * RPP + lane / LPR;
-      const f32x4_t* q = reinterpret_cast<const f32x4_t*>(stg + lr * STRIDE + (lane % LPR) * 32);
-      const f32x4_t x = q[0], y = q[1];
-      float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-      const int64_t row = crow0 + wm * WM + 32 * i + lr;
-      if (row < end && n > 0) {
-        if (g.part) store8(g.part + ((int64_t)split * g.m + row) * g.n + col, n, v);
-        else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);
+        const int64_t row = crow0 + wm * WM + 32 * i + lr;
+        if (pr < ROWS && row < end && n_in > 0) {
+          if (g.part) store8(g.part + ((int64_t)split * g.m + row) * g.n + col, n, v);
+          else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);
+        }
       }
+      if constexpr (WGK == 1) wave_fence();
     }
-    wave_fence();
-  }
+  };
+  if ((g.n & 7) == 0) strips(std::true_type{});
+  else strips(std::false_type{});
 }
 
 // Joins a split contraction: the partials of an entry are added in split
@@ -463,15 +513,15 @@ __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs g) {
   finish8<T>(g, v, bias, 0, row, col, n);
 }
 
-template <typename T, int BM, int BN, int WGM, int WGN, int NS, bool DIRECT, int MINB>
+template <typename T, int BM, int BN, int WGM, int WGN, int WGK, int NS, int LOADS>
 hipError_t launch_tile(const GemmArgs& g, bool ta, bool tb, hipStream_t s) {
   const int64_t blocks = (int64_t)g.tiles_m * g.tiles_n * g.splits * (ta && tb && g.offsets ? g.groups : 1);
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), block(64 * WGM * WGN);
-  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, NS, true, true, DIRECT, MINB>), grid, block, 0, s, g);
-  else if (tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, NS, false, true, DIRECT, MINB>), grid, block, 0, s, g);
-  else if (!ta) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, NS, false, false, DIRECT, MINB>), grid, block, 0, s, g);
+  const dim3 grid((unsigned)blocks), block(64 * WGM * WGN * WGK);
+  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, true, true, LOADS>), grid, block, 0, s, g);
+  else if (tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, false, true, LOADS>), grid, block, 0, s, g);
+  else if (!ta) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, false, false, LOADS>), grid, block, 0, s, g);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

@@ -4,22 +4,45 @@
 
 namespace muon {
 
-hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, bool direct, int tile, hipStream_t s) {
-  if (!direct) {
-    if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 2, false, 1>(g, ta, tb, s);
-    return launch_tile<float, 128, 128, 2, 2, 2, false, 1>(g, ta, tb, s);
+hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s) {
+  if (loads == kDirect4) {
+    if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 1, 4, kDirect4>(g, ta, tb, s);
+    return launch_tile<float, 128, 128, 2, 2, 1, 2, kDirect4>(g, ta, tb, s);
   }
-  if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 2, true, 1>(g, ta, tb, s);
-  if (tile == kTileRows32) return launch_tile<float, 32, 128, 1, 4, 4, true, 1>(g, ta, tb, s);
-  return launch_tile<float, 128, 128, 2, 2, 2, true, 1>(g, ta, tb, s);
+  if (loads == kStaged) {
+    if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
+    return launch_tile<float, 128, 128, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
+  }
+  switch (tile) {
+    case kTile64: return launch_tile<float, 64, 64, 2, 2, 1, 4, kDirect16>(g, ta, tb, s);
+    case kTileRows32: return launch_tile<float, 32, 128, 1, 4, 1, 4, kDirect16>(g, ta, tb, s);
+    case kTileRows32K: return launch_tile<float, 32, 64, 1, 2, 4, 3, kDirect16>(g, ta, tb, s);
+    default: return launch_tile<float, 128, 128, 2, 2, 1, 2, kDirect16>(g, ta, tb, s);
+  }
 }
 
-int gemm_tile_m(int tile) { return tile == kTile256 || tile == kTile256x128 ? 256 : tile == kTileRows32 ? 32 : tile == kTile64 ? 64 : 128; }
-int gemm_tile_n(int tile) { return tile == kTile256 ? 256 : tile == kTile64 ? 64 : 128; }
+int gemm_tile_m(int tile) {
+  switch (tile) {
+    case kTile256:
+    case kTile256x128: return 256;
+    case kTile64: return 64;
+    case kTileRows32:
+    case kTileRows32K: return 32;
+    default: return 128;
+  }
+}
+int gemm_tile_n(int tile) {
+  switch (tile) {
+    case kTile256: return 256;
+    case kTile64:
+    case kTileRows32K: return 64;
+    default: return 128;
+  }
+}
 
-hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, bool direct, int tile, hipStream_t s) {
-  return dtype == MUON_BF16 ? launch_gemm_bf16(g, ta, tb, direct, tile, s)
-                            : launch_gemm_f32(g, ta, tb, direct, tile, s);
+hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, int loads, int tile, hipStream_t s) {
+  return dtype == MUON_BF16 ? launch_gemm_bf16(g, ta, tb, loads, tile, s)
+                            : launch_gemm_f32(g, ta, tb, loads, tile, s);
 }
 
 hipError_t launch_gemm_join(const GemmArgs& g, int dtype, hipStream_t s) {
@@ -38,7 +61,7 @@ namespace {
 // Each lane holds 8 columns and each of the 4 waves every fourth row; the waves'
 // sums meet in LDS in wave order.  Bound by memory: it reads dy and z and
 // writes dz once.
-template <typename T>
+template <typename T, bool FULL>
 __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int cols = (int)((a.n + 511) / 512);
@@ -52,26 +75,36 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
     hi = (int)min((int64_t)lo + a.block, a.rows);
   }
   const int64_t col = (int64_t)cb * 512 + lane * 8;
-  const int n = (int)min((int64_t)8, a.n - col);
+  const int n = FULL ? (col < a.n ? 8 : 0) : (int)min((int64_t)8, a.n - col);
   float sum[8] = {};
   // Rows past the last group: their gradient is zero.
   const bool dead = a.offsets && e == a.groups;
   if (n > 0) {
-    for (int r = lo + wave; r < hi; r += 4) {
-      float v[8], z[8];
-      load8(static_cast<const T*>(a.dy) + (int64_t)r * a.lddy + col, n, v);
-      if (a.z) {
-        load8(static_cast<const T*>(a.z) + (int64_t)r * a.ldz + col, n, z);
+    constexpr int U = 4;  // rows in flight; past the block's end the last row is read again, not used
+    for (int r0 = lo + wave; r0 < hi; r0 += 4 * U) {
+      float v[U][8], z[U][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], a.act);
+      for (int u = 0; u < U; ++u) {
+        const int64_t r = min(r0 + 4 * u, hi - 1);
+        load8(static_cast<const T*>(a.dy) + r * a.lddy + col, FULL ? 8 : n, v[u]);
+        if (a.z) load8(static_cast<const T*>(a.z) + r * a.ldz + col, FULL ? 8 : n, z[u]);
       }
-      if (dead) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + 4 * u;
+        if (r >= hi) break;
+        if (a.z) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u][i] *= act_slope(z[u][i], a.act);
+        }
+        if (dead) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        }
+        if (a.dz) store8(static_cast<T*>(a.dz) + (int64_t)r * a.lddz + col, FULL ? 8 : n, v[u]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += v[u][i];
       }
-      if (a.dz) store8(static_cast<T*>(a.dz) + (int64_t)r * a.lddz + col, n, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
     }
   }
   if (!a.db || dead) return;  // uniform over the workgroup
@@ -150,8 +183,11 @@ hipError_t launch_act_grad(const ActGradArgs& args, int dtype, hipStream_t s) {
   if (blocks * cols > 0x7fffffff || a.groups > 65535) return hipErrorInvalidValue;
   if (blocks > 0) {
     const dim3 grid((unsigned)(cols * blocks));
-    if (dtype == MUON_BF16) hipLaunchKernelGGL((k_act_grad<uint16_t>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_act_grad<float>), grid, dim3(256), 0, s, a);
+    const bool full = a.n % 8 == 0;
+    if (dtype == MUON_BF16 && full) hipLaunchKernelGGL((k_act_grad<uint16_t, true>), grid, dim3(256), 0, s, a);
+    else if (dtype == MUON_BF16) hipLaunchKernelGGL((k_act_grad<uint16_t, false>), grid, dim3(256), 0, s, a);
+    else if (full) hipLaunchKernelGGL((k_act_grad<float, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_act_grad<float, false>), grid, dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

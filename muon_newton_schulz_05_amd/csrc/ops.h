@@ -35,13 +35,15 @@ struct GemmArgs {
   int32_t tiles_m, tiles_n;
 };
 
-enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTileRows32, kTile64 };
+enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTile64, kTileRows32, kTileRows32K };
 int gemm_tile_m(int tile);
 int gemm_tile_n(int tile);
-// direct: the operands may be loaded by aligned 16-byte pieces (gemm_direct).
-hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, bool direct, int tile, hipStream_t s);
-hipError_t launch_gemm_bf16(const GemmArgs& g, bool ta, bool tb, bool direct, int tile, hipStream_t s);
-hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, bool direct, int tile, hipStream_t s);
+// How operands reach LDS: through registers (any alignment), or directly by
+// aligned pieces of 16 or of 4 bytes a lane.
+enum GemmLoads { kStaged = 0, kDirect16, kDirect4 };
+hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, int loads, int tile, hipStream_t s);
+hipError_t launch_gemm_bf16(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s);
+hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s);
 hipError_t launch_gemm_join(const GemmArgs& g, int dtype, hipStream_t s);
 
 // dz = dy act'(z) and the column sums of dz over each group's rows.

@@ -37,20 +37,29 @@ int check_desc(const muon_linear_desc_t* d) {
   return MUON_OK;
 }
 
-// An operand of a product: may it be loaded by aligned 16-byte pieces with
-// 32-bit offsets inside a tile?  rows contiguous along k: whole pieces along k;
-// contiguous along its rows (t): whole pieces along them.
-bool direct(const void* p, int64_t ld, int64_t group_stride, bool t, int64_t rows, int64_t k, int tile_rows, int es) {
-  const int64_t piece = 16 / es;
-  if (!aligned(p, 16) || ld % piece != 0 || group_stride % piece != 0) return false;
-  if ((t ? rows : k) % piece != 0) return false;
-  return ld * es * (t ? 128 / es : tile_rows) < (int64_t(1) << 31) - 4096;
+// How an operand may be loaded: directly to LDS by aligned pieces of 16 or of 4
+// bytes with 32-bit offsets inside a tile, or through registers.  rows
+// contiguous along k: whole pieces along k; contiguous along its rows (t): whole
+// pieces along them.
+int loads_of(const void* p, int64_t ld, int64_t group_stride, bool t, int64_t rows, int64_t k, int es) {
+  if (ld * es * (t ? 128 / es : 256) >= (int64_t(1) << 31) - 4096) return muon::kStaged;
+  for (int bytes : {16, 4}) {
+    const int64_t piece = std::max(1, bytes / es);
+    if (aligned(p, bytes) && ld % piece == 0 && group_stride % piece == 0 && (t ? rows : k) % piece == 0)
+      return bytes == 16 ? muon::kDirect16 : muon::kDirect4;
+  }
+  return muon::kStaged;
+}
+// Both operands of a product take the same kind.
+int both_loads(int a, int b) {
+  if (a == muon::kStaged || b == muon::kStaged) return muon::kStaged;
+  return a == muon::kDirect16 && b == muon::kDirect16 ? muon::kDirect16 : muon::kDirect4;
 }
 
 struct Product {
   muon::GemmArgs g{};
   int tile = muon::kTile128;
-  bool direct = false;
+  int loads = muon::kStaged;
   uint64_t ws = 0;
 };
 
@@ -67,11 +76,13 @@ struct Product {
 //    times over (1024^3: 25 against 47; 4096^3: 1017 against 987).
 //  - 32 x 128 for at most 32 rows (a group), where time goes to reading B, and for
 //    grouped products whose 64-tiles leave units idle ([24, 10240] experts over
-//    8192 rows, dx: 52, with 64 x 64 75, with 128 x 128 104).
+//    8192 rows, dx: 52, with 64 x 64 75, with 128 x 128 104).  Dense and at least
+//    1024 deep: 32 x 64, the contraction shared by four sets of waves, which
+//    needs no join for 8192 columns and more.
 // A dense product whose tiles do not fill the card is split along the
 // contraction, at least 512 of it each, and joined.  Grouped products are not:
 // their tiles already number at least the groups with rows.
-void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int groups) {
+void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups) {
   muon::GemmArgs& g = p->g;
   const bool gk = ta && tb, grouped = groups > 0;
   auto tiles = [&](int t) {
@@ -81,11 +92,11 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int
   };
   const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
   const bool f32 = dtype == MUON_F32;
-  p->direct = aligned_ops;
-  if (!aligned_ops) {
+  p->loads = loads;
+  if (loads != muon::kDirect16) {
     p->tile = tiles(muon::kTile128) >= (f32 ? 4 : 2) * kCus ? muon::kTile128 : muon::kTile64;
   } else if (m_each <= 32) {
-    p->tile = muon::kTileRows32;
+    p->tile = !grouped && !gk && g.k >= 1024 ? muon::kTileRows32K : muon::kTileRows32;
   } else if (!f32 && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
     p->tile = muon::kTile256;
   } else if (!f32 && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
@@ -93,7 +104,9 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int
   } else if (tiles(muon::kTile128) >= (f32 ? 4 * kCus : kCus / 2)) {
     p->tile = muon::kTile128;
   } else {
-    p->tile = grouped && !gk && tiles(muon::kTile64) < kCus ? muon::kTileRows32 : muon::kTile64;
+    p->tile = !(grouped && !gk && tiles(muon::kTile64) < kCus) ? muon::kTile64
+              : g.n <= 64 && g.k >= 1024                        ? muon::kTileRows32K
+                                                                : muon::kTileRows32;
   }
   const int64_t bm = muon::gemm_tile_m(p->tile), bn = muon::gemm_tile_n(p->tile);
   g.tiles_m = (int32_t)(gk ? (g.m + bm - 1) / bm : muon::group_blocks(g.m, groups, grouped, bm));
@@ -102,8 +115,9 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, bool aligned_ops, int
   g.splits = 1;
   g.k_per = g.k;
   const int64_t t = tiles(p->tile);
-  if (!grouped && t > 0 && t < kCus && g.k >= 1024) {
-    int64_t s = std::min<int64_t>((2 * kCus + t - 1) / t, g.k / 512);
+  if (!grouped && t > 0 && t < (p->tile == muon::kTileRows32K ? kCus / 2 : kCus) && g.k >= 1024) {
+    const int64_t want = p->tile == muon::kTileRows32K ? kCus : 2 * kCus;
+    int64_t s = std::min<int64_t>((want + t - 1) / t, g.k / 512);
     s = std::min<int64_t>(s, 64);
     if (s > 1) {
       g.k_per = ((g.k + s - 1) / s + 63) / 64 * 64;
@@ -122,12 +136,12 @@ int run_product(Product* p, int dtype, bool ta, bool tb, void* ws, uint64_t ws_b
     if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
     g.part = static_cast<float*>(ws);
   }
-  hipError_t e = muon::launch_gemm(g, dtype, ta, tb, p->direct, p->tile, s);
+  hipError_t e = muon::launch_gemm(g, dtype, ta, tb, p->loads, p->tile, s);
   if (e == hipSuccess && g.splits > 1) e = muon::launch_gemm_join(g, dtype, s);
   return hip_result(e, what);
 }
 
-// The three products of a layer as C = A B^T; `ops_aligned` decides the loads.
+// The three products of a layer as C = A B^T; with what their operands' alignment allows.
 Product forward_product(const muon_linear_desc_t* d, const void* x, const void* w, bool* tb) {
   Product p;
   p.g.a = x;
@@ -140,8 +154,8 @@ Product forward_product(const muon_linear_desc_t* d, const void* x, const void* 
   p.g.k = d->k;
   *tb = d->w_layout == 0;
   const int es = elem(d->dtype);
-  const bool ok = direct(x, d->ldx, 0, false, d->rows, d->k, 256, es) &&
-                  direct(w, d->ldw, p.g.sb, *tb, d->n, d->k, 256, es);
+  const int ok = both_loads(loads_of(x, d->ldx, 0, false, d->rows, d->k, es),
+                            loads_of(w, d->ldw, p.g.sb, *tb, d->n, d->k, es));
   plan_product(&p, d->dtype, false, *tb, ok, d->groups);
   return p;
 }
@@ -157,8 +171,8 @@ Product input_product(const muon_linear_desc_t* d, const void* dz, const void* w
   p.g.k = d->n;
   *tb = d->w_layout == 1;
   const int es = elem(d->dtype);
-  const bool ok = direct(dz, d->ldg, 0, false, d->rows, d->n, 256, es) &&
-                  direct(w, d->ldw, p.g.sb, *tb, d->k, d->n, 256, es);
+  const int ok = both_loads(loads_of(dz, d->ldg, 0, false, d->rows, d->n, es),
+                            loads_of(w, d->ldw, p.g.sb, *tb, d->k, d->n, es));
   plan_product(&p, d->dtype, false, *tb, ok, d->groups);
   return p;
 }
@@ -174,8 +188,8 @@ Product weight_product(const muon_linear_desc_t* d, const void* x, const void* d
   p.g.k = d->rows;
   p.g.sc = p.g.m * p.g.n;
   const int es = elem(d->dtype);
-  const bool ok = direct(p.g.a, p.g.lda, 0, true, p.g.m, p.g.k, 256, es) &&
-                  direct(p.g.b, p.g.ldb, 0, true, p.g.n, p.g.k, 256, es);
+  const int ok = both_loads(loads_of(p.g.a, p.g.lda, 0, true, p.g.m, p.g.k, es),
+                            loads_of(p.g.b, p.g.ldb, 0, true, p.g.n, p.g.k, es));
   plan_product(&p, d->dtype, true, true, ok, d->groups);
   return p;
 }
@@ -190,6 +204,10 @@ int check_ptr(const muon_linear_desc_t* d, const void* p, int64_t count, const c
   if (count > 0 && !p) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is null", name);
   if (!aligned(p, elem(d->dtype))) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", name);
   return MUON_OK;
+}
+// dz of a layer with an activation, as part of a workspace.
+uint64_t dz_bytes(const muon_linear_desc_t* d) {
+  return d->act == MUON_ACT_NONE ? 0 : ((uint64_t)d->rows * d->n * elem(d->dtype) + 15) / 16 * 16;
 }
 #define MUON_TRY(x)                   \
   do {                                \
@@ -240,9 +258,24 @@ int muon_linear_workspace(const muon_linear_desc_t* d, int32_t op, uint64_t* byt
     *bytes = (uint64_t)muon::act_grad_blocks(d->rows, d->n, std::max(d->groups, 1), d->groups > 0) * d->n * 4;
     return set_error(MUON_OK, "%s", "");
   }
+  if (op == MUON_LINEAR_BACKWARD) {
+    // dz, then one area that the three steps use in turn.
+    uint64_t most = 0, b = 0;
+    muon_linear_desc_t dd = *d;
+    for (int32_t step : {MUON_LINEAR_GRAD_ACT, MUON_LINEAR_GRAD_INPUT, MUON_LINEAR_GRAD_WEIGHT}) {
+      for (int64_t ld : {d->ldg, d->n}) {
+        dd.ldg = ld;
+        MUON_TRY(muon_linear_workspace(&dd, step, &b));
+        most = std::max(most, b);
+      }
+    }
+    *bytes = dz_bytes(d) + most;
+    return set_error(MUON_OK, "%s", "");
+  }
   if (op < 0 || op > MUON_LINEAR_GRAD_WEIGHT) return bad("unknown operation");
-  // The plan depends on the pointers' alignment: the larger of both answers.
-  const void* probes[2] = {nullptr, reinterpret_cast<const void*>(uintptr_t(8))};
+  // The plan depends on the pointers' alignment: the largest of the answers.
+  const void* probes[3] = {nullptr, reinterpret_cast<const void*>(uintptr_t(4)),
+                           reinterpret_cast<const void*>(uintptr_t(2))};
   for (const void* q : probes) {
     bool tb;
     const Product p = op == MUON_LINEAR_FORWARD      ? forward_product(d, q, q, &tb)
@@ -337,6 +370,27 @@ int muon_linear_grad_weight(const muon_linear_desc_t* d, const int32_t* offsets,
   p.g.c = dw;
   p.g.ldc = p.g.n;
   return run_product(&p, d->dtype, true, true, ws, ws_bytes, stream, "muon_linear_grad_weight");
+}
+
+int muon_linear_backward(const muon_linear_desc_t* d, const int32_t* offsets, const void* x, const void* w,
+                         const void* z, const void* dy, void* dx, void* dw, void* db, void* ws, uint64_t ws_bytes,
+                         void* stream) {
+  MUON_TRY(check_desc(d));
+  const uint64_t dzb = (dx || dw) ? dz_bytes(d) : 0;
+  if (dzb > ws_bytes || (dzb && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
+  if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
+  char* rest = static_cast<char*>(ws) + (ws ? dzb : 0);
+  muon_linear_desc_t dd = *d;
+  const void* dz = dy;
+  if (dzb || db)
+    MUON_TRY(muon_linear_grad_act(d, offsets, dy, z, dzb ? ws : nullptr, db, rest, ws_bytes - dzb, stream));
+  if (dzb) {
+    dz = ws;
+    dd.ldg = d->n;
+  }
+  if (dx) MUON_TRY(muon_linear_grad_input(&dd, offsets, dz, w, dx, rest, ws_bytes - dzb, stream));
+  if (dw) MUON_TRY(muon_linear_grad_weight(&dd, offsets, x, dz, dw, rest, ws_bytes - dzb, stream));
+  return set_error(MUON_OK, "%s", "");
 }
 
 int muon_route_workspace(int64_t entries, int32_t experts, uint64_t* bytes) {

@@ -199,17 +199,15 @@ constexpr int kCols = 512;  // columns of one wave's piece, 8 a lane
 
 struct Piece {
   int64_t token, col;
-  int n;   // columns of this lane inside the row
-  bool in;
+  int n;  // this lane's columns inside the row (8 where FULL: h is a multiple of 8)
 };
-__device__ __forceinline__ Piece my_piece(const MoveArgs& a) {
+template <bool FULL>
+__device__ __forceinline__ bool my_piece(const MoveArgs& a, Piece& p) {
   const int64_t per = (a.h + kCols - 1) / kCols, u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  Piece p;
   p.token = u / per;
   p.col = (u - p.token * per) * kCols + (threadIdx.x & 63) * 8;
-  p.in = p.token < a.tokens && p.col < a.h;
-  p.n = (int)min((int64_t)8, a.h - p.col);
-  return p;
+  p.n = FULL ? 8 : (int)min((int64_t)8, a.h - p.col);
+  return p.token < a.tokens && p.col < a.h;
 }
 __device__ __forceinline__ int routed_rows(const MoveArgs& a) {
   return (int)min(max((int64_t)a.offsets[a.experts], (int64_t)0), a.tokens * a.top);
@@ -220,17 +218,17 @@ __device__ __forceinline__ int64_t row_at(const MoveArgs& a, int64_t t, int j) {
   return p >= 0 && p < a.tokens * a.top ? p : -1;
 }
 
-template <typename T>
+template <typename T, bool FULL, bool NT>
 __global__ __launch_bounds__(256) void k_dispatch(MoveArgs a) {
-  const Piece p = my_piece(a);
-  if (!p.in) return;
+  Piece p;
+  if (!my_piece<FULL>(a, p)) return;
   float v[8];
   load8(static_cast<const T*>(a.x) + p.token * a.ldx + p.col, p.n, v);
   const int all = routed_rows(a);
   T* out = static_cast<T*>(a.out);
   for (int j = 0; j < a.top; ++j) {
     const int64_t r = row_at(a, p.token, j);
-    if (r >= 0) store8(out + r * a.h + p.col, p.n, v);
+    if (r >= 0) store8<T, NT>(out + r * a.h + p.col, p.n, v);
   }
   const float zero[8] = {};
   for (int j = 0; j < a.top; ++j) {
@@ -239,13 +237,13 @@ __global__ __launch_bounds__(256) void k_dispatch(MoveArgs a) {
   }
 }
 
-// out[t] = sum_j w[t][j] x[position[t][j]] (+ res); w null: all ones.
-template <typename T>
+// out[t] = sum_j w[t][j] x[position[t][j]] (+ res); w null: all ones.  U rows are
+// in flight at once.
+template <typename T, int U, bool FULL, bool NT>
 __global__ __launch_bounds__(256) void k_gather_sum(MoveArgs a) {
-  const Piece p = my_piece(a);
-  if (!p.in) return;
+  Piece p;
+  if (!my_piece<FULL>(a, p)) return;
   float sum[8] = {};
-  constexpr int U = 4;  // rows in flight
   for (int j0 = 0; j0 < a.top; j0 += U) {
     float v[U][8], w[U];
     int64_t r[U];
@@ -254,15 +252,15 @@ __global__ __launch_bounds__(256) void k_gather_sum(MoveArgs a) {
       r[u] = j0 + u < a.top ? row_at(a, p.token, j0 + u) : -1;
       w[u] = a.w && j0 + u < a.top ? a.w[p.token * a.top + j0 + u] : 1.f;
     }
+    // Unguarded, so that the loads are in flight together: a row that is not
+    // there is read from row 0 and not used.
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (r[u] >= 0) load8(static_cast<const T*>(a.x) + r[u] * a.ldx + p.col, p.n, v[u]);
+      load8<T, NT>(static_cast<const T*>(a.x) + max(r[u], (int64_t)0) * a.ldx + p.col, p.n, v[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (r[u] >= 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += w[u] * v[u][i];
-      }
+      for (int i = 0; i < 8; ++i) sum[i] += r[u] >= 0 ? w[u] * v[u][i] : 0.f;
   }
   if (a.res) {
     float v[8];
@@ -276,13 +274,12 @@ __global__ __launch_bounds__(256) void k_gather_sum(MoveArgs a) {
 // One wave a token: dys[position[t][j]] = w[t][j] dy[t] and
 // dw[t][j] = <dy[t], ys[position[t][j]]>, both from one reading of dy; rows of
 // dys past the routed ones are zero.
-template <typename T>
+template <typename T, int U, bool FULL, bool NT>
 __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (t >= a.tokens) return;
   const int all = routed_rows(a);
-  constexpr int U = 4;
   T* out = static_cast<T*>(a.out);
   for (int j0 = 0; j0 < a.top; j0 += U) {
     int64_t r[U];
@@ -293,19 +290,16 @@ __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
       w[u] = j0 + u < a.top ? a.w[t * a.top + j0 + u] : 0.f;
     }
     for (int64_t c = lane * 8; c < a.h; c += kCols) {
-      const int n = (int)min((int64_t)8, a.h - c);
+      const int n = FULL ? 8 : (int)min((int64_t)8, a.h - c);
       float d[8], v[U][8];
       load8(static_cast<const T*>(a.g) + t * a.ldg + c, n, d);
       if (a.dw) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (r[u] >= 0) load8(static_cast<const T*>(a.x) + r[u] * a.ldx + c, n, v[u]);
+        for (int u = 0; u < U; ++u) load8<T, NT>(static_cast<const T*>(a.x) + max(r[u], (int64_t)0) * a.ldx + c, n, v[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (r[u] >= 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot[u] += d[i] * v[u][i];
-          }
+          for (int i = 0; i < 8; ++i) dot[u] += r[u] >= 0 ? d[i] * v[u][i] : 0.f;
       }
       if (out) {
 #pragma unroll
@@ -314,7 +308,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = w[u] * d[i];
-            store8(out + r[u] * a.h + c, n, o);
+            store8<T, NT>(out + r[u] * a.h + c, n, o);
           }
       }
     }
@@ -331,7 +325,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(MoveArgs a) {
   for (int j = 0; j < a.top; ++j) {
     const int64_t r = t * a.top + j;
     if (r < all) continue;
-    for (int64_t c = lane * 8; c < a.h; c += kCols) store8(out + r * a.h + c, (int)min((int64_t)8, a.h - c), zero);
+    for (int64_t c = lane * 8; c < a.h; c += kCols) store8(out + r * a.h + c, FULL ? 8 : (int)min((int64_t)8, a.h - c), zero);
   }
 }
 
@@ -361,22 +355,70 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+namespace {
+
+// Sorted rows past the memory-side cache's 256 MB are streamed (non-temporal):
+// kept in it, their write-back takes the next kernel's bandwidth.  16384 tokens
+// x 8 at h = 2048, bf16 (512 MiB of sorted rows): dispatch, combine and both
+// gradients 611 us against 647.  Smaller tensors stay for their reader.
+template <typename T>
+bool streams(const MoveArgs& a) {
+  return a.tokens * a.top * a.h * (int64_t)sizeof(T) > (int64_t(256) << 20);
+}
+
+template <typename T, bool FULL>
+void move_rows(const MoveArgs& a, unsigned blocks, hipStream_t s) {
+  if (streams<T>(a)) hipLaunchKernelGGL((k_dispatch<T, FULL, true>), dim3(blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_dispatch<T, FULL, false>), dim3(blocks), dim3(256), 0, s, a);
+}
+// Four rows in flight, eight where there are more than four choices (16384
+// tokens x 8: combine's gradient 226 us against 237; with three choices four are
+// faster, 28 against 34, the others being read for nothing).
+template <typename T, int U, bool FULL>
+void gather(const MoveArgs& a, unsigned blocks, hipStream_t s) {
+  if (streams<T>(a)) hipLaunchKernelGGL((k_gather_sum<T, U, FULL, true>), dim3(blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_gather_sum<T, U, FULL, false>), dim3(blocks), dim3(256), 0, s, a);
+}
+template <typename T, int U, bool FULL>
+void combine_grad(const MoveArgs& a, unsigned blocks, hipStream_t s) {
+  if (streams<T>(a)) hipLaunchKernelGGL((k_combine_grad<T, U, FULL, true>), dim3(blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_combine_grad<T, U, FULL, false>), dim3(blocks), dim3(256), 0, s, a);
+}
+template <typename T>
+void pick_gather(const MoveArgs& a, unsigned b, hipStream_t s) {
+  const bool wide = a.top > 4, full = a.h % 8 == 0;
+  if (wide) full ? gather<T, 8, true>(a, b, s) : gather<T, 8, false>(a, b, s);
+  else full ? gather<T, 4, true>(a, b, s) : gather<T, 4, false>(a, b, s);
+}
+template <typename T>
+void pick_combine_grad(const MoveArgs& a, unsigned b, hipStream_t s) {
+  const bool wide = a.top > 4, full = a.h % 8 == 0;
+  if (wide) full ? combine_grad<T, 8, true>(a, b, s) : combine_grad<T, 8, false>(a, b, s);
+  else full ? combine_grad<T, 4, true>(a, b, s) : combine_grad<T, 4, false>(a, b, s);
+}
+int64_t pieces(const MoveArgs& a) { return a.tokens * ((a.h + kCols - 1) / kCols); }
+
+}  // namespace
+
 hipError_t launch_dispatch(const MoveArgs& a, int dtype, hipStream_t s) {
-  return launch_units(a.tokens * ((a.h + kCols - 1) / kCols), [&](unsigned b) {
-    if (dtype == MUON_BF16) hipLaunchKernelGGL((k_dispatch<uint16_t>), dim3(b), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_dispatch<float>), dim3(b), dim3(256), 0, s, a);
+  return launch_units(pieces(a), [&](unsigned b) {
+    const bool full = a.h % 8 == 0;
+    if (dtype == MUON_BF16) full ? move_rows<uint16_t, true>(a, b, s) : move_rows<uint16_t, false>(a, b, s);
+    else full ? move_rows<float, true>(a, b, s) : move_rows<float, false>(a, b, s);
   });
 }
+
 hipError_t launch_gather_sum(const MoveArgs& a, int dtype, hipStream_t s) {
-  return launch_units(a.tokens * ((a.h + kCols - 1) / kCols), [&](unsigned b) {
-    if (dtype == MUON_BF16) hipLaunchKernelGGL((k_gather_sum<uint16_t>), dim3(b), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_gather_sum<float>), dim3(b), dim3(256), 0, s, a);
+  return launch_units(pieces(a), [&](unsigned b) {
+    if (dtype == MUON_BF16) pick_gather<uint16_t>(a, b, s);
+    else pick_gather<float>(a, b, s);
   });
 }
+
 hipError_t launch_combine_grad(const MoveArgs& a, int dtype, hipStream_t s) {
   return launch_units(a.tokens, [&](unsigned b) {
-    if (dtype == MUON_BF16) hipLaunchKernelGGL((k_combine_grad<uint16_t>), dim3(b), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_combine_grad<float>), dim3(b), dim3(256), 0, s, a);
+    if (dtype == MUON_BF16) pick_combine_grad<uint16_t>(a, b, s);
+    else pick_combine_grad<float>(a, b, s);
   });
 }
 

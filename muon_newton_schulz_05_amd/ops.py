@@ -29,10 +29,10 @@ from .binding import MUON_BF16, MUON_F32, MUON_OK, MuonError, load_library, muon
 MUON_ROUTE_MAX_EXPERTS = 1024
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 EXPORTED_OPS = ("muon_linear_workspace", "muon_linear_forward", "muon_linear_grad_act", "muon_linear_grad_input",
-                "muon_linear_grad_weight", "muon_route_workspace", "muon_route", "muon_dispatch",
+                "muon_linear_grad_weight", "muon_linear_backward", "muon_route_workspace", "muon_route", "muon_dispatch",
                 "muon_dispatch_grad", "muon_combine", "muon_combine_grad", "muon_dropout")
 
-_FORWARD, _GRAD_ACT, _GRAD_INPUT, _GRAD_WEIGHT = range(4)
+_FORWARD, _BACKWARD = 0, 4
 
 
 class LinearDesc(ctypes.Structure):
@@ -65,6 +65,7 @@ def load_ops():
         "muon_linear_grad_act": [D, P, P, P, P, P, P, U64, P],
         "muon_linear_grad_input": [D, P, P, P, P, P, U64, P],
         "muon_linear_grad_weight": [D, P, P, P, P, P, U64, P],
+        "muon_linear_backward": [D, P, P, P, P, P, P, P, P, P, U64, P],
         "muon_route_workspace": [I64, I32, UP],
         "muon_route": [P, I32, I64, I32, I32, P, P, P, P, U64, P],
         "muon_dispatch": [M, P, P, P, P, P],
@@ -251,32 +252,16 @@ def _forward(x, w, bias, residual, offsets, act, keep_z):
 
 def _backward(dy, x, w, z, offsets, act, need_x, need_w, need_b):
     p = _plan(x, w, act, offsets is not None)
-    dz, ld, off = dy, _ld(dy), _ptr(offsets)
-    dx = dw = db = None
-    store = act != 0 and (need_x or need_w)
-    if store or need_b:
-        d, size = p.get(_GRAD_ACT, ld)
-        if store:
-            dz = torch.empty(p.y_shape, dtype=x.dtype, device=x.device)
-        if need_b:
-            db = torch.empty((p.groups, p.n) if p.groups else (p.n,), dtype=x.dtype, device=x.device)
-        ws = _workspace(size, x) if need_b else None
-        _call("muon_linear_grad_act", x, d, off, dy.data_ptr(), _ptr(z), dz.data_ptr() if store else None, _ptr(db),
-              _ptr(ws), size)
-        if store:
-            ld = max(p.n, 1)
-    if need_x:
-        d, size = p.get(_GRAD_INPUT, ld)
-        dx = torch.empty((p.rows, p.k), dtype=x.dtype, device=x.device)
-        ws = _workspace(size, x)
-        _call("muon_linear_grad_input", x, d, off, dz.data_ptr(), w.data_ptr(), dx.data_ptr(), _ptr(ws), size)
-    if need_w:
-        d, size = p.get(_GRAD_WEIGHT, ld)
-        dw = torch.empty(p.dw_shape, dtype=x.dtype, device=x.device)
-        ws = _workspace(size, x)
-        _call("muon_linear_grad_weight", x, d, off, x.data_ptr(), dz.data_ptr(), dw.data_ptr(), _ptr(ws), size)
-        if p.layout == 1:
-            dw = dw.transpose(-1, -2)
+    d, size = p.get(_BACKWARD, _ld(dy))
+    like = {"dtype": x.dtype, "device": x.device}
+    dx = torch.empty((p.rows, p.k), **like) if need_x else None
+    dw = torch.empty(p.dw_shape, **like) if need_w else None
+    db = torch.empty((p.groups, p.n) if p.groups else (p.n,), **like) if need_b else None
+    ws = _workspace(size, x)
+    _call("muon_linear_backward", x, d, _ptr(offsets), x.data_ptr(), w.data_ptr(), _ptr(z), dy.data_ptr(), _ptr(dx),
+          _ptr(dw), _ptr(db), _ptr(ws), size)
+    if dw is not None and p.layout == 1:
+        dw = dw.transpose(-1, -2)
     return dx, dw, db
 
 
