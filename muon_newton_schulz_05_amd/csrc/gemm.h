@@ -262,7 +262,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   typedef Panel<T, BN, TB, NW, LOADS, PD> PB;
   typedef typename Mma<T>::Frag Frag;
   constexpr int BK = PA::BK, SUB = KB / 64, STAGE = PA::BYTES + PB::BYTES;
-  constexpr int STRIDE = WN * 4 + 16;  // bytes of a staged epilogue row: rows 4 apart fall on distinct bank quarters
+  constexpr int STRIDE = WN * 4 + 16;  // bytes of a staged epilogue row: 16 rows at one column fall on distinct 16-byte bank groups
   constexpr int LDS = WGK * (NS * STAGE > NW * 32 * STRIDE ? NS * STAGE : NW * 32 * STRIDE);
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
 
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(af[s & 1][i], bf[s & 1][j], acc[i][j], q);
+        for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(bf[s & 1][j], af[s & 1][i], acc[i][j], q);
   };
 
   if constexpr (DIRECT) {
@@ -436,8 +436,9 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   __syncthreads();  // every wave is done with the operand stages
 
   // ---- epilogue: 32 rows at a time through this wave's own staging, so that
-  // a row of C leaves as whole 16-byte pieces.  Register u of a block is row
-  // 4 (lane / 16) + u, column lane mod 16.
+  // a row of C leaves as whole 16-byte pieces.  The products are of B by A, so a
+  // block's register u in a lane is row lane mod 16 and column 4 (lane / 16) + u:
+  // four columns of a row, one 16-byte write.
   constexpr int LPR = WN / 8, RPP = 64 / LPR;
   char* stg = lds + wave_all * 32 * STRIDE;
   const int col = tn * BN + wn * WN + 8 * (lane % LPR);
@@ -456,12 +457,9 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
       for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int lr = 16 * ii + 4 * (lane >> 4) + u;
-            *reinterpret_cast<float*>(stg + lr * STRIDE + (16 * j + (lane & 15)) * 4) = acc[2 * i + ii][j][u];
-          }
-      if constexpr (WGK > 1) __syncthreads();
+          *reinterpret_cast<f32x4_t*>(stg + (16 * ii + (lane & 15)) * STRIDE + (16 * j + 4 * (lane >> 4)) * 4) =
+              acc[2 * i + ii][j];
+    if constexpr (WGK > 1) __syncthreads();
       else wave_fence();
       // One wave reads its strip back; with several sets, each set takes its share
       // of the 32 rows and adds the sets' values in order.

@@ -7,14 +7,17 @@ namespace muon {
 hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s) {
   if (loads == kDirect4) {
     if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 1, 4, kDirect4>(g, ta, tb, s);
+    if (tile == kTile32x64) return launch_tile<float, 32, 64, 1, 4, 1, 4, kDirect4>(g, ta, tb, s);
     return launch_tile<float, 128, 128, 2, 2, 1, 2, kDirect4>(g, ta, tb, s);
   }
   if (loads == kStaged) {
     if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
+    if (tile == kTile32x64) return launch_tile<float, 32, 64, 1, 4, 1, 2, kStaged>(g, ta, tb, s);
     return launch_tile<float, 128, 128, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
   }
   switch (tile) {
     case kTile64: return launch_tile<float, 64, 64, 2, 2, 1, 4, kDirect16>(g, ta, tb, s);
+    case kTile32x64: return launch_tile<float, 32, 64, 1, 4, 1, 4, kDirect16>(g, ta, tb, s);
     case kTileRows32: return launch_tile<float, 32, 128, 1, 4, 1, 4, kDirect16>(g, ta, tb, s);
     case kTileRows32K: return launch_tile<float, 32, 64, 1, 2, 4, 3, kDirect16>(g, ta, tb, s);
     default: return launch_tile<float, 128, 128, 2, 2, 1, 2, kDirect16>(g, ta, tb, s);
@@ -26,6 +29,7 @@ int gemm_tile_m(int tile) {
     case kTile256:
     case kTile256x128: return 256;
     case kTile64: return 64;
+    case kTile32x64:
     case kTileRows32:
     case kTileRows32K: return 32;
     default: return 128;
@@ -35,6 +39,7 @@ int gemm_tile_n(int tile) {
   switch (tile) {
     case kTile256: return 256;
     case kTile64:
+    case kTile32x64:
     case kTileRows32K: return 64;
     default: return 128;
   }

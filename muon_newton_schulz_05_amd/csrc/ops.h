@@ -35,7 +35,7 @@ struct GemmArgs {
   int32_t tiles_m, tiles_n;
 };
 
-enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTile64, kTileRows32, kTileRows32K };
+enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTile64, kTile32x64, kTileRows32, kTileRows32K };
 int gemm_tile_m(int tile);
 int gemm_tile_n(int tile);
 // How operands reach LDS: through registers (any alignment), or directly by

@@ -68,12 +68,16 @@ struct Product {
 //  - 256 x 256 has the best rate (1400 TFLOP/s at 8192^3) once every unit has a
 //    tile: 4096^3 takes 110 / 105 / 106, with 256 x 128 120 / 120 / 131, with
 //    128 x 128 132 / 148 / 140.
+//    A contraction of one slice is all prologue and epilogue, and takes
+//    128 x 128, two of which share a unit ([24, 10240] experts over 8192 rows,
+//    forward: 96 against 109).
 //  - 256 x 128 where only it fills the card: 2048 x 16384 x 4096 forward 224, with
 //    128 x 128 256, with 256 x 256 split four ways 248.
 //  - 128 x 128 down to half a card of tiles (2048^3: 30 / 31 / 29, with 256 x 128
 //    50), then 64 x 64.  float32 products are bound by their lower matrix rate,
 //    not by operand traffic, and take 64 x 64 until 128 x 128 fills the card four
-//    times over (1024^3: 25 against 47; 4096^3: 1017 against 987).
+//    times over (1024^3: 25 against 47; 4096^3: 1017 against 987), and 32 x 64
+//    while 64 x 64 fills it at most twice (777 x 1001 x 1343: 39 against 47).
 //  - 32 x 128 for at most 32 rows (a group), where time goes to reading B, and for
 //    grouped products whose 64-tiles leave units idle ([24, 10240] experts over
 //    8192 rows, dx: 52, with 64 x 64 75, with 128 x 128 104).  Dense and at least
@@ -91,15 +95,15 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
     return tm * ((g.n + bn - 1) / bn) * (gk && grouped ? groups : 1);
   };
   const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
-  const bool f32 = dtype == MUON_F32;
+  const bool f32 = dtype == MUON_F32, wide = !f32 && g.k > 64;
   p->loads = loads;
   if (loads != muon::kDirect16) {
     p->tile = tiles(muon::kTile128) >= (f32 ? 4 : 2) * kCus ? muon::kTile128 : muon::kTile64;
   } else if (m_each <= 32) {
     p->tile = !grouped && !gk && g.k >= 1024 ? muon::kTileRows32K : muon::kTileRows32;
-  } else if (!f32 && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
+  } else if (wide && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
     p->tile = muon::kTile256;
-  } else if (!f32 && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
+  } else if (wide && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
     p->tile = muon::kTile256x128;
   } else if (tiles(muon::kTile128) >= (f32 ? 4 * kCus : kCus / 2)) {
     p->tile = muon::kTile128;
@@ -108,6 +112,7 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
               : g.n <= 64 && g.k >= 1024                        ? muon::kTileRows32K
                                                                 : muon::kTileRows32;
   }
+  if (f32 && p->tile == muon::kTile64 && tiles(muon::kTile64) <= 2 * kCus) p->tile = muon::kTile32x64;
   const int64_t bm = muon::gemm_tile_m(p->tile), bn = muon::gemm_tile_n(p->tile);
   g.tiles_m = (int32_t)(gk ? (g.m + bm - 1) / bm : muon::group_blocks(g.m, groups, grouped, bm));
   g.tiles_n = (int32_t)((g.n + bn - 1) / bn);
@@ -115,9 +120,9 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   g.splits = 1;
   g.k_per = g.k;
   const int64_t t = tiles(p->tile);
-  if (!grouped && t > 0 && t < (p->tile == muon::kTileRows32K ? kCus / 2 : kCus) && g.k >= 1024) {
-    const int64_t want = p->tile == muon::kTileRows32K ? kCus : 2 * kCus;
-    int64_t s = std::min<int64_t>((want + t - 1) / t, g.k / 512);
+  const bool sets = p->tile == muon::kTileRows32K;
+  if (!grouped && t > 0 && t < (sets ? kCus / 2 : kCus) && g.k >= 1024) {
+    int64_t s = std::min<int64_t>(((sets ? kCus : 2 * kCus) + t - 1) / t, g.k / 512);
     s = std::min<int64_t>(s, 64);
     if (s > 1) {
       g.k_per = ((g.k + s - 1) / s + 63) / 64 * 64;
