@@ -1,4 +1,4 @@
-// act.h -- activations, their derivatives, and the finding of a row block's group.
+// act.h -- activations, their derivatives, and the blocks of grouped rows.
 #pragma once
 #include "device_common.h"
 #include "ops.h"
@@ -74,51 +74,60 @@ __device__ __forceinline__ void group_range(const int32_t* offsets, int groups, 
   hi = e == groups ? r : max(lo, min(offsets[e + 1], r));
 }
 
-// The group of row block `mt` when every group's rows are cut into blocks of
-// BM: each lane counts its share of the groups' blocks, a wave-wide prefix
-// sum finds the lane whose share holds mt.  Results are uniform over the
-// wave.  False: there are fewer blocks.
-__device__ __forceinline__ bool find_group(const int32_t* offsets, int groups, int64_t rows, int BM, int mt, int& e,
-                                           int& row0, int& end) {
-  const int lane = threadIdx.x & 63;
-  const int per = (groups + 64) / 64;  // groups + 1 ranges over 64 lanes
-  const int e0 = lane * per, e1 = min(e0 + per, groups + 1);
-  int cnt = 0;
-  for (int i = e0; i < e1; ++i) {
-    int lo, hi;
-    group_range(offsets, groups, rows, i, lo, hi);
-    cnt += (hi - lo + BM - 1) / BM;
-  }
-  int incl = cnt;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += v;
-  }
-  int left = mt - (incl - cnt);  // blocks of this lane's share ahead of mt
-  const uint64_t hit = __ballot(left >= 0 && left < cnt);
-  if (hit == 0) return false;
-  int fe = 0, f0 = 0, f1 = 0;
-  if (left >= 0 && left < cnt) {
+// Every group's rows cut into blocks of `block`: each lane counts its share of the
+// groups' blocks, and a wave-wide prefix sum places the shares.  Results are
+// uniform over the wave.
+struct GroupBlocks {
+  int e0, e1;         // this lane's groups
+  int before, count;  // blocks ahead of them, and theirs
+  int total;
+
+  __device__ __forceinline__ GroupBlocks(const int32_t* offsets, int groups, int64_t rows, int block) {
+    const int lane = threadIdx.x & 63, per = (groups + 64) / 64;  // groups + 1 ranges over 64 lanes
+    e0 = lane * per;
+    e1 = min(e0 + per, groups + 1);
+    count = 0;
     for (int i = e0; i < e1; ++i) {
       int lo, hi;
       group_range(offsets, groups, rows, i, lo, hi);
-      const int c = (hi - lo + BM - 1) / BM;
-      if (left < c) {
-        fe = i;
-        f0 = lo + left * BM;
-        f1 = hi;
-        break;
-      }
-      left -= c;
+      count += (hi - lo + block - 1) / block;
     }
+    int incl = count;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += v;
+    }
+    before = incl - count;
+    total = __builtin_amdgcn_readlane(incl, 63);
   }
-  const int src = __builtin_ctzll(hit);
-  e = __builtin_amdgcn_readlane(fe, src);
-  row0 = __builtin_amdgcn_readlane(f0, src);
-  end = __builtin_amdgcn_readlane(f1, src);
-  return true;
-}
+
+  // The group e of block b (0 <= b < total), its first row and its group's end.
+  __device__ __forceinline__ void find(const int32_t* offsets, int groups, int64_t rows, int block, int b, int& e,
+                                       int& row0, int& end) const {
+    int left = b - before, fe = 0, f0 = 0, f1 = 0;
+    const bool mine = left >= 0 && left < count;
+    const uint64_t hit = __ballot(mine);
+    if (mine) {
+      for (int i = e0; i < e1; ++i) {
+        int lo, hi;
+        group_range(offsets, groups, rows, i, lo, hi);
+        const int c = (hi - lo + block - 1) / block;
+        if (left < c) {
+          fe = i;
+          f0 = lo + left * block;
+          f1 = hi;
+          break;
+        }
+        left -= c;
+      }
+    }
+    const int src = __builtin_ctzll(hit);
+    e = __builtin_amdgcn_readlane(fe, src);
+    row0 = __builtin_amdgcn_readlane(f0, src);
+    end = __builtin_amdgcn_readlane(f1, src);
+  }
+};
 
 // Eight consecutive elements as float32, n of them inside the row (the others
 // are zero).  Whole groups move as 16-byte accesses at any alignment of

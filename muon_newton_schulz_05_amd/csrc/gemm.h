@@ -281,28 +281,33 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   constexpr bool GK = TA && TB;  // groups divide the contraction
   const int tiles = g.tiles_m * g.tiles_n;
   int b = blockIdx.x, split = 0, e = 0, tm, tn;
-  if (g.splits > 1) {
-    split = b / tiles;
-    b -= split * tiles;
-  }
-  if (GK && g.offsets) {
-    e = b / tiles;
-    b -= e * tiles;
-  }
-  stripe(xcd_place(b, tiles), g.tiles_m, g.tiles_n, tm, tn);
-  int64_t row0 = (int64_t)tm * BM, end = g.m, k0 = 0, k1 = g.k;
-  if (g.offsets) {
+  int64_t row0, end = g.m, k0 = 0, k1 = g.k;
+  if (!GK && g.offsets) {
+    // The grid is an upper bound: what the groups really fill is counted here, so
+    // that every XCD gets its share of it.
+    const GroupBlocks gb(g.offsets, g.groups, g.m, BM);
+    if (b >= gb.total * g.tiles_n) return;  // uniform, before any barrier
+    stripe(xcd_place(b, gb.total * g.tiles_n), gb.total, g.tiles_n, tm, tn);
     int lo, hi;
-    if (GK) {
+    gb.find(g.offsets, g.groups, g.m, BM, tm, e, lo, hi);
+    row0 = lo;
+    end = hi;
+    if (e == g.groups) k1 = 0;  // rows past the last group: zeros
+  } else {
+    if (g.splits > 1) {
+      split = b / tiles;
+      b -= split * tiles;
+    }
+    if (GK && g.offsets) {
+      e = b / tiles;
+      b -= e * tiles;
+      int lo, hi;
       group_range(g.offsets, g.groups, g.k, e, lo, hi);
       k0 = lo;
       k1 = hi;
-    } else {
-      if (!find_group(g.offsets, g.groups, g.m, BM, tm, e, lo, hi)) return;  // uniform, before any barrier
-      row0 = lo;
-      end = hi;
-      if (e == g.groups) k1 = 0;  // rows past the last group: zeros
     }
+    stripe(xcd_place(b, tiles), g.tiles_m, g.tiles_n, tm, tn);
+    row0 = (int64_t)tm * BM;
   }
   if (g.splits > 1) {
     k0 = (int64_t)split * g.k_per;
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   PA pa;
   PB pb;
   {
-    const int64_t ra = GK ? (int64_t)tm * BM : row0, cb = (int64_t)tn * BN;
+    const int64_t ra = row0, cb = (int64_t)tn * BN;
     const T* A = static_cast<const T*>(g.a) + (TA ? k0 * g.lda + ra : ra * g.lda + k0);
     const T* B = static_cast<const T*>(g.b) + (GK || k1 == 0 ? 0 : e * g.sb) + (TB ? k0 * g.ldb + cb : cb * g.ldb + k0);
     pa.init(reinterpret_cast<const char*>(A), g.lda * (int64_t)sizeof(T), rows_a, wave, lane);
@@ -446,7 +451,6 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   float bias[8] = {};
   if (g.bias && n_in > 0 && !g.part && !(!GK && e == g.groups && g.offsets))
     load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n_in, bias);
-  const int64_t crow0 = GK ? (int64_t)tm * BM : row0;
   // Where n is a multiple of 8 every piece is whole: no branch between the loads and
   // stores of a strip.
   auto strips = [&](auto full_tag) __attribute__((always_inline)) {
@@ -479,7 +483,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
             v[4 + c] += y[c];
           }
         }
-        const int64_t row = crow0 + wm * WM + 32 * i + lr;
+        const int64_t row = row0 + wm * WM + 32 * i + lr;
         if (pr < ROWS && row < end && n_in > 0) {
           if (g.part) store8(g.part + ((int64_t)split * g.m + row) * g.n + col, n, v);
           else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);

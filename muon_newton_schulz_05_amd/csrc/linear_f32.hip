@@ -73,7 +73,9 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
   const int blk = blockIdx.x / cols, cb = blockIdx.x - blk * cols;
   int e = 0, lo = 0, hi = 0;
   if (a.offsets) {
-    if (!find_group(a.offsets, a.groups, a.rows, a.block, blk, e, lo, hi)) return;
+    const GroupBlocks gb(a.offsets, a.groups, a.rows, a.block);
+    if (blk >= gb.total) return;
+    gb.find(a.offsets, a.groups, a.rows, a.block, blk, e, lo, hi);
     hi = min(hi, lo + a.block);
   } else {
     lo = blk * a.block;
