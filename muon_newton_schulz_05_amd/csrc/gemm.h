@@ -294,24 +294,25 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
     end = hi;
     if (e == g.groups) k1 = 0;  // rows past the last group: zeros
   } else {
-    if (g.splits > 1) {
-      split = b / tiles;
-      b -= split * tiles;
-    }
+    // Splits, then groups, then tiles.
+    const int e_split = b / tiles;
+    b -= e_split * tiles;
+    split = e_split / g.groups;
+    e = e_split - split * g.groups;
+    int64_t per = g.k_per;
     if (GK && g.offsets) {
-      e = b / tiles;
-      b -= e * tiles;
       int lo, hi;
       group_range(g.offsets, g.groups, g.k, e, lo, hi);
       k0 = lo;
       k1 = hi;
+      per = ((hi - lo + g.splits - 1) / g.splits + 63) / 64 * 64;
+    }
+    if (g.splits > 1) {
+      k0 += split * per;
+      k1 = min(k0 + per, k1);
     }
     stripe(xcd_place(b, tiles), g.tiles_m, g.tiles_n, tm, tn);
     row0 = (int64_t)tm * BM;
-  }
-  if (g.splits > 1) {
-    k0 = (int64_t)split * g.k_per;
-    k1 = min(k0 + g.k_per, k1);
   }
   e = __builtin_amdgcn_readfirstlane(e);
   const int rows_a = (int)min((int64_t)BM, end - row0), rows_b = (int)min((int64_t)BN, g.n - (int64_t)tn * BN);
@@ -332,6 +333,23 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{};
+
+  // float32: the accumulators are emptied into a second set every 512 of the
+  // contraction, so that rounding grows with 512 + K / 512 additions, not with K
+  // (a dW over 12000 rows is 4e-7 off its float64 value).
+  constexpr bool TWO = sizeof(T) == 4;
+  f32x4_t total[TWO ? FM : 1][TWO ? FN : 1] = {};
+  auto empty = [&] __attribute__((always_inline)) {
+    if constexpr (TWO) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          total[i][j] += acc[i][j];
+          acc[i][j] = f32x4_t{};
+        }
+    }
+  };
 
   // A wave whose rows or columns all lie outside C multiplies nothing.
   const bool idle = wm * WM >= rows_a || wn * WN >= rows_b;
@@ -401,6 +419,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
             else interleave<RD, 0, 1, MM>();
           }
         };
+        if (TWO && (kt & 15) == 15) empty();
         step(stages + (stage == 0 ? NS - 1 : stage - 1) * STAGE, stages + stage * STAGE);
         stage = stage == NS - 1 ? 0 : stage + 1;
       }
@@ -430,6 +449,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0: this wave's part is in LDS; loads stay in flight
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        if (TWO && (kt & 15) == 15) empty();
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
           read(st, s);
@@ -437,6 +457,12 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
         }
       }
     }
+  }
+  if constexpr (TWO) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] += total[i][j];
   }
   __syncthreads();  // every wave is done with the operand stages
 
@@ -485,7 +511,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
         }
         const int64_t row = row0 + wm * WM + 32 * i + lr;
         if (pr < ROWS && row < end && n_in > 0) {
-          if (g.part) store8(g.part + ((int64_t)split * g.m + row) * g.n + col, n, v);
+          if (g.part) store8(g.part + (((int64_t)split * g.groups + e) * g.m + row) * g.n + col, n, v);
           else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);
         }
       }
@@ -497,17 +523,18 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
 }
 
 // Joins a split contraction: the partials of an entry are added in split
-// order, then the epilogue runs as in the kernel above.
+// order, then the epilogue runs as in the kernel above.  The groups' results
+// lie one behind the other, as rows of one matrix.
 template <typename T>
 __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs g) {
-  const int64_t per = (g.n + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= per * g.m) return;
+  const int64_t per = (g.n + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = g.m * g.groups;
+  if (i >= per * rows) return;
   const int64_t row = i / per;
   const int col = (int)(i - row * per) * 8, n = (int)min((int64_t)8, g.n - col);
   float v[8] = {}, bias[8] = {};
   for (int s = 0; s < g.splits; ++s) {
     float p[8];
-    load8(g.part + ((int64_t)s * g.m + row) * g.n + col, n, p);
+    load8(g.part + ((int64_t)s * rows + row) * g.n + col, n, p);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += p[k];
   }

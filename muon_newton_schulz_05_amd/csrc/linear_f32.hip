@@ -6,21 +6,18 @@ namespace muon {
 
 hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s) {
   if (loads == kDirect4) {
-    if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 1, 4, kDirect4>(g, ta, tb, s);
     if (tile == kTile32x64) return launch_tile<float, 32, 64, 1, 4, 1, 4, kDirect4>(g, ta, tb, s);
-    return launch_tile<float, 128, 128, 2, 2, 1, 2, kDirect4>(g, ta, tb, s);
+    return launch_tile<float, 64, 64, 2, 2, 1, 2, kDirect4>(g, ta, tb, s);
   }
   if (loads == kStaged) {
-    if (tile == kTile64) return launch_tile<float, 64, 64, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
     if (tile == kTile32x64) return launch_tile<float, 32, 64, 1, 4, 1, 2, kStaged>(g, ta, tb, s);
-    return launch_tile<float, 128, 128, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
+    return launch_tile<float, 64, 64, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
   }
   switch (tile) {
-    case kTile64: return launch_tile<float, 64, 64, 2, 2, 1, 4, kDirect16>(g, ta, tb, s);
     case kTile32x64: return launch_tile<float, 32, 64, 1, 4, 1, 4, kDirect16>(g, ta, tb, s);
     case kTileRows32: return launch_tile<float, 32, 128, 1, 4, 1, 4, kDirect16>(g, ta, tb, s);
     case kTileRows32K: return launch_tile<float, 32, 64, 1, 2, 4, 3, kDirect16>(g, ta, tb, s);
-    default: return launch_tile<float, 128, 128, 2, 2, 1, 2, kDirect16>(g, ta, tb, s);
+    default: return launch_tile<float, 64, 64, 2, 2, 1, 2, kDirect16>(g, ta, tb, s);
   }
 }
 
@@ -51,7 +48,7 @@ hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, int loads
 }
 
 hipError_t launch_gemm_join(const GemmArgs& g, int dtype, hipStream_t s) {
-  const int64_t blocks = ((g.n + 7) / 8 * g.m + 255) / 256;
+  const int64_t blocks = ((g.n + 7) / 8 * g.m * g.groups + 255) / 256;
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   if (dtype == MUON_BF16) hipLaunchKernelGGL((k_gemm_join<uint16_t>), dim3((unsigned)blocks), dim3(256), 0, s, g);

@@ -28,10 +28,11 @@ struct GemmArgs {
   const void* res;         // null, or rows of ldr elements
   int64_t ldc, sc, ldr, sbias;
   int32_t act;
-  // split contraction: part != null stores float32 partials [splits][m][n]
+  // split contraction: part != null stores float32 partials [splits][groups][m][n]
   float* part;
   int32_t splits;
-  int64_t k_per;           // contraction of one split (a multiple of 64)
+  int64_t k_per;           // contraction of one split (a multiple of 64); a grouped
+                           // contraction's splits go by each group's length
   int32_t tiles_m, tiles_n;
 };
 

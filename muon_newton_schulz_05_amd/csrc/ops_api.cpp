@@ -75,17 +75,18 @@ struct Product {
 //    128 x 128 256, with 256 x 256 split four ways 248.
 //  - 128 x 128 down to half a card of tiles (2048^3: 30 / 31 / 29, with 256 x 128
 //    50), then 64 x 64.  float32 products are bound by their lower matrix rate,
-//    not by operand traffic, and take 64 x 64 until 128 x 128 fills the card four
-//    times over (1024^3: 25 against 47; 4096^3: 1017 against 987), and 32 x 64
-//    while 64 x 64 fills it at most twice (777 x 1001 x 1343: 39 against 47).
+//    not by operand traffic, and take 64 x 64 throughout, or 32 x 64 while
+//    64 x 64 fills the card at most twice (777 x 1001 x 1343: 39 against 47).
 //  - 32 x 128 for at most 32 rows (a group), where time goes to reading B, and for
 //    grouped products whose 64-tiles leave units idle ([24, 10240] experts over
 //    8192 rows, dx: 52, with 64 x 64 75, with 128 x 128 104).  Dense and at least
 //    1024 deep: 32 x 64, the contraction shared by four sets of waves, which
 //    needs no join for 8192 columns and more.
-// A dense product whose tiles do not fill the card is split along the
-// contraction, at least 512 of it each, and joined.  Grouped products are not:
-// their tiles already number at least the groups with rows.
+// A product whose tiles do not fill the card is split along the contraction, at
+// least 512 of it each, and joined; one over grouped rows is not, its tiles
+// number at least the groups with rows.  A grouped contraction has groups of
+// unlike length, and is split until the card is filled four times (three
+// experts' [678, 520] over 31936 rows, float32 dW: 345 against 383).
 void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups) {
   muon::GemmArgs& g = p->g;
   const bool gk = ta && tb, grouped = groups > 0;
@@ -98,14 +99,14 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   const bool f32 = dtype == MUON_F32, wide = !f32 && g.k > 64;
   p->loads = loads;
   if (loads != muon::kDirect16) {
-    p->tile = tiles(muon::kTile128) >= (f32 ? 4 : 2) * kCus ? muon::kTile128 : muon::kTile64;
+    p->tile = !f32 && tiles(muon::kTile128) >= 2 * kCus ? muon::kTile128 : muon::kTile64;
   } else if (m_each <= 32) {
     p->tile = !grouped && !gk && g.k >= 1024 ? muon::kTileRows32K : muon::kTileRows32;
   } else if (wide && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
     p->tile = muon::kTile256;
   } else if (wide && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
     p->tile = muon::kTile256x128;
-  } else if (tiles(muon::kTile128) >= (f32 ? 4 * kCus : kCus / 2)) {
+  } else if (!f32 && tiles(muon::kTile128) >= kCus / 2) {
     p->tile = muon::kTile128;
   } else {
     p->tile = !(grouped && !gk && tiles(muon::kTile64) < kCus) ? muon::kTile64
@@ -121,13 +122,15 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   g.k_per = g.k;
   const int64_t t = tiles(p->tile);
   const bool sets = p->tile == muon::kTileRows32K;
-  if (!grouped && t > 0 && t < (sets ? kCus / 2 : kCus) && g.k >= 1024) {
-    int64_t s = std::min<int64_t>(((sets ? kCus : 2 * kCus) + t - 1) / t, g.k / 512);
+  const int64_t k_each = grouped && gk ? g.k / groups : g.k;
+  const int64_t below = sets ? kCus / 2 : grouped ? 2 * kCus : kCus, want = sets ? kCus : grouped ? 4 * kCus : 2 * kCus;
+  if ((gk || !grouped) && t > 0 && t < below && k_each >= 1024) {
+    int64_t s = std::min<int64_t>((want + t - 1) / t, k_each / 512);
     s = std::min<int64_t>(s, 64);
     if (s > 1) {
       g.k_per = ((g.k + s - 1) / s + 63) / 64 * 64;
-      g.splits = (int32_t)((g.k + g.k_per - 1) / g.k_per);
-      p->ws = (uint64_t)g.splits * g.m * g.n * 4;
+      g.splits = (int32_t)(grouped ? s : (g.k + g.k_per - 1) / g.k_per);
+      p->ws = (uint64_t)g.splits * g.groups * g.m * g.n * 4;
     }
   }
 }

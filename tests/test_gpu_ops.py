@@ -447,3 +447,18 @@ def test_capture_of_forward_and_backward(muon):
         torch.cuda.synchronize()
         for a, b in zip(out, eager):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("counts", [[5000, 0, 37, 1300], [64, 4100]], ids=["uneven", "few"])
+def test_experts_weight_gradient_over_long_groups(muon, counts, dtype):
+    """Few experts with many rows: the contraction is split, with splits of a short or an empty group left empty."""
+    e, k, n = len(counts), 72, 40
+    offsets = torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    rows = int(offsets[-1])
+    x, dy, w = normal((rows, k), dtype, 1), normal((rows, n), dtype, 2), normal((e, k, n), dtype, 3)
+    gw = w.cuda().requires_grad_()
+    (dw,) = torch.autograd.grad(muon.expert_linear(x.cuda(), gw, offsets.cuda()), gw, dy.cuda())
+    for i in range(e):
+        lo, hi = offsets[i], offsets[i + 1]
+        ref.check(i, dw[i], ref.linear64(x[lo:hi], w[i], None, None, dy[lo:hi], "none")["dw"])
