@@ -51,7 +51,8 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     case MUON_ACT_GELU_TANH: {
       const float q = sigmoid_f(2.f * kGeluC * (z + kGeluA * z * z * z));
-      return q + z * q * (1.f - q) * 2.f * kGeluC * (1.f + 3.f * kGeluA * z * z);
+      // z^2 is bounded so that its overflow does not meet 1 - q = 0.
+      return q + z * q * (1.f - q) * 2.f * kGeluC * (1.f + 3.f * kGeluA * fminf(z * z, 1e30f));
     }
     default: return 1.f;
   }

@@ -462,3 +462,57 @@ def test_experts_weight_gradient_over_long_groups(muon, counts, dtype):
     for i in range(e):
         lo, hi = offsets[i], offsets[i + 1]
         ref.check(i, dw[i], ref.linear64(x[lo:hi], w[i], None, None, dy[lo:hi], "none")["dw"])
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_activations_of_large_arguments(muon, act):
+    """z over the range where the factors saturate: act(z) is z or nothing, its slope one or nothing."""
+    z = torch.tensor([-1e30, -1e10, -200.0, -60.0, -0.0, 0.0, 60.0, 200.0, 1e10, 1e30])
+    x = z[:, None].cuda().requires_grad_()
+    y = muon.linear(x, torch.ones(1, 8, device="cuda"), activation=act)
+    (dx,) = torch.autograd.grad(y, x, torch.ones_like(y))
+    want, slope = ref.act64(z.double(), act)
+    want, slope = want.nan_to_num(0), slope.nan_to_num(0)   # the reference's own inf * 0 past e^709
+    assert torch.allclose(y[:, 0].double().cpu(), want, rtol=1e-5, atol=1e-20)
+    ok = z != 0                                              # relu's slope at zero is a convention
+    assert torch.allclose(dx[ok, 0].double().cpu() / 8, slope[ok], rtol=1e-5, atol=1e-6)
+
+
+def test_linear_past_32_bit_offsets(muon):
+    """An output of 2^32 elements and more, its gradient read back: sampled rows and columns against float64."""
+    m, k, n = 66000, 64, 66048
+    x, w = normal((m, k), BF16, 1).cuda(), normal((k, n), BF16, 2, k ** -0.5).cuda()
+    y = muon.linear(x, w)
+    rows = torch.tensor([0, 1, 32511, 32513, 65023, 65535, m - 1], device="cuda")
+    want = x[rows].double() @ w.double()
+    ref.check("y", y[rows], (want.cpu(), (ref.unit(BF16) * want.abs()).cpu() + 1e-5))
+    dx, dw, db = muon.linear_backward(y, x, w)
+    g = y[rows].double()
+    want = (g @ w.double().t()).cpu()
+    ref.check("dx", dx[rows], (want, ref.unit(BF16) * want.abs() + n * ref.U32 * 8))
+    cols = torch.tensor([0, 5, 33024, n - 1], device="cuda")
+    g = y[:, cols].double()
+    want = (x.double().t() @ g).cpu()
+    ref.check("dw", dw[:, cols], (want, ref.unit(BF16) * want.abs() + m * ref.U32 * 8))
+    ref.check("db", db[cols], (g.sum(0).cpu(), ref.unit(BF16) * g.sum(0).abs().cpu() + m * ref.U32 * 4))
+
+
+def test_moves_past_32_bit_offsets(muon):
+    """2^31 elements and more of sorted rows."""
+    t, top, h = 262144, 8, 1032
+    ids = torch.randint(0, 64, (t, top), generator=torch.Generator().manual_seed(1)).cuda()
+    r = muon.route(ids, 64)
+    x = normal((t, h), BF16, 2).cuda()
+    xs = muon.dispatch(x, r)
+    at = torch.tensor([0, 1, 1040384, 2080768, 2080769, t * top - 1], device="cuda")
+    assert torch.equal(xs[at], x[(r.order[at] // top).long()])
+    ones = torch.ones(t, top, device="cuda")
+    y = muon.combine(xs, r, ones)
+    rows = torch.tensor([0, 77, 131072, t - 1], device="cuda")
+    assert torch.equal(y[rows], (x[rows].float() * top).bfloat16())
+    dys, dw = muon.combine_backward(x, xs, r, ones)
+    assert torch.equal(dys[at], xs[at])
+    want = (x[rows].double() ** 2).sum(1, keepdim=True).expand(-1, top).cpu()
+    ref.check("dw", dw[rows], (want, h * ref.U32 * want))
+    # An order of its rows undoes the sort: every entry comes back to its token.
+    assert torch.equal(muon.dispatch_backward(xs, r)[rows], (x[rows].float() * top).bfloat16())
