@@ -3,22 +3,32 @@
 // along its rows, over groups of rows or of the contraction, and bias,
 // activation and residual in the epilogue.
 //
-// A workgroup owns a BM x BN tile of C; each of its waves owns a block of
-// 32 x 32 matrix-core products.  Operand k-slices of KB = 64 or 128 bytes
-// a row go from memory straight into LDS, NS stages
-// deep, with one barrier a slice.  What is out of range (rows past the
-// group, the contraction's tail) is given an offset past the buffer
-// descriptor's end, for which the load writes zeros to LDS.
+// A workgroup owns a BM x BN tile of C; each of its waves owns a block of it,
+// as 16 x 16 matrix-core products.  Operand k-slices of KB = 128 bytes a row
+// go from memory straight into LDS, NS stages deep, with one barrier a slice.
+// What is out of range (rows past the group, the contraction's tail) is
+// given an offset past the buffer descriptor's end, for which the load writes
+// zeros to LDS.
 //
 //  - An operand contiguous along k sits in LDS as rows of KB bytes; the
-//    16-byte chunk c of row r at slot c ^ (r / 2 mod 8) (KB = 128) or
-//    c ^ (r / 4 mod 4) (64), so that 16 lanes
+//    16-byte chunk c of row r at slot c ^ (r / 2 mod 8), so that 16 lanes
 //    reading one chunk of 16 rows touch 16 distinct 16-byte bank groups.
 //  - An operand contiguous along its rows sits as k-rows.  bf16: fragments
 //    are read by ds_read_b64_tr_b16, which hands lane i of 16 the column i of
-//    a 4 x 16 block (four k of one row of the operand); k-rows k .. k + 3 of one
-//    64-byte block are kept in distinct banks by chunk ^ 4 (k mod 4).
-//    float32: 32 lanes read 32 consecutive values, no transposition.
+//    a 4 x 16 block (four k of one row of the operand); the eight 32-byte
+//    pieces that 32 lanes read at once are kept in distinct banks by an XOR of
+//    the chunk with their k.  float32: 16 lanes read 16 consecutive values of
+//    each of four k, no transposition.
+//
+// What bounds it.  bf16, 256 x 256 tiles, 8192^3: 1400 TFLOP/s forward and dW,
+// 1430 dx; the matrix cores are busy 70 - 73% of the cycles, at about 1.9 GHz
+// under the card's power limit (the best library kernel measured: 1574, 87% at
+// 1.74 GHz).  The rest is waiting at the slices' barriers.  Four waves of
+// 128 x 128 read a third less from LDS and were 7 - 12% slower; half slices, four
+// or five deep, were equal for operands along their rows and 8% slower for
+// operands along k, whose loads then take half lines.  With few slices a tile
+// (experts: 12 to 32) the tile's start and its epilogue, about 12 us, show: one
+// workgroup holds a unit's LDS, so nothing runs beside them.
 #pragma once
 #include <type_traits>
 
@@ -258,7 +268,7 @@ template <typename T, int BM, int BN, int WGM, int WGN, int WGK, int NS, bool TA
 __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
   constexpr bool DIRECT = LOADS != kStaged;
-  constexpr int PD = DIRECT ? 1 : BM * BN <= 64 * 64 ? 4 : 2;
+  constexpr int PD = DIRECT ? 1 : 4;
   typedef Panel<T, BM, TA, NW, LOADS, PD> PA;
   typedef Panel<T, BN, TB, NW, LOADS, PD> PB;
   typedef typename Mma<T>::Frag Frag;
@@ -271,10 +281,12 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave = wave_all % NW, set = wave_all / NW;
   static_assert(WGK == 1 || (DIRECT && BM == 32), "sets of waves: direct loads, one strip of rows");
+  static_assert(DIRECT || (NS == 2 && BM * BN <= 64 * 64), "staged loads: two stages, registers for four slices");
   // Waves w and w + 4 share a SIMD.  With 2 x 4 of them, each SIMD gets one wave
   // of the tile's upper and one of its lower half, and one of its left and one of
   // its right half, so that a tile with half of its rows or columns outside
-  // C leaves every SIMD half its work.
+  // C leaves every SIMD half its work (64 experts' [2048, 1408], whose last column
+  // tile is half empty: forward 439 us against 460).
   const int wm = NW == 8 && WGM == 2 ? (wave & 1) ^ (wave >> 2) : wave / WGN;
   const int wn = NW == 8 && WGM == 2 ? (wave >> 1) & 3 : wave % WGN;
 
@@ -413,7 +425,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
           for (int s = 0; s < SUB; ++s) {
             read(st, s);
             multiply(s + 1);  // of the other parity: substep s - 1
-            // The loads go out over the first half of the products: at 8192^3
+            // The loads go out over the first half of the substep's products: at 8192^3
             // 1416 / 1419 / 1411 TFLOP/s (forward, dx, dW) against 1388 / 1392 /
             // 1345 over all of them and 1407 / 1371 / 1406 over the first quarter.
             if (s == 0) interleave<RD, L, MM / 2, MM>();

@@ -4,14 +4,8 @@
 namespace muon {
 
 hipError_t launch_gemm_bf16(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s) {
-  if (loads == kDirect4) {
-    if (tile == kTile64) return launch_tile<uint16_t, 64, 64, 2, 2, 1, 4, kDirect4>(g, ta, tb, s);
-    return launch_tile<uint16_t, 128, 128, 2, 2, 1, 2, kDirect4>(g, ta, tb, s);
-  }
-  if (loads == kStaged) {
-    if (tile == kTile64) return launch_tile<uint16_t, 64, 64, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
-    return launch_tile<uint16_t, 128, 128, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
-  }
+  if (loads == kDirect4) return launch_tile<uint16_t, 64, 64, 2, 2, 1, 4, kDirect4>(g, ta, tb, s);
+  if (loads == kStaged) return launch_tile<uint16_t, 64, 64, 2, 2, 1, 2, kStaged>(g, ta, tb, s);
   switch (tile) {
     case kTile256: return launch_tile<uint16_t, 256, 256, 2, 4, 1, 2, kDirect16>(g, ta, tb, s);
     case kTile256x128: return launch_tile<uint16_t, 256, 128, 4, 2, 1, 3, kDirect16>(g, ta, tb, s);

@@ -65,23 +65,27 @@ struct Product {
 
 // The tile and the split of a product, by how many tiles there are for the
 // card's 256 compute units (times in us, bf16, forward / dx / dW):
-//  - 256 x 256 has the best rate (1400 TFLOP/s at 8192^3) once every unit has a
-//    tile: 4096^3 takes 110 / 105 / 106, with 256 x 128 120 / 120 / 131, with
-//    128 x 128 132 / 148 / 140.
-//    A contraction of one slice is all prologue and epilogue, and takes
-//    128 x 128, two of which share a unit ([24, 10240] experts over 8192 rows,
-//    forward: 96 against 109).
-//  - 256 x 128 where only it fills the card: 2048 x 16384 x 4096 forward 224, with
-//    128 x 128 256, with 256 x 256 split four ways 248.
-//  - 128 x 128 down to half a card of tiles (2048^3: 30 / 31 / 29, with 256 x 128
-//    50), then 64 x 64.  float32 products are bound by their lower matrix rate,
-//    not by operand traffic, and take 64 x 64 throughout, or 32 x 64 while
-//    64 x 64 fills the card at most twice (777 x 1001 x 1343: 39 against 47).
+//  - 256 x 256 has the best rate (about 1400 TFLOP/s at 8192^3) once every unit has
+//    a tile: 4096^3 takes 113 / 109 / 110, with 256 x 128 130 / 127 / 134, with
+//    128 x 128 134 / 134 / 129.
+//  - 256 x 128 where only it fills the card: 2048 x 16384 x 4096 forward 233, with
+//    256 x 256 split four ways 253, with 128 x 128 257.
+//  - 128 x 128 down to half a card of tiles (2048^3: 29 / 28 / 30, with 256 x 128
+//    51, with 64 x 64 31) and for groups of fewer than 256 rows (64 experts over
+//    8192 rows: 116 / 113, with 256 x 256 137 / 132), then 64 x 64 (1024^3: 12, with
+//    128 x 128 18).
 //  - 32 x 128 for at most 32 rows (a group), where time goes to reading B, and for
-//    grouped products whose 64-tiles leave units idle ([24, 10240] experts over
-//    8192 rows, dx: 52, with 64 x 64 75, with 128 x 128 104).  Dense and at least
-//    1024 deep: 32 x 64, the contraction shared by four sets of waves, which
-//    needs no join for 8192 columns and more.
+//    grouped products whose 64-tiles leave units idle.  At least 1024 deep,
+//    for dense ones and for at most 64 columns of grouped ones: 32 x 64, the
+//    contraction shared by four sets of waves (16 x 4096 x 16384: 25 / 27, with
+//    32 x 128 and a join 27 / 30; [24, 10240] experts over 8192 rows, dx from
+//    memory: 71, with 32 x 128 84).
+//  - Operands that no 16-byte loads reach: 64 x 64, whose staging hides better
+//    behind other workgroups (4001 x 2001 x 4003: 184 / 226 / 324, with 128 x 128
+//    204 / 272 / 472).
+//  - float32 products are bound by their lower matrix rate, not by operand
+//    traffic: 64 x 64, or 32 x 64 while 64 x 64 fills the card at most twice
+//    (777 x 1001 x 1343: 38 / 37 / 35 against 45 / 37 / 37).
 // A product whose tiles do not fill the card is split along the contraction, at
 // least 512 of it each, and joined; one over grouped rows is not, its tiles
 // number at least the groups with rows.  A grouped contraction has groups of
@@ -96,15 +100,15 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
     return tm * ((g.n + bn - 1) / bn) * (gk && grouped ? groups : 1);
   };
   const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
-  const bool f32 = dtype == MUON_F32, wide = !f32 && g.k > 64;
+  const bool f32 = dtype == MUON_F32;
   p->loads = loads;
   if (loads != muon::kDirect16) {
-    p->tile = !f32 && tiles(muon::kTile128) >= 2 * kCus ? muon::kTile128 : muon::kTile64;
+    p->tile = muon::kTile64;
   } else if (m_each <= 32) {
     p->tile = !grouped && !gk && g.k >= 1024 ? muon::kTileRows32K : muon::kTileRows32;
-  } else if (wide && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
+  } else if (!f32 && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
     p->tile = muon::kTile256;
-  } else if (wide && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
+  } else if (!f32 && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
     p->tile = muon::kTile256x128;
   } else if (!f32 && tiles(muon::kTile128) >= kCus / 2) {
     p->tile = muon::kTile128;

@@ -7,6 +7,9 @@
 // The moves are bound by memory.  They are cut by tokens, not by sorted rows:
 // a token's row (or its gradient) is read once and meets its `top` rows
 // from registers, and each sum over them runs in the order of the choices.
+// 16384 tokens x 8 of 64 experts at h = 2048 in bf16: sort 21 us, dispatch 114,
+// combine and dispatch's gradient 116 each, combine's gradient 249 (4.6 - 5.3 TB/s).
+// Up to 4096 entries the sort is one launch (64 tokens x 6: 3.5 us).
 #include "act.h"
 #include "device_common.h"
 #include "ops.h"
