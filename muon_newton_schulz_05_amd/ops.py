@@ -164,7 +164,8 @@ class _Plan:
         else:
             layout, ld = 1, w.stride(-1) if n > 1 else max(k, 1)
         self.rows, self.k, self.n, self.groups, self.layout = x.shape[0], k, n, groups, layout
-        self.y_shape = (self.rows, n)
+        self.y_shape, self.x_shape = (self.rows, n), (self.rows, k)
+        self.db_shape = (groups, n) if grouped else (n,)
         lead = (groups,) if grouped else ()
         self.dw_shape = (*lead, k, n) if layout == 0 else (*lead, n, k)
         self.args = [_dtype(x, "x"), act, groups, layout, self.rows, k, n, _ld(x), ld, w.stride(0) if grouped else 0]
@@ -250,14 +251,14 @@ def _forward(x, w, bias, residual, offsets, act, keep_z):
     return y, z
 
 
-def _backward(dy, x, w, z, offsets, act, need_x, need_w, need_b):
-    p = _plan(x, w, act, offsets is not None)
+def _backward(p, dy, x, w, z, offsets, need_x, need_w, need_b):
+    """dx, dw, db of plan p for dy [rows, N] with contiguous rows."""
     d, size = p.get(_BACKWARD, _ld(dy))
-    like = {"dtype": x.dtype, "device": x.device}
-    dx = torch.empty((p.rows, p.k), **like) if need_x else None
-    dw = torch.empty(p.dw_shape, **like) if need_w else None
-    db = torch.empty((p.groups, p.n) if p.groups else (p.n,), **like) if need_b else None
-    ws = _workspace(size, x)
+    dtype, dev = x.dtype, x.device
+    dx = torch.empty(p.x_shape, dtype=dtype, device=dev) if need_x else None
+    dw = torch.empty(p.dw_shape, dtype=dtype, device=dev) if need_w else None
+    db = torch.empty(p.db_shape, dtype=dtype, device=dev) if need_b else None
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     _call("muon_linear_backward", x, d, _ptr(offsets), x.data_ptr(), w.data_ptr(), _ptr(z), dy.data_ptr(), _ptr(dx),
           _ptr(dw), _ptr(db), _ptr(ws), size)
     if dw is not None and p.layout == 1:
@@ -296,7 +297,8 @@ def linear_backward(dy, x, weight, z=None, activation="none", offsets=None, need
         raise ValueError("z must be the tensor that linear_forward(..., keep_z=True) returned")
     k, n = weight.shape[-2:]
     w = weight if _layout_ok(weight) else weight.contiguous()
-    dx, dw, db = _backward(_flat(dy, n), _flat(x, k), w, z, offsets, act, *needs)
+    x2 = _flat(x, k)
+    dx, dw, db = _backward(_plan(x2, w, act, offsets is not None), _flat(dy, n), x2, w, z, offsets, *needs)
     return None if dx is None else dx.view(x.shape), dw, db
 
 
@@ -305,7 +307,7 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, bias, residual, offsets, act):
         y, z, x2, w = _prepared(x, weight, bias, residual, offsets, act, True)
         ctx.save_for_backward(x2, w, z, offsets)
-        ctx.act, ctx.x_shape = act, x.shape
+        ctx.plan, ctx.x_shape = _plan(x2, w, act, offsets is not None), x.shape
         return y
 
     @staticmethod
@@ -315,8 +317,8 @@ class _Linear(torch.autograd.Function):
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
         dx = dw = db = None
         if need_x or need_w or need_b:
-            dx, dw, db = _backward(_flat(dy, w.shape[-1]), x, w, z, offsets, ctx.act, need_x, need_w, need_b)
-            if dx is not None:
+            dx, dw, db = _backward(ctx.plan, _flat(dy, w.shape[-1]), x, w, z, offsets, need_x, need_w, need_b)
+            if dx is not None and len(ctx.x_shape) != 2:
                 dx = dx.view(ctx.x_shape)
         return dx, dw, db, dy if need_r else None, None, None
 
@@ -396,11 +398,6 @@ def route(expert_ids, n_experts):
     return Routing(buf[:n_experts + 1], buf[e4:e4 + end], buf[e4 + p4:e4 + p4 + end].view(tokens, top))
 
 
-def _move(routing, rows, h, dtype):
-    tokens, top = routing.position.shape
-    return MoveDesc(dtype, routing.offsets.shape[0] - 1, top, 0, tokens, h, h, h, h)
-
-
 def _check_routing(routing, t, rows, what):
     _gpu(t, what)
     _dtype(t, what)
@@ -416,29 +413,36 @@ def _check_routing(routing, t, rows, what):
         raise ValueError("routing must be what route() returned")
 
 
+def _dispatch(x, offsets, position):
+    tokens, top = position.shape
+    x = _rows(x)
+    h = x.shape[1]
+    d = MoveDesc(_dtype(x, "x"), offsets.shape[0] - 1, top, 0, tokens, h, _ld(x), h, h)
+    xs = torch.empty((tokens * top, h), dtype=x.dtype, device=x.device)
+    _call("muon_dispatch", x, ctypes.byref(d), offsets.data_ptr(), position.data_ptr(), x.data_ptr(), xs.data_ptr())
+    return xs
+
+
+def _dispatch_grad(dxs, offsets, position):
+    tokens, top = position.shape
+    dxs = _rows(dxs)
+    h = dxs.shape[1]
+    d = MoveDesc(_dtype(dxs, "dxs"), offsets.shape[0] - 1, top, 0, tokens, h, _ld(dxs), h, h)
+    dx = torch.empty((tokens, h), dtype=dxs.dtype, device=dxs.device)
+    _call("muon_dispatch_grad", dxs, ctypes.byref(d), position.data_ptr(), dxs.data_ptr(), dx.data_ptr())
+    return dx
+
+
 def dispatch_forward(x, routing):
     """``dispatch`` without autograd."""
-    tokens, top = routing.position.shape
-    _check_routing(routing, x, tokens, "x")
-    x = _rows(x)
-    d = _move(routing, tokens, x.shape[1], _dtype(x, "x"))
-    d.ldx = _ld(x)
-    xs = torch.empty((tokens * top, x.shape[1]), dtype=x.dtype, device=x.device)
-    _call("muon_dispatch", x, ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(), x.data_ptr(),
-          xs.data_ptr())
-    return xs
+    _check_routing(routing, x, routing.position.shape[0], "x")
+    return _dispatch(x, routing.offsets, routing.position)
 
 
 def dispatch_backward(dxs, routing):
     """dx of ``dispatch``: each token's sum over its rows of dxs."""
-    tokens, top = routing.position.shape
-    _check_routing(routing, dxs, tokens * top, "dxs")
-    dxs = _rows(dxs)
-    d = _move(routing, tokens, dxs.shape[1], _dtype(dxs, "dxs"))
-    d.ldx = _ld(dxs)
-    dx = torch.empty((tokens, dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
-    _call("muon_dispatch_grad", dxs, ctypes.byref(d), routing.position.data_ptr(), dxs.data_ptr(), dx.data_ptr())
-    return dx
+    _check_routing(routing, dxs, routing.position.numel(), "dxs")
+    return _dispatch_grad(dxs, routing.offsets, routing.position)
 
 
 def _check_weights(routing, weights):
@@ -448,80 +452,95 @@ def _check_weights(routing, weights):
         raise ValueError(f"weights is on {weights.device}, the routing is on {routing.position.device}")
 
 
+def _combine(ys, offsets, position, weights, residual):
+    tokens, top = position.shape
+    ys, w = _rows(ys), weights.contiguous()
+    h = ys.shape[1]
+    residual = None if residual is None else _rows(residual)
+    d = MoveDesc(_dtype(ys, "ys"), offsets.shape[0] - 1, top, 0, tokens, h, _ld(ys), h,
+                 h if residual is None else _ld(residual))
+    y = torch.empty((tokens, h), dtype=ys.dtype, device=ys.device)
+    _call("muon_combine", ys, ctypes.byref(d), position.data_ptr(), w.data_ptr(), ys.data_ptr(), _ptr(residual),
+          y.data_ptr())
+    return y
+
+
+def _combine_grad(dy, ys, offsets, position, weights, need_ys, need_w):
+    tokens, top = position.shape
+    dy, ys, w = _rows(dy), _rows(ys), weights.contiguous()
+    h = ys.shape[1]
+    d = MoveDesc(_dtype(ys, "ys"), offsets.shape[0] - 1, top, 0, tokens, h, _ld(ys), _ld(dy), h)
+    dys = torch.empty((tokens * top, h), dtype=ys.dtype, device=ys.device) if need_ys else None
+    dw = torch.empty((tokens, top), dtype=torch.float32, device=ys.device) if need_w else None
+    _call("muon_combine_grad", ys, ctypes.byref(d), offsets.data_ptr(), position.data_ptr(), w.data_ptr(),
+          ys.data_ptr(), dy.data_ptr(), _ptr(dys), _ptr(dw))
+    return dys, dw
+
+
+def _check_combine(ys, routing, weights, residual):
+    _check_routing(routing, ys, routing.position.numel(), "ys")
+    _check_weights(routing, weights)
+    if residual is not None:
+        _same(ys, residual=residual)
+        want = (routing.position.shape[0], ys.shape[1])
+        if residual.shape != want:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {want}")
+
+
 def combine_forward(ys, routing, weights, residual=None):
     """``combine`` without autograd (weights float32)."""
-    tokens, top = routing.position.shape
-    _check_routing(routing, ys, tokens * top, "ys")
-    _check_weights(routing, weights)
-    _same(ys, residual=residual)
-    h = ys.shape[1]
-    if residual is not None and tuple(residual.shape) != (tokens, h):
-        raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {(tokens, h)}")
-    ys, w = _rows(ys), weights.contiguous()
-    residual = None if residual is None else _rows(residual)
-    d = _move(routing, tokens, h, _dtype(ys, "ys"))
-    d.ldx = _ld(ys)
-    if residual is not None:
-        d.ldr = _ld(residual)
-    y = torch.empty((tokens, h), dtype=ys.dtype, device=ys.device)
-    _call("muon_combine", ys, ctypes.byref(d), routing.position.data_ptr(), w.data_ptr(), ys.data_ptr(),
-          _ptr(residual), y.data_ptr())
-    return y
+    _check_combine(ys, routing, weights, residual)
+    return _combine(ys, routing.offsets, routing.position, weights, residual)
 
 
 def combine_backward(dy, ys, routing, weights, needs=(True, True)):
     """(dys, dweights) of ``combine``; needs: which of them are computed."""
-    tokens, top = routing.position.shape
-    _check_routing(routing, dy, tokens, "dy")
-    _check_routing(routing, ys, tokens * top, "ys")
+    _check_routing(routing, dy, routing.position.shape[0], "dy")
+    _check_routing(routing, ys, routing.position.numel(), "ys")
     _check_weights(routing, weights)
     _same(ys, dy=dy)
     if dy.shape[1] != ys.shape[1]:
         raise ValueError(f"dy has {dy.shape[1]} columns, ys has {ys.shape[1]}")
-    dy, ys, w = _rows(dy), _rows(ys), weights.contiguous()
-    d = _move(routing, tokens, ys.shape[1], _dtype(ys, "ys"))
-    d.ldx, d.ldg = _ld(ys), _ld(dy)
-    dys = torch.empty((tokens * top, ys.shape[1]), dtype=ys.dtype, device=ys.device) if needs[0] else None
-    dw = torch.empty((tokens, top), dtype=torch.float32, device=ys.device) if needs[1] else None
-    _call("muon_combine_grad", ys, ctypes.byref(d), routing.offsets.data_ptr(), routing.position.data_ptr(),
-          w.data_ptr(), ys.data_ptr(), dy.data_ptr(), _ptr(dys), _ptr(dw))
-    return dys, dw
+    return _combine_grad(dy, ys, routing.offsets, routing.position, weights, *needs)
 
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, offsets, order, position):
-        ctx.save_for_backward(offsets, order, position)
-        return dispatch_forward(x, Routing(offsets, order, position))
+    def forward(ctx, x, offsets, position):
+        ctx.save_for_backward(offsets, position)
+        return _dispatch(x, offsets, position)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dxs):
-        return dispatch_backward(dxs, Routing(*ctx.saved_tensors)), None, None, None
+        return _dispatch_grad(dxs, *ctx.saved_tensors), None, None
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, ys, weights, residual, offsets, order, position):
-        ctx.save_for_backward(ys, weights, offsets, order, position)
-        return combine_forward(ys, Routing(offsets, order, position), weights, residual)
+    def forward(ctx, ys, weights, residual, offsets, position):
+        ctx.save_for_backward(ys, weights, offsets, position)
+        return _combine(ys, offsets, position, weights, residual)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        ys, weights, *routing = ctx.saved_tensors
+        ys, weights, offsets, position = ctx.saved_tensors
         need_ys, need_w, need_r = ctx.needs_input_grad[:3]
         dys = dw = None
         if need_ys or need_w:
-            dys, dw = combine_backward(dy, ys, Routing(*routing), weights, (need_ys, need_w))
-        return dys, dw, dy if need_r else None, None, None, None
+            dys, dw = _combine_grad(dy, ys, offsets, position, weights, need_ys, need_w)
+        return dys, dw, dy if need_r else None, None, None
 
 
 def dispatch(x, routing):
     """Rows of x [tokens, H] in sorted order: xs[position[t][j]] = x[t], [tokens * top, H].
 
     Rows past the routed ones are zero.  Differentiable in x."""
-    return _Dispatch.apply(x, *routing) if _tracked(x) else dispatch_forward(x, routing)
+    _check_routing(routing, x, routing.position.shape[0], "x")
+    if not _tracked(x):
+        return _dispatch(x, routing.offsets, routing.position)
+    return _Dispatch.apply(x, routing.offsets, routing.position)
 
 
 def combine(ys, routing, weights, residual=None):
@@ -533,7 +552,8 @@ def combine(ys, routing, weights, residual=None):
         weights = weights.float()
     if not _tracked(ys, weights, residual):
         return combine_forward(ys, routing, weights, residual)
-    return _Combine.apply(ys, weights, residual, *routing)
+    _check_combine(ys, routing, weights, residual)
+    return _Combine.apply(ys, weights, residual, routing.offsets, routing.position)
 
 
 # ------------------------------------------------------------------ dropout
