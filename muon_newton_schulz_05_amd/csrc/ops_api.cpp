@@ -68,8 +68,10 @@ struct Product {
 //  - 256 x 256 has the best rate (about 1400 TFLOP/s at 8192^3) once every unit has
 //    a tile: 4096^3 takes 113 / 109 / 110, with 256 x 128 130 / 127 / 134, with
 //    128 x 128 134 / 134 / 129.
-//  - 256 x 128 where only it fills the card: 2048 x 16384 x 4096 forward 233, with
-//    256 x 256 split four ways 253, with 128 x 128 257.
+//  - 256 x 256 split in two where that just fills the card, 16384 deep and more:
+//    2048 x 16384 x 4096 forward 224, with 256 x 128 234, with 128 x 128 257
+//    (8192 deep the join costs more than it gives: 124 against 117).
+//  - 256 x 128 where only it fills the card (2048 x 8192 x 4096: 117).
 //  - 128 x 128 down to half a card of tiles (2048^3: 29 / 28 / 30, with 256 x 128
 //    51, with 64 x 64 31) and for groups of fewer than 256 rows (64 experts over
 //    8192 rows: 116 / 113, with 256 x 256 137 / 132), then 64 x 64 (1024^3: 12, with
@@ -101,12 +103,17 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   };
   const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
   const bool f32 = dtype == MUON_F32;
+  const int64_t t256 = tiles(muon::kTile256);
+  const bool halves = !f32 && !grouped && m_each >= 256 && g.n >= 256 && 2 * t256 <= kCus && 16 * t256 >= 7 * kCus &&
+                      g.k >= 16384;
   p->loads = loads;
   if (loads != muon::kDirect16) {
     p->tile = muon::kTile64;
   } else if (m_each <= 32) {
     p->tile = !grouped && !gk && g.k >= 1024 ? muon::kTileRows32K : muon::kTileRows32;
   } else if (!f32 && m_each >= 256 && g.n >= 256 && tiles(muon::kTile256) >= kCus) {
+    p->tile = muon::kTile256;
+  } else if (halves) {
     p->tile = muon::kTile256;
   } else if (!f32 && m_each >= 256 && tiles(muon::kTile256x128) >= kCus) {
     p->tile = muon::kTile256x128;
@@ -130,7 +137,7 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   const int64_t below = sets ? kCus / 2 : grouped ? 2 * kCus : kCus, want = sets ? kCus : grouped ? 4 * kCus : 2 * kCus;
   if ((gk || !grouped) && t > 0 && t < below && k_each >= 1024) {
     int64_t s = std::min<int64_t>((want + t - 1) / t, k_each / 512);
-    s = std::min<int64_t>(s, 64);
+    s = p->tile == muon::kTile256 ? 2 : std::min<int64_t>(s, 64);
     if (s > 1) {
       g.k_per = ((g.k + s - 1) / s + 63) / 64 * 64;
       g.splits = (int32_t)(grouped ? s : (g.k + g.k_per - 1) / g.k_per);

@@ -78,7 +78,7 @@ def test_linear_activations(muon, act, w_t, dtype):
 
 
 @pytest.mark.parametrize("w_t", [False, True], ids=["kn", "nk"])
-@pytest.mark.parametrize("m,k,n", [(4096, 72, 4096), (4100, 200, 4104), (300, 4096, 4096)])
+@pytest.mark.parametrize("m,k,n", [(4096, 72, 4096), (4100, 200, 4104), (300, 4096, 4096), (2040, 256, 4096)])
 def test_linear_large_tiles(muon, m, k, n, w_t):
     """Shapes whose products fill the card with 256-wide tiles, whole and ragged ones."""
     run_linear(muon, m, k, n, BF16, "silu", w_t, True, True)
@@ -193,6 +193,19 @@ def test_linear_refusals(muon):
                  lambda: muon.linear(x.double(), w.double())]:
         with pytest.raises(TypeError):
             call()
+
+
+@pytest.mark.parametrize("w_t", [False, True], ids=["kn", "nk"])
+def test_linear_large_tiles_split_in_two(muon, w_t):
+    """256-wide tiles that fill half the card, over a contraction long enough to be split."""
+    m, k, n = 2000, 16392, 4000
+    x, w = normal((m, k), BF16, 1), normal((n, k) if w_t else (k, n), BF16, 2, k ** -0.5)
+    r, b = normal((m, n), BF16, 3), normal((n,), BF16, 4)
+    gw = w.cuda().t() if w_t else w.cuda()
+    y = muon.linear(x.cuda(), gw, b.cuda(), activation="silu", residual=r.cuda())
+    rows = torch.tensor([0, 1, 255, 256, 1023, 1024, 1791, 1792, 1999])
+    want = ref.linear64(x[rows], w.t() if w_t else w, b, r[rows], None, "silu")
+    ref.check("y", y[rows.cuda()], want["y"], norm_bound(BF16, k))
 
 
 # ------------------------------------------------------------------ experts
