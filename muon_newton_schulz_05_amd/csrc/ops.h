@@ -34,6 +34,7 @@ struct GemmArgs {
   int64_t k_per;           // contraction of one split (a multiple of 64); a grouped
                            // contraction's splits go by each group's length
   int32_t tiles_m, tiles_n;
+  int32_t share;           // grouped contraction: XCDs that share a group's tiles; 0: all
 };
 
 enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTile64, kTile32x64, kTileRows32, kTileRows32K };

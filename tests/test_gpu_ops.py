@@ -256,6 +256,23 @@ def test_experts_large_tiles(muon, counts):
             ref.check((name, i), got, want[name], norm_bound(BF16, 1) if hi > lo else None)
 
 
+@pytest.mark.parametrize("e", [32, 35])
+def test_experts_weight_gradient_of_many_groups(muon, e):
+    """Groups enough to be dealt to sets of XCDs, and a number that does not divide among them."""
+    k, n = 200, 136
+    counts = [(37 * i) % 1400 for i in range(e)]
+    counts[3], counts[-1] = 0, 2500
+    offsets = torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    rows = int(offsets[-1])
+    assert rows >= 512 * e
+    x, dy, w = normal((rows, k), BF16, 1), normal((rows, n), BF16, 2), normal((e, k, n), BF16, 3)
+    gw = w.cuda().requires_grad_()
+    (dw,) = torch.autograd.grad(muon.expert_linear(x.cuda(), gw, offsets.cuda()), gw, dy.cuda())
+    for i in range(e):
+        lo, hi = offsets[i], offsets[i + 1]
+        ref.check(i, dw[i], ref.linear64(x[lo:hi], w[i], None, None, dy[lo:hi], "none")["dw"])
+
+
 def test_expert_results_do_not_depend_on_the_other_experts(muon):
     """The same rows and weight give the same bits, alone or among others of the same average load."""
     w = normal((4, 64, 128), BF16, 1, 0.1).cuda()
