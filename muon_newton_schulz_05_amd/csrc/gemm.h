@@ -97,9 +97,10 @@ template <> struct Mma<float> {
   }
 };
 
-// One operand's tile: R rows x one k-slice.
 constexpr int KB = 128;  // bytes of a k-slice's row
 
+// One operand's tile: R rows x one k-slice, loaded by NW waves (PD: slices held in
+// registers ahead of LDS where loads are not direct).
 template <typename T, int R, bool TR, int NW, int LOADS, int PD>
 struct Panel {
   static constexpr bool DIRECT = LOADS != kStaged;
@@ -170,7 +171,7 @@ struct Panel {
   }
   // Otherwise: slice kt into registers (any alignment; a chunk that is only
   // partly inside is taken element by element), then from there to LDS.
-  __device__ __forceinline__ void fetch(int kt, int k_left, int slot_, int wave, int lane) {
+  __device__ __forceinline__ void fetch(int kt, int k_left, int q, int wave, int lane) {
 #pragma unroll
     for (int u = 0; u < LI; ++u) {
       const int s = place(u, wave, lane), r = lrow(s), c = chunk(s);
@@ -180,20 +181,20 @@ struct Panel {
       if (n >= EPC) {
         __builtin_memcpy(&v, p, 16);
       } else {
-        const T* q = reinterpret_cast<const T*>(p);
+        const T* el = reinterpret_cast<const T*>(p);
 #pragma unroll
         for (int i = 0; i < EPC; ++i)
           if (i < n) {
-            if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(q[i]);
-            else v[i / 2] |= (uint32_t)q[i] << (16 * (i & 1));
+            if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(el[i]);
+            else v[i / 2] |= (uint32_t)el[i] << (16 * (i & 1));
           }
       }
-      reg[slot_][u] = v;
+      reg[q][u] = v;
     }
   }
-  __device__ __forceinline__ void put(char* st, int slot_, int wave, int lane) const {
+  __device__ __forceinline__ void put(char* st, int q, int wave, int lane) const {
 #pragma unroll
-    for (int u = 0; u < LI; ++u) *reinterpret_cast<u32x4_t*>(st + (wave + NW * u) * 1024 + lane * 16) = reg[slot_][u];
+    for (int u = 0; u < LI; ++u) *reinterpret_cast<u32x4_t*>(st + (wave + NW * u) * 1024 + lane * 16) = reg[q][u];
   }
 
   // The fragment of substep s (32 bf16 or 16 float32 of k) for rows
@@ -263,7 +264,6 @@ __device__ __forceinline__ void stripe(int t, int tiles_m, int tiles_n, int& tm,
 
 // WGM x WGN waves share a tile; WGK such sets of waves take every WGK-th k-slice
 // each, with stages of their own, and add up in the epilogue in set order.
-// PD: slices held in registers ahead of LDS where loads are not direct.
 template <typename T, int BM, int BN, int WGM, int WGN, int WGK, int NS, bool TA, bool TB, int LOADS>
 __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
           // matrix cores have work while the first fragments are read.  (Ahead of
           // the first slice these are products of zeros.)
           constexpr int RD = PA::READS * FM + PB::READS * FN, MM = FM * FN * Mma<T>::N;
-  #pragma unroll
+#pragma unroll
           for (int s = 0; s < SUB; ++s) {
             read(st, s);
             multiply(s + 1);  // of the other parity: substep s - 1
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
         for (int j = 0; j < FN; ++j)
           *reinterpret_cast<f32x4_t*>(stg + (16 * ii + (lane & 15)) * STRIDE + (16 * j + 4 * (lane >> 4)) * 4) =
               acc[2 * i + ii][j];
-    if constexpr (WGK > 1) __syncthreads();
+      if constexpr (WGK > 1) __syncthreads();
       else wave_fence();
       // One wave reads its strip back; with several sets, each set takes its share
       // of the 32 rows and adds the sets' values in order.
