@@ -68,7 +68,8 @@ typedef enum {
 } muon_linear_op_t;
 
 /* Workspace of one of the calls below, for pointers that are 16-byte
- * aligned or not (host only; 0 for many shapes). */
+ * aligned or not (host only; 0 for many shapes).  A large bf16 product of odd
+ * sizes copies its operands there. */
 int muon_linear_workspace(const muon_linear_desc_t* desc, int32_t op, uint64_t* bytes);
 
 /* z = x W + b, y = act(z) + r.  bias [max(groups, 1), n], residual (groups = 0

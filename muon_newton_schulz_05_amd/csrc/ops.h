@@ -46,6 +46,15 @@ enum GemmLoads { kStaged = 0, kDirect16, kDirect4 };
 hipError_t launch_gemm(const GemmArgs& g, int dtype, bool ta, bool tb, int loads, int tile, hipStream_t s);
 hipError_t launch_gemm_bf16(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s);
 hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s);
+// dst[g][r][0 .. ld) = src[g][r][0 .. cols) with zeros behind: a bf16 operand laid
+// out for 16-byte loads.  ld is cols rounded up to 8; one group's dst follows another's.
+struct AlignArgs {
+  const void* src;
+  void* dst;
+  int64_t rows, cols, src_ld, src_step, ld;  // src_step: from one group to the next
+  int32_t groups;
+};
+hipError_t launch_align(const AlignArgs& a, hipStream_t s);
 hipError_t launch_gemm_join(const GemmArgs& g, int dtype, hipStream_t s);
 
 // dz = dy act'(z) and the column sums of dz over each group's rows.

@@ -60,8 +60,54 @@ struct Product {
   muon::GemmArgs g{};
   int tile = muon::kTile128;
   int loads = muon::kStaged;
-  uint64_t ws = 0;
+  uint64_t ws = 0;            // partials of a split contraction
+  muon::AlignArgs copy[2]{};  // of A and B, where copy_bytes > 0
+  uint64_t copy_bytes[2] = {0, 0};
+  uint64_t total() const { return ws + copy_bytes[0] + copy_bytes[1]; }
 };
+
+// A larger bf16 product whose operands no 16-byte loads reach first copies them
+// into rows that they do, padded with zeros, which add nothing.  Without and with
+// the copies, in us (forward / dx / dW, weight [K, N]):
+//    4001 x 2001 x 4003   227 / 197 / 337    79 / 97 / 95
+//    2001 x 1001 x 2003    47 /  39 /  75    31 / 38 / 36
+//    1031 x 1001 x 1003    31 /  21 /  33    23 / 21 / 18
+//  - From 2 GFLOP on that pays, or costs nothing (513 x 2001 x 1003: 28 / 22 / 21,
+//    27 / 24 / 20), except where both operands lie along the contraction (dx here):
+//    the other loads serve those better, and it takes 8 GFLOP.
+//  - A copy has to be used often enough: 100001 x 101 x 101 (100 FLOP per byte
+//    copied) 33 and 38 forward, 64 experts of 1001 x 999 over 2000 rows (30) 84 and
+//    98, 129 x 4001 x 4003 (124) 52 and 42.  dW, whose other loads are the slowest,
+//    gains at any rate (100001 x 101 x 101: 133 and 78).
+//  - Float32 is bound by its matrix instructions either way: 583 and 556 at the
+//    first of these, 79 and 89 at the second.
+bool align_operands(Product* p, int dtype, bool ta, bool tb, const int (&have)[2], int groups) {
+  muon::GemmArgs& g = p->g;
+  const double flop = 2.0 * g.m * g.n * g.k;
+  if (dtype != MUON_BF16 || std::min({g.m, g.n, g.k}) < 64 || flop < (tb ? 2e9 : 8e9)) return false;
+  const bool t[2] = {ta, tb};
+  const int64_t rows[2] = {ta ? g.k : g.m, tb ? g.k : g.n}, cols[2] = {ta ? g.m : g.k, tb ? g.n : g.k};
+  const int64_t from[2] = {g.lda, g.ldb};
+  muon::AlignArgs c[2]{};
+  uint64_t bytes[2] = {0, 0};
+  for (int i = 0; i < 2; ++i) {
+    if (have[i] == muon::kDirect16) continue;
+    const bool each = i == 1 && !ta && groups > 0;  // a weight for each group
+    c[i] = muon::AlignArgs{nullptr, nullptr, rows[i], cols[i], from[i], each ? g.sb : 0, (cols[i] + 7) / 8 * 8,
+                           each ? groups : 1};
+    bytes[i] = (uint64_t)c[i].ld * c[i].rows * c[i].groups * 2;
+    if (loads_of(nullptr, c[i].ld, 0, t[i], c[i].ld, c[i].ld, 2) != muon::kDirect16) return false;
+  }
+  if (!ta && flop < 120.0 * (double)(bytes[0] + bytes[1])) return false;
+  for (int i = 0; i < 2; ++i) {
+    if (bytes[i] == 0) continue;
+    p->copy[i] = c[i];
+    p->copy_bytes[i] = bytes[i];
+    (i ? g.ldb : g.lda) = c[i].ld;
+    if (c[i].groups > 1) g.sb = c[i].rows * c[i].ld;
+  }
+  return true;
+}
 
 // The tile and the split of a product, by how many tiles there are for the
 // card's 256 compute units (times in us, bf16, forward / dx / dW):
@@ -151,16 +197,34 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   }
 }
 
+void plan_aligned(Product* p, int dtype, bool ta, bool tb, int la, int lb, int groups) {
+  int loads = both_loads(la, lb);
+  if (loads != muon::kDirect16 && align_operands(p, dtype, ta, tb, {la, lb}, groups)) loads = muon::kDirect16;
+  plan_product(p, dtype, ta, tb, loads, groups);
+}
+
 int run_product(Product* p, int dtype, bool ta, bool tb, void* ws, uint64_t ws_bytes, void* stream, const char* what) {
   muon::GemmArgs& g = p->g;
   if (g.m == 0 || g.n == 0) return set_error(MUON_OK, "%s", "");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (g.splits > 1) {
-    if (ws_bytes < p->ws || !ws) return bad("the workspace is smaller than muon_linear_workspace says");
+  if (p->total() > 0) {
+    if (ws_bytes < p->total() || !ws) return bad("the workspace is smaller than muon_linear_workspace says");
     if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
-    g.part = static_cast<float*>(ws);
   }
-  hipError_t e = muon::launch_gemm(g, dtype, ta, tb, p->loads, p->tile, s);
+  char* at = static_cast<char*>(ws);
+  hipError_t e = hipSuccess;
+  const void** operand[2] = {&g.a, &g.b};
+  for (int i = 0; i < 2; ++i) {
+    if (p->copy_bytes[i] == 0) continue;
+    p->copy[i].src = *operand[i];
+    p->copy[i].dst = at;
+    *operand[i] = at;
+    at += p->copy_bytes[i];
+    if (e == hipSuccess) e = muon::launch_align(p->copy[i], s);
+  }
+  if (e != hipSuccess) return hip_result(e, what);
+  if (g.splits > 1) g.part = reinterpret_cast<float*>(at);
+  e = muon::launch_gemm(g, dtype, ta, tb, p->loads, p->tile, s);
   if (e == hipSuccess && g.splits > 1) e = muon::launch_gemm_join(g, dtype, s);
   return hip_result(e, what);
 }
@@ -178,9 +242,8 @@ Product forward_product(const muon_linear_desc_t* d, const void* x, const void* 
   p.g.k = d->k;
   *tb = d->w_layout == 0;
   const int es = elem(d->dtype);
-  const int ok = both_loads(loads_of(x, d->ldx, 0, false, d->rows, d->k, es),
-                            loads_of(w, d->ldw, p.g.sb, *tb, d->n, d->k, es));
-  plan_product(&p, d->dtype, false, *tb, ok, d->groups);
+  plan_aligned(&p, d->dtype, false, *tb, loads_of(x, d->ldx, 0, false, d->rows, d->k, es),
+               loads_of(w, d->ldw, p.g.sb, *tb, d->n, d->k, es), d->groups);
   return p;
 }
 Product input_product(const muon_linear_desc_t* d, const void* dz, const void* w, bool* tb) {
@@ -195,9 +258,8 @@ Product input_product(const muon_linear_desc_t* d, const void* dz, const void* w
   p.g.k = d->n;
   *tb = d->w_layout == 1;
   const int es = elem(d->dtype);
-  const int ok = both_loads(loads_of(dz, d->ldg, 0, false, d->rows, d->n, es),
-                            loads_of(w, d->ldw, p.g.sb, *tb, d->k, d->n, es));
-  plan_product(&p, d->dtype, false, *tb, ok, d->groups);
+  plan_aligned(&p, d->dtype, false, *tb, loads_of(dz, d->ldg, 0, false, d->rows, d->n, es),
+               loads_of(w, d->ldw, p.g.sb, *tb, d->k, d->n, es), d->groups);
   return p;
 }
 Product weight_product(const muon_linear_desc_t* d, const void* x, const void* dz) {
@@ -212,9 +274,8 @@ Product weight_product(const muon_linear_desc_t* d, const void* x, const void* d
   p.g.k = d->rows;
   p.g.sc = p.g.m * p.g.n;
   const int es = elem(d->dtype);
-  const int ok = both_loads(loads_of(p.g.a, p.g.lda, 0, true, p.g.m, p.g.k, es),
-                            loads_of(p.g.b, p.g.ldb, 0, true, p.g.n, p.g.k, es));
-  plan_product(&p, d->dtype, true, true, ok, d->groups);
+  plan_aligned(&p, d->dtype, true, true, loads_of(p.g.a, p.g.lda, 0, true, p.g.m, p.g.k, es),
+               loads_of(p.g.b, p.g.ldb, 0, true, p.g.n, p.g.k, es), d->groups);
   return p;
 }
 
@@ -300,13 +361,14 @@ int muon_linear_workspace(const muon_linear_desc_t* d, int32_t op, uint64_t* byt
   // The plan depends on the pointers' alignment: the largest of the answers.
   const void* probes[3] = {nullptr, reinterpret_cast<const void*>(uintptr_t(4)),
                            reinterpret_cast<const void*>(uintptr_t(2))};
-  for (const void* q : probes) {
-    bool tb;
-    const Product p = op == MUON_LINEAR_FORWARD      ? forward_product(d, q, q, &tb)
-                      : op == MUON_LINEAR_GRAD_INPUT ? input_product(d, q, q, &tb)
-                                                     : weight_product(d, q, q);
-    *bytes = std::max(*bytes, p.ws);
-  }
+  for (const void* q : probes)
+    for (const void* r : probes) {
+      bool tb;
+      const Product p = op == MUON_LINEAR_FORWARD      ? forward_product(d, q, r, &tb)
+                        : op == MUON_LINEAR_GRAD_INPUT ? input_product(d, q, r, &tb)
+                                                       : weight_product(d, q, r);
+      *bytes = std::max(*bytes, p.total());
+    }
   return set_error(MUON_OK, "%s", "");
 }
 

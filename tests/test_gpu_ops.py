@@ -208,6 +208,43 @@ def test_linear_large_tiles_split_in_two(muon, w_t):
     ref.check("y", y[rows.cuda()], want["y"], norm_bound(BF16, k))
 
 
+@pytest.mark.parametrize("w_t", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("m,k,n", [(1031, 1001, 1003), (2001, 1001, 2003), (1201, 1000, 1003), (1537, 1023, 1336)])
+def test_linear_large_and_odd(muon, m, k, n, w_t):
+    """Products over 2 and over 8 GFLOP with one operand, or both, out of reach of 16-byte loads."""
+    run_linear(muon, m, k, n, BF16, "silu", w_t, True, True)
+
+
+@pytest.mark.parametrize("off_x,off_w", [(1, 0), (0, 1), (2, 1), (1, 1)])
+@pytest.mark.parametrize("m,k,n", [(100, 4096, 4096), (1100, 1024, 1024), (2100, 1024, 2048)])
+def test_linear_large_with_unaligned_storage(muon, m, k, n, off_x, off_w):
+    """Rows that are whole 16-byte pieces apart, but begin between them, of either operand or of both."""
+    x, w, dy = normal((m, k), BF16, 1), normal((k, n), BF16, 2, k ** -0.5), normal((m, n), BF16, 3)
+    want = ref.linear64(x, w, None, None, dy, "none")
+
+    def shifted(t, by):
+        s = torch.full((t.numel() + by,), float("nan"), dtype=BF16, device="cuda")
+        s[by:] = t.flatten().cuda()
+        return s[by:].view(t.shape).requires_grad_()
+    gx, gw = shifted(x, off_x), shifted(w, off_w)
+    y = muon.linear(gx, gw)
+    dx, dw = torch.autograd.grad(y, (gx, gw), shifted(dy, off_x).detach())
+    ref.check("y", y, want["y"], norm_bound(BF16, k))
+    ref.check("dx", dx, want["dx"], norm_bound(BF16, n))
+    ref.check("dw", dw, want["dw"], norm_bound(BF16, m))
+
+
+def test_linear_large_and_odd_keeps_infinities_in_their_rows(muon):
+    """The zeros behind a copied row meet no infinity of the other operand."""
+    x, w = normal((1031, 1001), BF16, 1), normal((1001, 1003), BF16, 2)
+    rest = [i for i in range(1031) if i not in (7, 1030)]
+    want = ref.linear64(x[rest], w, None, None, None, "none")
+    x[7], x[1030, 1000] = float("inf"), float("nan")
+    y = muon.linear(x.cuda(), w.cuda()).cpu()
+    assert not y[7].isfinite().any() and y[1030].isnan().all()
+    ref.check("y", y[rest], want["y"])
+
+
 # ------------------------------------------------------------------ experts
 
 LOADS = {"even": [40, 40, 40], "empty": [0, 130, 0, 0, 7, 0], "one": [300], "single": [1, 0, 1, 1, 257, 2],
@@ -252,6 +289,27 @@ def test_experts_large_tiles(muon, counts):
     for i in range(e):
         lo, hi = offsets[i], offsets[i + 1]
         want = ref.linear64(x[lo:hi], w[i], b[i], None, dy[lo:hi], "gelu")
+        for name, got in (("y", y[lo:hi]), ("dx", dx[lo:hi]), ("dw", dw[i]), ("db", db[i])):
+            ref.check((name, i), got, want[name], norm_bound(BF16, 1) if hi > lo else None)
+
+
+@pytest.mark.parametrize("w_t", [False, True], ids=["kn", "nk"])
+def test_experts_large_and_odd(muon, w_t):
+    """Over 8 GFLOP of odd sizes, experts without rows, and rows past the last one that hold no numbers."""
+    counts, tail, k, n = [2100, 0, 1301, 1, 700], 33, 1001, 999
+    e, used = len(counts), sum(counts)
+    offsets = torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    x, dy = normal((used + tail, k), BF16, 1), normal((used + tail, n), BF16, 2)
+    x[used:], dy[used:] = float("nan"), float("inf")
+    w, b = normal((e, n, k) if w_t else (e, k, n), BF16, 3, k ** -0.5), normal((e, n), BF16, 4)
+    g = [t.cuda().requires_grad_() for t in (x, w, b)]
+    y = muon.expert_linear(g[0], g[1].transpose(1, 2) if w_t else g[1], offsets.cuda(), g[2], activation="gelu")
+    dx, dw, db = torch.autograd.grad(y, g, dy.cuda())
+    dw = dw.transpose(1, 2) if w_t else dw
+    assert not y[used:].any() and not dx[used:].any()
+    for i in range(e):
+        lo, hi = offsets[i], offsets[i + 1]
+        want = ref.linear64(x[lo:hi], w[i].t() if w_t else w[i], b[i], None, dy[lo:hi], "gelu")
         for name, got in (("y", y[lo:hi]), ("dx", dx[lo:hi]), ("dw", dw[i]), ("db", db[i])):
             ref.check((name, i), got, want[name], norm_bound(BF16, 1) if hi > lo else None)
 

@@ -114,6 +114,30 @@ def test_linear_split_needs_its_workspace(ops):
     assert lib.muon_linear_forward(ctypes.byref(d), None, q, q, None, None, q, None, q, 16, None) == INVALID
 
 
+def test_linear_copies_need_their_workspace(ops):
+    """A large odd product lays out both operands anew; a smaller one, and float32, need nothing."""
+    lib, q = ops.load_ops(), 4096
+    odd = dict(rows=2001, k=1001, n=2003, ldx=1001, ldw=2003, ldg=2003)
+    d, need = _desc(ops, **odd), ctypes.c_uint64(0)
+    assert lib.muon_linear_workspace(ctypes.byref(d), 0, ctypes.byref(need)) == 0
+    assert need.value >= 2 * (2001 * 1008 + 1001 * 2008)
+    f = lib.muon_linear_forward
+    assert f(ctypes.byref(d), None, q, q, None, None, q, None, None, 0, None) == INVALID
+    assert f(ctypes.byref(d), None, q, q, None, None, q, None, q, need.value - 1, None) == INVALID
+    assert f(ctypes.byref(d), None, q, q, None, None, q, None, q + 8, need.value, None) == INVALID
+    for other in (dict(odd, dtype=0), dict(odd, rows=65)):
+        assert lib.muon_linear_workspace(ctypes.byref(_desc(ops, **other)), 0, ctypes.byref(need)) == 0
+        assert need.value < 2 * 1001 * 2008
+
+
+def test_linear_workspace_covers_one_unaligned_operand(ops):
+    """x alone out of reach is copied where both together are not: the larger need is told."""
+    lib, need = ops.load_ops(), ctypes.c_uint64(0)
+    d = _desc(ops, rows=100, k=4096, n=4096, ldx=4096, ldw=4096)
+    assert lib.muon_linear_workspace(ctypes.byref(d), 0, ctypes.byref(need)) == 0
+    assert 2 * 100 * 4096 <= need.value
+
+
 def test_route_refuses(ops):
     lib, q = ops.load_ops(), 4096
     need = ctypes.c_uint64(0)
