@@ -95,7 +95,8 @@ int muon_linear_grad_weight(const muon_linear_desc_t* desc, const int32_t* offse
                             void* dw, void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* The three steps above in one call: dx, dw and db, each NULL where not wanted,
- * from x, W, z and dy; dz stays in the workspace. */
+ * from x, W, z and dy; dz stays in the workspace.  For up to 64 bf16 rows dz
+ * keeps what its rounding loses, which the three steps alone do not. */
 int muon_linear_backward(const muon_linear_desc_t* desc, const int32_t* offsets, const void* x, const void* w,
                          const void* z, const void* dy, void* dx, void* dw, void* db, void* workspace,
                          uint64_t workspace_bytes, void* stream);

@@ -535,7 +535,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
         }
         const int64_t row = row0 + wm * WM + 32 * i + lr;
         if (pr < ROWS && row < end && n_in > 0) {
-          if (g.part) store8(g.part + (((int64_t)split * g.groups + e) * g.m + row) * g.n + col, n, v);
+          if (g.part) store8(g.part + (((int64_t)split * (GK ? g.groups : 1) + (GK ? e : 0)) * g.m + row) * g.n + col, n, v);
           else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);
         }
       }
@@ -558,7 +558,8 @@ __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs g) {
   float v[8] = {}, bias[8] = {};
   for (int s = 0; s < g.splits; ++s) {
     float p[8];
-    load8(g.part + ((int64_t)s * rows + row) * g.n + col, n, p);
+    const int64_t at = g.pairs ? 2 * ((s >> 1) * rows + row) + (s & 1) : s * rows + row;
+    load8(g.part + at * g.n + col, n, p);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += p[k];
   }

@@ -69,6 +69,8 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
   const int cols = (int)((a.n + 511) / 512);
   const int blk = blockIdx.x / cols, cb = blockIdx.x - blk * cols;
   int e = 0, lo = 0, hi = 0;
+  if (a.offsets2 && blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= a.groups; i += 256) a.offsets2[i] = 2 * min(max(a.offsets[i], 0), (int)a.rows);
   if (a.offsets) {
     const GroupBlocks gb(a.offsets, a.groups, a.rows, a.block);
     if (blk >= gb.total) return;
@@ -105,7 +107,18 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
         }
-        if (a.dz) store8(static_cast<T*>(a.dz) + (int64_t)r * a.lddz + col, FULL ? 8 : n, v[u]);
+        if (a.dz) store8(static_cast<T*>(a.dz) + (int64_t)(r << a.pairs) * a.lddz + col, FULL ? 8 : n, v[u]);
+        if constexpr (sizeof(T) == 2) {
+          if (a.pairs) {
+            float lost[8];  // nothing where the value, or its rounding, is not finite
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float d = v[u][i] - from_bf16(to_bf16(v[u][i]));
+              lost[i] = fabsf(d) < __builtin_huge_valf() ? d : 0.f;
+            }
+            store8(static_cast<T*>(a.dz) + (int64_t)(2 * r + 1) * a.lddz + col, FULL ? 8 : n, lost);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] += v[u][i];
       }

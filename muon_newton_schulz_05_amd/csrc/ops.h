@@ -34,6 +34,7 @@ struct GemmArgs {
   int64_t k_per;           // contraction of one split (a multiple of 64); a grouped
                            // contraction's splits go by each group's length
   int32_t tiles_m, tiles_n;
+  int32_t pairs;           // join: row r of the result is the sum of rows 2r and 2r + 1
   int32_t share;           // grouped contraction: XCDs that share a group's tiles; 0: all
 };
 
@@ -68,6 +69,8 @@ struct ActGradArgs {
   const int32_t* offsets;
   int32_t groups, act;
   int32_t block;           // rows of one block (launch_act_grad sets it)
+  int32_t pairs;           // bf16: dz rounded in row 2r of dz, and what that lost in row 2r + 1
+  int32_t* offsets2;       // pairs of grouped rows: where the offsets of dz's rows go
 };
 int64_t act_grad_blocks(int64_t rows, int64_t n, int32_t groups, bool grouped);
 hipError_t launch_act_grad(const ActGradArgs& a, int dtype, hipStream_t s);

@@ -63,6 +63,7 @@ struct Product {
   uint64_t ws = 0;            // partials of a split contraction
   muon::AlignArgs copy[2]{};  // of A and B, where copy_bytes > 0
   uint64_t copy_bytes[2] = {0, 0};
+  bool pairs = false;         // rows 2r and 2r + 1 are added to one row of C
   uint64_t total() const { return ws + copy_bytes[0] + copy_bytes[1]; }
 };
 
@@ -223,8 +224,14 @@ int run_product(Product* p, int dtype, bool ta, bool tb, void* ws, uint64_t ws_b
     if (e == hipSuccess) e = muon::launch_align(p->copy[i], s);
   }
   if (e != hipSuccess) return hip_result(e, what);
-  if (g.splits > 1) g.part = reinterpret_cast<float*>(at);
+  if (g.splits > 1 || p->pairs) g.part = reinterpret_cast<float*>(at);
   e = muon::launch_gemm(g, dtype, ta, tb, p->loads, p->tile, s);
+  if (p->pairs) {
+    g.m /= 2;
+    g.groups = 1;
+    g.splits *= 2;
+    g.pairs = 1;
+  }
   if (e == hipSuccess && g.splits > 1) e = muon::launch_gemm_join(g, dtype, s);
   return hip_result(e, what);
 }
@@ -290,6 +297,45 @@ int check_ptr(const muon_linear_desc_t* d, const void* p, int64_t count, const c
   if (!aligned(p, elem(d->dtype))) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", name);
   return MUON_OK;
 }
+// A bf16 layer's dz is rounded to bf16 for the products that follow, like every
+// operand of the matrix instructions: dx and dW are then about 1.4 times as far
+// off in the norm as their own rounding, which for a few rows may be 1.9 times
+// (an error that few values share is not averaged).  Up to 64 rows, where the
+// products wait for the weight, what the rounding lost is kept too: dz has two rows
+// for each, the rounded one and the rest, dx adds the pairs of its rows in float32,
+// and dW multiplies each row of x twice.  The whole backward pass without and with:
+// 1 x 4096 x 16384 77 and 81 us, 16 x 4096 x 4096 40 and 44, 64 x 1024 x 4096 30
+// and 39; 128 x 4096 x 16384 would take 124 and 167.
+constexpr int64_t kPairRows = 64;
+struct Pairs {
+  bool on = false;
+  muon_linear_desc_t d{};            // the layer of twice the rows
+  muon::AlignArgs x{};               // each row of x twice
+  uint64_t dz = 0, x2 = 0, offsets = 0;  // bytes, multiples of 16
+  uint64_t bytes() const { return dz + x2 + offsets; }
+};
+Pairs pairs_of(const muon_linear_desc_t* d) {
+  Pairs q;
+  q.on = d->dtype == MUON_BF16 && d->act != MUON_ACT_NONE && d->rows > 0 && d->rows <= kPairRows && d->k > 0 && d->n > 0;
+  if (!q.on) return q;
+  q.x = muon::AlignArgs{nullptr, nullptr, 2, d->k, 0, d->ldx, (d->k + 7) / 8 * 8, (int32_t)d->rows};
+  q.d = *d;
+  q.d.rows = 2 * d->rows;
+  q.d.ldg = d->n;
+  q.d.ldx = q.x.ld;
+  q.dz = ((uint64_t)q.d.rows * d->n * 2 + 15) / 16 * 16;
+  q.x2 = (uint64_t)q.d.rows * q.x.ld * 2;
+  q.offsets = d->groups > 0 ? ((uint64_t)d->groups * 4 + 4 + 15) / 16 * 16 : 0;
+  return q;
+}
+// The input gradient of a layer of pairs.
+Product pairs_input(const Pairs& q, const void* dz, const void* w, bool* tb) {
+  Product p = input_product(&q.d, dz, w, tb);
+  p.pairs = true;
+  p.ws = (uint64_t)p.g.splits * p.g.m * p.g.n * 4;
+  return p;
+}
+
 // dz of a layer with an activation, as part of a workspace.
 uint64_t dz_bytes(const muon_linear_desc_t* d) {
   return d->act == MUON_ACT_NONE ? 0 : ((uint64_t)d->rows * d->n * elem(d->dtype) + 15) / 16 * 16;
@@ -347,6 +393,18 @@ int muon_linear_workspace(const muon_linear_desc_t* d, int32_t op, uint64_t* byt
     // dz, then one area that the three steps use in turn.
     uint64_t most = 0, b = 0;
     muon_linear_desc_t dd = *d;
+    const Pairs q = pairs_of(d);
+    if (q.on) {
+      MUON_TRY(muon_linear_workspace(d, MUON_LINEAR_GRAD_ACT, &most));
+      MUON_TRY(muon_linear_workspace(&q.d, MUON_LINEAR_GRAD_WEIGHT, &b));
+      most = std::max(most, b);
+      for (uintptr_t w : {0, 4, 2}) {
+        bool tb;
+        most = std::max(most, pairs_input(q, nullptr, reinterpret_cast<const void*>(w), &tb).total());
+      }
+      *bytes = q.bytes() + most;
+      return set_error(MUON_OK, "%s", "");
+    }
     for (int32_t step : {MUON_LINEAR_GRAD_ACT, MUON_LINEAR_GRAD_INPUT, MUON_LINEAR_GRAD_WEIGHT}) {
       for (int64_t ld : {d->ldg, d->n}) {
         dd.ldg = ld;
@@ -398,8 +456,8 @@ int muon_linear_forward(const muon_linear_desc_t* d, const int32_t* offsets, con
   return run_product(&p, d->dtype, false, tb, ws, ws_bytes, stream, "muon_linear_forward");
 }
 
-int muon_linear_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const void* dy, const void* z, void* dz,
-                         void* db, void* ws, uint64_t ws_bytes, void* stream) {
+static int grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const void* dy, const void* z, void* dz,
+                    int32_t* offsets2, bool pairs, void* db, void* ws, uint64_t ws_bytes, void* stream) {
   MUON_TRY(check_desc(d));
   MUON_TRY(check_offsets(d, offsets));
   MUON_TRY(check_ptr(d, dy, d->rows * d->n, "dy"));
@@ -420,6 +478,8 @@ int muon_linear_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, co
   a.offsets = offsets;
   a.groups = std::max(d->groups, 1);
   a.act = d->act;
+  a.pairs = pairs;
+  a.offsets2 = offsets2;
   if (db) {
     const uint64_t need = (uint64_t)muon::act_grad_blocks(d->rows, d->n, a.groups, offsets != nullptr) * d->n * 4;
     if (need > ws_bytes || (need && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
@@ -427,6 +487,11 @@ int muon_linear_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, co
     a.part = static_cast<float*>(ws);
   }
   return hip_result(muon::launch_act_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_linear_grad_act");
+}
+
+int muon_linear_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const void* dy, const void* z, void* dz,
+                         void* db, void* ws, uint64_t ws_bytes, void* stream) {
+  return grad_act(d, offsets, dy, z, dz, nullptr, false, db, ws, ws_bytes, stream);
 }
 
 int muon_linear_grad_input(const muon_linear_desc_t* d, const int32_t* offsets, const void* dz, const void* w, void* dx,
@@ -458,6 +523,37 @@ int muon_linear_grad_weight(const muon_linear_desc_t* d, const int32_t* offsets,
   return run_product(&p, d->dtype, true, true, ws, ws_bytes, stream, "muon_linear_grad_weight");
 }
 
+static int backward_pairs(const Pairs& q, const muon_linear_desc_t* d, const int32_t* offsets, const void* x,
+                          const void* w, const void* z, const void* dy, void* dx, void* dw, void* db, void* ws,
+                          uint64_t ws_bytes, void* stream) {
+  if (ws_bytes < q.bytes() || !ws) return bad("the workspace is smaller than muon_linear_workspace says");
+  MUON_TRY(check_offsets(d, offsets));
+  char *dz = static_cast<char*>(ws), *x2 = dz + q.dz, *rest = x2 + q.x2 + q.offsets;
+  int32_t* offsets2 = offsets ? reinterpret_cast<int32_t*>(x2 + q.x2) : nullptr;
+  ws_bytes -= q.bytes();
+  MUON_TRY(grad_act(d, offsets, dy, z, dz, offsets2, true, db, rest, ws_bytes, stream));
+  if (dx) {
+    MUON_TRY(check_ptr(d, w, d->k * d->n, "w"));
+    MUON_TRY(check_ptr(d, dx, d->rows * d->k, "dx"));
+    bool tb;
+    Product p = pairs_input(q, dz, w, &tb);
+    p.g.offsets = offsets2;
+    p.g.c = dx;
+    p.g.ldc = d->k;
+    MUON_TRY(run_product(&p, d->dtype, false, tb, rest, ws_bytes, stream, "muon_linear_backward"));
+  }
+  if (dw) {
+    MUON_TRY(check_ptr(d, x, d->rows * d->k, "x"));
+    muon::AlignArgs twice = q.x;
+    twice.src = x;
+    twice.dst = x2;
+    const hipError_t e = muon::launch_align(twice, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_result(e, "muon_linear_backward");
+    MUON_TRY(muon_linear_grad_weight(&q.d, offsets2, x2, dz, dw, rest, ws_bytes, stream));
+  }
+  return set_error(MUON_OK, "%s", "");
+}
+
 int muon_linear_backward(const muon_linear_desc_t* d, const int32_t* offsets, const void* x, const void* w,
                          const void* z, const void* dy, void* dx, void* dw, void* db, void* ws, uint64_t ws_bytes,
                          void* stream) {
@@ -465,6 +561,10 @@ int muon_linear_backward(const muon_linear_desc_t* d, const int32_t* offsets, co
   const uint64_t dzb = (dx || dw) ? dz_bytes(d) : 0;
   if (dzb > ws_bytes || (dzb && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
   if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
+  if (dx || dw) {
+    const Pairs q = pairs_of(d);
+    if (q.on) return backward_pairs(q, d, offsets, x, w, z, dy, dx, dw, db, ws, ws_bytes, stream);
+  }
   char* rest = static_cast<char*>(ws) + (ws ? dzb : 0);
   muon_linear_desc_t dd = *d;
   const void* dz = dy;

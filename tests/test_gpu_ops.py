@@ -245,6 +245,54 @@ def test_linear_large_and_odd_keeps_infinities_in_their_rows(muon):
     ref.check("y", y[rest], want["y"])
 
 
+def few_rows_bounds(x, w, z, dy, act):
+    """dx and dw of a layer whose z is given, and their tolerances where dz is carried to twice bf16's digits."""
+    u, x, w, z, dy = ref.unit(BF16), *(t.double() for t in (x, w, z, dy))
+    dz = dy * ref.act64(z, act)[1]
+    # dz: the slope in float32, the rest after two roundings; float32 sums of 2 (rows or columns) products; one rounding.
+    edz = 16 * ref.U32 * dy.abs() + u * u * dz.abs()
+    out = {}
+    for name, v, far, size, terms in (("dx", dz @ w.t(), edz @ w.abs().t(), dz.abs() @ w.abs().t(), w.shape[1]),
+                                      ("dw", x.t() @ dz, x.abs().t() @ edz, x.abs().t() @ dz.abs(), x.shape[0])):
+        err = far + (2 * terms + 4) * ref.U32 * size
+        out[name] = v, err + u * (v.abs() + err) + 1e-37
+    return out
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("m,k,n,w_t", [(1, 1656, 64, True), (1, 24, 4096, False), (3, 37, 21, False), (17, 520, 264, True),
+                                       (64, 2048, 24, False), (63, 65, 1001, True), (64, 512, 1024, False)])
+def test_linear_gradients_of_few_rows(muon, m, k, n, w_t, act):
+    """Up to 64 rows the gradient of the activation loses nothing that dx and dw keep."""
+    x, w, dy = normal((m, k), BF16, 1), normal((n, k) if w_t else (k, n), BF16, 2, k ** -0.5), normal((m, n), BF16, 3)
+    gx, gw = x.cuda(), w.cuda().t() if w_t else w.cuda()
+    w = w.t() if w_t else w
+    z = muon.linear_forward(gx, gw, activation=act, keep_z=True)[1]
+    dx, dw, db = muon.linear_backward(dy.cuda(), gx, gw, z, act)
+    want = few_rows_bounds(x, w, z.cpu(), dy, act)
+    ref.check("dx", dx, want["dx"])
+    ref.check("dw", dw, want["dw"])
+    for needs in ((True, False, False), (False, True, False)):
+        one = muon.linear_backward(dy.cuda(), gx, gw, z, act, needs=needs)
+        assert all(torch.equal(a, b) for a, b, need in zip(one, (dx, dw, db), needs) if need)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 3.3895e38])
+def test_linear_gradients_of_few_rows_keep_infinities(muon, bad):
+    """What a rounding lost is nothing where the value is not finite: an infinite gradient stays one."""
+    x, w, dy = normal((5, 16), BF16, 1).abs() + 1, normal((16, 8), BF16, 2).abs() + 1, normal((5, 8), BF16, 3)
+    dy[2, 4] = bad
+    gx, gw = x.cuda(), w.cuda()
+    z = torch.full((5, 8), 0.75, dtype=BF16, device="cuda")
+    dx, dw, db = (t.cpu() for t in muon.linear_backward(dy.cuda(), gx, gw, z, "silu"))
+    dz = dy.double() * ref.act64(z.cpu().double(), "silu")[1]
+    assert dx[[0, 1, 3, 4]].isfinite().all() and dw[:, [0, 1, 2, 3, 5, 6, 7]].isfinite().all()
+    for got, want in ((dx[2], (dz @ w.double().t())[2]), (dw[:, 4], (x.double().t() @ dz)[:, 4])):
+        want = want.to(BF16)                                # past the type's range where dz is that large
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[got.isinf()], want[got.isinf()])
+        assert torch.equal(got.isinf(), want.isinf())
+
+
 # ------------------------------------------------------------------ experts
 
 LOADS = {"even": [40, 40, 40], "empty": [0, 130, 0, 0, 7, 0], "one": [300], "single": [1, 0, 1, 1, 257, 2],
@@ -274,6 +322,27 @@ def test_experts(muon, load, k, n, w_t, tail, dtype):
         want = ref.linear64(x[lo:hi], w[i].t() if w_t else w[i], b[i], None, dy[lo:hi], "silu")
         for name, got in (("y", y[lo:hi]), ("dx", dx[lo:hi]), ("dw", dw[i]), ("db", db[i])):
             ref.check((name, i), got, want[name])
+
+
+@pytest.mark.parametrize("counts,tail", [([1], 0), ([0, 3, 0, 1, 50], 5), ([0, 0], 7), ([1] * 60, 0), ([20, 40, 4], 0)],
+                         ids=["one", "uneven", "none", "many", "all"])
+@pytest.mark.parametrize("k,n,w_t", [(64, 72, False), (37, 21, True), (640, 552, False)])
+def test_experts_gradients_of_few_rows(muon, counts, tail, k, n, w_t):
+    e, used = len(counts), sum(counts)
+    offsets = torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    x, dy = normal((used + tail, k), BF16, 1), normal((used + tail, n), BF16, 2)
+    x[used:], dy[used:] = float("nan"), float("inf")
+    w = normal((e, n, k) if w_t else (e, k, n), BF16, 3, k ** -0.5)
+    gx, gw, off = x.cuda(), w.cuda().transpose(1, 2) if w_t else w.cuda(), offsets.cuda()
+    w = w.transpose(1, 2) if w_t else w
+    z = muon.linear_forward(gx, gw, activation="gelu", offsets=off, keep_z=True)[1]
+    dx, dw, _ = muon.linear_backward(dy.cuda(), gx, gw, z, "gelu", offsets=off)
+    assert not dx[used:].any()
+    for i in range(e):
+        lo, hi = offsets[i], offsets[i + 1]
+        want = few_rows_bounds(x[lo:hi], w[i], z[lo:hi].cpu(), dy[lo:hi], "gelu")
+        ref.check(("dx", i), dx[lo:hi], want["dx"])
+        ref.check(("dw", i), dw[i], want["dw"])
 
 
 @pytest.mark.parametrize("counts", [[700, 0, 513, 256, 900, 2000], [1400, 1400, 1400, 300]], ids=["skewed", "few"])

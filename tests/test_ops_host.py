@@ -138,6 +138,22 @@ def test_linear_workspace_covers_one_unaligned_operand(ops):
     assert 2 * 100 * 4096 <= need.value
 
 
+def test_linear_backward_needs_its_workspace(ops):
+    """Up to 64 rows: two rows of dz for each, each row of x twice, and dx in float32; more rows keep one."""
+    lib, q, need = ops.load_ops(), 4096, ctypes.c_uint64(0)
+    d = _desc(ops, act=2, rows=64, k=24, n=72, ldx=24, ldw=72, ldg=72)
+    assert lib.muon_linear_workspace(ctypes.byref(d), 4, ctypes.byref(need)) == 0
+    assert need.value >= 2 * 64 * (2 * 72 + 2 * 24 + 4 * 24)
+    f = lib.muon_linear_backward
+    assert f(ctypes.byref(d), None, q, q, q, q, q, q, q, None, 0, None) == INVALID
+    assert f(ctypes.byref(d), None, q, q, q, q, q, q, q, q, 64, None) == INVALID
+    assert f(ctypes.byref(d), None, q, q, q, q, q, q, q, q + 8, need.value, None) == INVALID
+    for other in (dict(rows=65), dict(act=0), dict(dtype=0)):
+        o = _desc(ops, **{**dict(act=2, rows=64, k=24, n=72, ldx=24, ldw=72, ldg=72), **other})
+        assert lib.muon_linear_workspace(ctypes.byref(o), 4, ctypes.byref(need)) == 0
+        assert need.value < 2 * 64 * (2 * 72 + 2 * 24 + 4 * 24)
+
+
 def test_route_refuses(ops):
     lib, q = ops.load_ops(), 4096
     need = ctypes.c_uint64(0)
