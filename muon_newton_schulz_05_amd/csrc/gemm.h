@@ -548,20 +548,29 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
 
 // Joins a split contraction: the partials of an entry are added in split
 // order, then the epilogue runs as in the kernel above.  The groups' results
-// lie one behind the other, as rows of one matrix.
+// lie one behind the other, as rows of one matrix.  Of a pair of rows, what the
+// second holds corrects the first's last digits.  Where the first is not finite (an
+// infinite operand, say) there is nothing to correct, and the second, whose
+// infinities need not have the first's sign, would turn it into NaN.
 template <typename T>
 __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs g) {
   const int64_t per = (g.n + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = g.m * g.groups;
   if (i >= per * rows) return;
   const int64_t row = i / per;
   const int col = (int)(i - row * per) * 8, n = (int)min((int64_t)8, g.n - col);
-  float v[8] = {}, bias[8] = {};
+  float v[8] = {}, rest[8] = {}, bias[8] = {};
   for (int s = 0; s < g.splits; ++s) {
     float p[8];
+    const bool second = g.pairs && (s & 1);
     const int64_t at = g.pairs ? 2 * ((s >> 1) * rows + row) + (s & 1) : s * rows + row;
     load8(g.part + at * g.n + col, n, p);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += p[k];
+    for (int k = 0; k < 8; ++k) (second ? rest[k] : v[k]) += p[k];
+  }
+  if (g.pairs) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (fabsf(v[k]) < __builtin_huge_valf()) v[k] += rest[k];
   }
   if (g.bias) load8(static_cast<const T*>(g.bias) + col, n, bias);
   finish8<T>(g, v, bias, 0, row, col, n);

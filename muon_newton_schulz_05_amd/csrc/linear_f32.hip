@@ -191,6 +191,10 @@ __global__ __launch_bounds__(256) void k_align(AlignArgs a) {
   float v[8];  // bf16 to float and back is exact
   load8(static_cast<const uint16_t*>(a.src) + e * a.src_step + (row - e * a.rows) * a.src_ld + col,
         (int)min((int64_t)8, a.cols - col), v);
+  if (a.pairs && (row & 1)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fabsf(v[i]) < __builtin_huge_valf() ? v[i] : 0.f;
+  }
   store8(static_cast<uint16_t*>(a.dst) + row * a.ld + col, 8, v);
 }
 

@@ -34,7 +34,7 @@ struct GemmArgs {
   int64_t k_per;           // contraction of one split (a multiple of 64); a grouped
                            // contraction's splits go by each group's length
   int32_t tiles_m, tiles_n;
-  int32_t pairs;           // join: row r of the result is the sum of rows 2r and 2r + 1
+  int32_t pairs;           // join: row r of the result is row 2r and, where that is finite, row 2r + 1
   int32_t share;           // grouped contraction: XCDs that share a group's tiles; 0: all
 };
 
@@ -49,11 +49,12 @@ hipError_t launch_gemm_bf16(const GemmArgs& g, bool ta, bool tb, int loads, int 
 hipError_t launch_gemm_f32(const GemmArgs& g, bool ta, bool tb, int loads, int tile, hipStream_t s);
 // dst[g][r][0 .. ld) = src[g][r][0 .. cols) with zeros behind: a bf16 operand laid
 // out for 16-byte loads.  ld is cols rounded up to 8; one group's dst follows another's.
+// pairs: odd rows of dst take zeros where src is not finite.
 struct AlignArgs {
   const void* src;
   void* dst;
   int64_t rows, cols, src_ld, src_step, ld;  // src_step: from one group to the next
-  int32_t groups;
+  int32_t groups, pairs;
 };
 hipError_t launch_align(const AlignArgs& a, hipStream_t s);
 hipError_t launch_gemm_join(const GemmArgs& g, int dtype, hipStream_t s);

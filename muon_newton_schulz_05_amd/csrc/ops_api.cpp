@@ -95,7 +95,7 @@ bool align_operands(Product* p, int dtype, bool ta, bool tb, const int (&have)[2
     if (have[i] == muon::kDirect16) continue;
     const bool each = i == 1 && !ta && groups > 0;  // a weight for each group
     c[i] = muon::AlignArgs{nullptr, nullptr, rows[i], cols[i], from[i], each ? g.sb : 0, (cols[i] + 7) / 8 * 8,
-                           each ? groups : 1};
+                           each ? groups : 1, 0};
     bytes[i] = (uint64_t)c[i].ld * c[i].rows * c[i].groups * 2;
     if (loads_of(nullptr, c[i].ld, 0, t[i], c[i].ld, c[i].ld, 2) != muon::kDirect16) return false;
   }
@@ -303,7 +303,9 @@ int check_ptr(const muon_linear_desc_t* d, const void* p, int64_t count, const c
 // (an error that few values share is not averaged).  Up to 64 rows, where the
 // products wait for the weight, what the rounding lost is kept too: dz has two rows
 // for each, the rounded one and the rest, dx adds the pairs of its rows in float32,
-// and dW multiplies each row of x twice.  The whole backward pass without and with:
+// and dW multiplies each row of x twice.  An infinite operand meets the rounded row
+// alone: dx drops the rest of a sum that is not finite, and the row of x for the
+// rest has zeros there.  The whole backward pass without and with:
 // 1 x 4096 x 16384 77 and 81 us, 16 x 4096 x 4096 40 and 44, 64 x 1024 x 4096 30
 // and 39; 128 x 4096 x 16384 would take 124 and 167.
 constexpr int64_t kPairRows = 64;
@@ -318,7 +320,7 @@ Pairs pairs_of(const muon_linear_desc_t* d) {
   Pairs q;
   q.on = d->dtype == MUON_BF16 && d->act != MUON_ACT_NONE && d->rows > 0 && d->rows <= kPairRows && d->k > 0 && d->n > 0;
   if (!q.on) return q;
-  q.x = muon::AlignArgs{nullptr, nullptr, 2, d->k, 0, d->ldx, (d->k + 7) / 8 * 8, (int32_t)d->rows};
+  q.x = muon::AlignArgs{nullptr, nullptr, 2, d->k, 0, d->ldx, (d->k + 7) / 8 * 8, (int32_t)d->rows, 1};
   q.d = *d;
   q.d.rows = 2 * d->rows;
   q.d.ldg = d->n;

@@ -1,0 +1,69 @@
+"""GPU tests of the layer operators' edges: non-finite operands, the tails of the activations, paths that only
+unusual shapes reach, several streams and threads, against the plain float64 forms of tests/ops_reference.py."""
+
+from __future__ import annotations
+
+import itertools
+
+import pytest
+import torch
+
+import ops_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
+
+
+@pytest.fixture(scope="module")
+def muon():
+    import muon_newton_schulz_05_amd as pkg
+    return pkg
+
+
+def normal(shape, dtype, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(dtype)
+
+
+def same_non_finite(got, want):
+    """Infinities and NaN in the same places, of the same sign."""
+    got, want = got.double().cpu(), want.to(got.dtype).double()
+    assert torch.equal(got.isnan(), want.isnan())
+    bad = want.isinf()
+    assert torch.equal(got.isinf(), bad) and torch.equal(got[bad], want[bad])
+
+
+# ------------------------------------------------------------------ infinite operands of a gradient
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("rows", [1, 5, 64, 65, 200])
+def test_linear_gradients_of_infinite_operands(muon, rows, act):
+    """x and W that hold infinities and NaN give the dx and dW that the formula gives, for any number of rows."""
+    k, n = 24, 40
+    x, w, dy = normal((rows, k), BF16, 1), normal((k, n), BF16, 2), normal((rows, n), BF16, 3)
+    z = normal((rows, n), BF16, 4).abs() + 0.25             # a slope that is not zero
+    dz = dy.double() * ref.act64(z.double(), act)[1]
+    x[0, 3], x[0, 7], x[rows - 1, 20] = float("inf"), float("nan"), -float("inf")
+    w[2, 1], w[9, 30], w[9, 31], w[20, 5] = float("inf"), -float("inf"), float("inf"), float("nan")
+    dx, dw, _ = muon.linear_backward(dy.cuda(), x.cuda(), w.cuda(), z.cuda(), act)
+    same_non_finite(dx, dz @ w.double().t())
+    same_non_finite(dw, x.double().t() @ dz)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu"])
+@pytest.mark.parametrize("counts", [[3, 0, 5, 1], [30, 2, 30, 2]], ids=["few", "all"])
+def test_experts_gradients_of_infinite_operands(muon, counts, act):
+    e, k, n, rows = len(counts), 24, 40, sum(counts)
+    offsets = torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    x, w, dy = normal((rows, k), BF16, 1), normal((e, k, n), BF16, 2), normal((rows, n), BF16, 3)
+    z = normal((rows, n), BF16, 4).abs() + 0.25
+    x[0, 3], x[rows - 1, 20], w[2, 2, 1], w[0, 9, 30] = float("inf"), -float("inf"), float("inf"), -float("inf")
+    dx, dw, _ = muon.linear_backward(dy.cuda(), x.cuda(), w.cuda(), z.cuda(), act, offsets=offsets.cuda())
+    dz = dy.double() * ref.act64(z.double(), act)[1]
+    for i in range(e):
+        lo, hi = offsets[i], offsets[i + 1]
+        same_non_finite(dx[lo:hi], dz[lo:hi] @ w[i].double().t())
+        same_non_finite(dw[i], x[lo:hi].double().t() @ dz[lo:hi])
