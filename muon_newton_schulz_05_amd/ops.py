@@ -13,7 +13,9 @@ caching allocator on the current stream, and ties the calls to autograd.
 Tensors are float32 or bfloat16, on one GPU, on the current torch stream.  Rows
 may be strided; a tensor whose last dimension is not contiguous is copied
 first.  The ``*_forward`` and ``*_backward`` functions are the same passes without
-autograd, for code that captures them into a HIP graph.
+autograd, for code that captures them into a HIP graph: they take a tensor's value alone,
+whether it requires a gradient or carries a tangent.  The others are differentiable
+backwards, once; forward-mode differentiation raises.
 """
 
 from __future__ import annotations
@@ -23,6 +25,7 @@ import math
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import MUON_BF16, MUON_F32, MUON_OK, MuonError, load_library, muon_last_error
 
@@ -324,6 +327,10 @@ class _Linear(torch.autograd.Function):
 
 
 def _tracked(*tensors):
+    """Whether a call goes through its autograd function: for its gradient or, with forward-mode
+    differentiation on, because torch refuses a tangent there (it would be dropped otherwise)."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:
+        return True
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
