@@ -15,13 +15,15 @@ may be strided; a tensor whose last dimension is not contiguous is copied
 first.  The ``*_forward`` and ``*_backward`` functions are the same passes without
 autograd, for code that captures them into a HIP graph: they take a tensor's value alone,
 whether it requires a gradient or carries a tangent.  The others are differentiable
-backwards, once; forward-mode differentiation raises.
+backwards, once; forward-mode differentiation raises, and so do tracers (``make_fx``,
+``torch.jit.trace``), which cannot see the kernels.
 """
 
 from __future__ import annotations
 
 import ctypes
 import math
+import sys
 from typing import NamedTuple
 
 import torch
@@ -134,8 +136,26 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_jit_tracing, _modes, _key_on = torch._C._is_tracing, torch._C._len_torch_dispatch_stack, \
+    torch._C._dispatch_tls_is_dispatch_key_included
+_PRE_DISPATCH = torch._C.DispatchKey.PreDispatch
+
+
+def _traced():
+    """Whether torch.jit.trace or an fx tracer is recording.  An fx tracer is asked for only where some dispatch mode
+    is on, which takes under a microsecond to see; other modes (a FLOP counter, say) are no tracers."""
+    if _jit_tracing():
+        return True
+    if not (_modes() or _key_on(_PRE_DISPATCH)):
+        return False
+    tracer = sys.modules.get("torch.fx.experimental.proxy_tensor")
+    return tracer is not None and tracer.get_proxy_mode() is not None
+
+
 def _call(name, t, *args):
     """The C function on t's device and current stream."""
+    if _traced():
+        raise RuntimeError(f"{name} cannot be traced: a tracer would record its outputs' allocation alone")
     index = t.get_device()
     f = getattr(_ops or load_ops(), name)
     if index == torch.cuda.current_device():

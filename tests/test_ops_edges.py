@@ -55,3 +55,25 @@ def test_forward_mode_is_refused(on_cpu, monkeypatch, name, grad):
         x, ys = (forward_ad.make_dual(torch.randn(n, 8), torch.ones(n, 8)) for n in (3, 6))
         with pytest.raises((RuntimeError, NotImplementedError), match="forward"):
             operator_calls(on_cpu, x, ys)[name]()
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("how", ["make_fx", "make_fx, pre-dispatch", "jit.trace"])
+def test_tracing_is_refused(on_cpu, name, how):
+    """A tracer sees none of the kernels: it would record a program that returns memory nobody wrote."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    x, ys = torch.randn(3, 8), torch.randn(6, 8)
+
+    def program(x, ys):
+        return operator_calls(on_cpu, x, ys)[name]()
+    with pytest.raises(RuntimeError, match="cannot be traced"):
+        if how == "jit.trace":
+            torch.jit.trace(program, (x, ys))
+        else:
+            make_fx(program, pre_dispatch=how != "make_fx")(x, ys)
+
+
+def test_tracing_of_a_sort_is_refused(on_cpu):
+    from torch.fx.experimental.proxy_tensor import make_fx
+    with pytest.raises(RuntimeError, match="cannot be traced"):
+        make_fx(lambda ids: on_cpu.route(ids, 4).order)(torch.zeros(3, 2, dtype=torch.int64))
