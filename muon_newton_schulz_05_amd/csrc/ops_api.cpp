@@ -22,6 +22,12 @@ int hip_result(hipError_t e, const char* what) {
   return set_error(MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+#define MUON_TRY(x)                   \
+  do {                                \
+    const int rc_ = (x);              \
+    if (rc_ != MUON_OK) return rc_;   \
+  } while (0)
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int elem(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 
@@ -65,6 +71,7 @@ struct Product {
   uint64_t copy_bytes[2] = {0, 0};
   bool pairs = false;         // rows 2r and 2r + 1 are added to one row of C
   uint64_t total() const { return ws + copy_bytes[0] + copy_bytes[1]; }
+  uint64_t need() const { return g.m == 0 || g.n == 0 ? 0 : total(); }  // nothing to compute: nothing is used
 };
 
 // A larger bf16 product whose operands no 16-byte loads reach first copies them
@@ -204,14 +211,17 @@ void plan_aligned(Product* p, int dtype, bool ta, bool tb, int la, int lb, int g
   plan_product(p, dtype, ta, tb, loads, groups);
 }
 
-int run_product(Product* p, int dtype, bool ta, bool tb, void* ws, uint64_t ws_bytes, void* stream, const char* what) {
+int check_workspace(uint64_t need, const void* ws, uint64_t ws_bytes) {
+  if (ws_bytes < need || (need && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
+  if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
+  return MUON_OK;
+}
+
+// A product whose pointers and workspace have been checked.
+int run_product(Product* p, int dtype, bool ta, bool tb, void* ws, void* stream, const char* what) {
   muon::GemmArgs& g = p->g;
   if (g.m == 0 || g.n == 0) return set_error(MUON_OK, "%s", "");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (p->total() > 0) {
-    if (ws_bytes < p->total() || !ws) return bad("the workspace is smaller than muon_linear_workspace says");
-    if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
-  }
   char* at = static_cast<char*>(ws);
   hipError_t e = hipSuccess;
   const void** operand[2] = {&g.a, &g.b};
@@ -341,12 +351,10 @@ Product pairs_input(const Pairs& q, const void* dz, const void* w, bool* tb) {
 // dz of a layer with an activation, as part of a workspace.
 uint64_t dz_bytes(const muon_linear_desc_t* d) {
   return d->act == MUON_ACT_NONE ? 0 : ((uint64_t)d->rows * d->n * elem(d->dtype) + 15) / 16 * 16;
+}// The column sums of the activation's gradient, by blocks of rows.
+uint64_t col_sum_bytes(const muon_linear_desc_t* d) {
+  return (uint64_t)muon::act_grad_blocks(d->rows, d->n, std::max(d->groups, 1), d->groups > 0) * d->n * 4;
 }
-#define MUON_TRY(x)                   \
-  do {                                \
-    const int rc_ = (x);              \
-    if (rc_ != MUON_OK) return rc_;   \
-  } while (0)
 
 int check_move(const muon_move_desc_t* d) {
   if (!d) return bad("desc is null");
@@ -388,7 +396,7 @@ int muon_linear_workspace(const muon_linear_desc_t* d, int32_t op, uint64_t* byt
   *bytes = 0;
   MUON_TRY(check_desc(d));
   if (op == MUON_LINEAR_GRAD_ACT) {
-    *bytes = (uint64_t)muon::act_grad_blocks(d->rows, d->n, std::max(d->groups, 1), d->groups > 0) * d->n * 4;
+    *bytes = col_sum_bytes(d);
     return set_error(MUON_OK, "%s", "");
   }
   if (op == MUON_LINEAR_BACKWARD) {
@@ -455,23 +463,25 @@ int muon_linear_forward(const muon_linear_desc_t* d, const int32_t* offsets, con
   p.g.ldr = d->ldr;
   p.g.sbias = d->n;
   p.g.act = d->act;
-  return run_product(&p, d->dtype, false, tb, ws, ws_bytes, stream, "muon_linear_forward");
+  MUON_TRY(check_workspace(p.need(), ws, ws_bytes));
+  return run_product(&p, d->dtype, false, tb, ws, stream, "muon_linear_forward");
 }
 
-static int grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const void* dy, const void* z, void* dz,
-                    int32_t* offsets2, bool pairs, void* db, void* ws, uint64_t ws_bytes, void* stream) {
-  MUON_TRY(check_desc(d));
-  MUON_TRY(check_offsets(d, offsets));
+// The activation's gradient: its checks, and its launch.
+static int check_grad_act(const muon_linear_desc_t* d, const void* dy, const void* z, const void* dz, const void* db) {
   MUON_TRY(check_ptr(d, dy, d->rows * d->n, "dy"));
   MUON_TRY(check_ptr(d, z, d->act != MUON_ACT_NONE ? d->rows * d->n : 0, "z"));
   MUON_TRY(check_ptr(d, dz, 0, "dz"));
-  MUON_TRY(check_ptr(d, db, 0, "db"));
-  if (!dz && !db) return set_error(MUON_OK, "%s", "");
+  return check_ptr(d, db, 0, "db");
+}
+static int run_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const void* dy, const void* z, void* dz,
+                        int32_t* offsets2, bool pairs, void* db, void* ws, void* stream, const char* what) {
   muon::ActGradArgs a{};
   a.dy = dy;
   a.z = d->act != MUON_ACT_NONE ? z : nullptr;
   a.dz = dz;
   a.db = db;
+  a.part = static_cast<float*>(ws);
   a.rows = d->rows;
   a.n = d->n;
   a.lddy = d->ldg;
@@ -482,18 +492,17 @@ static int grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const v
   a.act = d->act;
   a.pairs = pairs;
   a.offsets2 = offsets2;
-  if (db) {
-    const uint64_t need = (uint64_t)muon::act_grad_blocks(d->rows, d->n, a.groups, offsets != nullptr) * d->n * 4;
-    if (need > ws_bytes || (need && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
-    if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
-    a.part = static_cast<float*>(ws);
-  }
-  return hip_result(muon::launch_act_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_linear_grad_act");
+  return hip_result(muon::launch_act_grad(a, d->dtype, static_cast<hipStream_t>(stream)), what);
 }
 
 int muon_linear_grad_act(const muon_linear_desc_t* d, const int32_t* offsets, const void* dy, const void* z, void* dz,
                          void* db, void* ws, uint64_t ws_bytes, void* stream) {
-  return grad_act(d, offsets, dy, z, dz, nullptr, false, db, ws, ws_bytes, stream);
+  MUON_TRY(check_desc(d));
+  MUON_TRY(check_offsets(d, offsets));
+  MUON_TRY(check_grad_act(d, dy, z, dz, db));
+  if (!dz && !db) return set_error(MUON_OK, "%s", "");
+  if (db) MUON_TRY(check_workspace(col_sum_bytes(d), ws, ws_bytes));
+  return run_grad_act(d, offsets, dy, z, dz, nullptr, false, db, ws, stream, "muon_linear_grad_act");
 }
 
 int muon_linear_grad_input(const muon_linear_desc_t* d, const int32_t* offsets, const void* dz, const void* w, void* dx,
@@ -505,10 +514,11 @@ int muon_linear_grad_input(const muon_linear_desc_t* d, const int32_t* offsets, 
   MUON_TRY(check_ptr(d, dx, d->rows * d->k, "dx"));
   bool tb;
   Product p = input_product(d, dz, w, &tb);
+  MUON_TRY(check_workspace(p.need(), ws, ws_bytes));
   p.g.offsets = offsets;
   p.g.c = dx;
   p.g.ldc = d->k;
-  return run_product(&p, d->dtype, false, tb, ws, ws_bytes, stream, "muon_linear_grad_input");
+  return run_product(&p, d->dtype, false, tb, ws, stream, "muon_linear_grad_input");
 }
 
 int muon_linear_grad_weight(const muon_linear_desc_t* d, const int32_t* offsets, const void* x, const void* dz, void* dw,
@@ -519,65 +529,64 @@ int muon_linear_grad_weight(const muon_linear_desc_t* d, const int32_t* offsets,
   MUON_TRY(check_ptr(d, dz, d->rows * d->n, "dz"));
   MUON_TRY(check_ptr(d, dw, d->k * d->n, "dw"));
   Product p = weight_product(d, x, dz);
+  MUON_TRY(check_workspace(p.need(), ws, ws_bytes));
   p.g.offsets = offsets;
   p.g.c = dw;
   p.g.ldc = p.g.n;
-  return run_product(&p, d->dtype, true, true, ws, ws_bytes, stream, "muon_linear_grad_weight");
-}
-
-static int backward_pairs(const Pairs& q, const muon_linear_desc_t* d, const int32_t* offsets, const void* x,
-                          const void* w, const void* z, const void* dy, void* dx, void* dw, void* db, void* ws,
-                          uint64_t ws_bytes, void* stream) {
-  if (ws_bytes < q.bytes() || !ws) return bad("the workspace is smaller than muon_linear_workspace says");
-  MUON_TRY(check_offsets(d, offsets));
-  char *dz = static_cast<char*>(ws), *x2 = dz + q.dz, *rest = x2 + q.x2 + q.offsets;
-  int32_t* offsets2 = offsets ? reinterpret_cast<int32_t*>(x2 + q.x2) : nullptr;
-  ws_bytes -= q.bytes();
-  MUON_TRY(grad_act(d, offsets, dy, z, dz, offsets2, true, db, rest, ws_bytes, stream));
-  if (dx) {
-    MUON_TRY(check_ptr(d, w, d->k * d->n, "w"));
-    MUON_TRY(check_ptr(d, dx, d->rows * d->k, "dx"));
-    bool tb;
-    Product p = pairs_input(q, dz, w, &tb);
-    p.g.offsets = offsets2;
-    p.g.c = dx;
-    p.g.ldc = d->k;
-    MUON_TRY(run_product(&p, d->dtype, false, tb, rest, ws_bytes, stream, "muon_linear_backward"));
-  }
-  if (dw) {
-    MUON_TRY(check_ptr(d, x, d->rows * d->k, "x"));
-    muon::AlignArgs twice = q.x;
-    twice.src = x;
-    twice.dst = x2;
-    const hipError_t e = muon::launch_align(twice, static_cast<hipStream_t>(stream));
-    if (e != hipSuccess) return hip_result(e, "muon_linear_backward");
-    MUON_TRY(muon_linear_grad_weight(&q.d, offsets2, x2, dz, dw, rest, ws_bytes, stream));
-  }
-  return set_error(MUON_OK, "%s", "");
+  return run_product(&p, d->dtype, true, true, ws, stream, "muon_linear_grad_weight");
 }
 
 int muon_linear_backward(const muon_linear_desc_t* d, const int32_t* offsets, const void* x, const void* w,
                          const void* z, const void* dy, void* dx, void* dw, void* db, void* ws, uint64_t ws_bytes,
                          void* stream) {
+  const char* what = "muon_linear_backward";
   MUON_TRY(check_desc(d));
-  const uint64_t dzb = (dx || dw) ? dz_bytes(d) : 0;
-  if (dzb > ws_bytes || (dzb && !ws)) return bad("the workspace is smaller than muon_linear_workspace says");
-  if (!aligned(ws, 16)) return bad("the workspace is not 16-byte aligned");
-  if (dx || dw) {
-    const Pairs q = pairs_of(d);
-    if (q.on) return backward_pairs(q, d, offsets, x, w, z, dy, dx, dw, db, ws, ws_bytes, stream);
+  if (!dx && !dw && !db) return set_error(MUON_OK, "%s", "");
+  MUON_TRY(check_offsets(d, offsets));
+  MUON_TRY(check_grad_act(d, dy, z, nullptr, db));
+  MUON_TRY(check_ptr(d, dx, 0, "dx"));
+  MUON_TRY(check_ptr(d, dw, 0, "dw"));
+  if (dx) MUON_TRY(check_ptr(d, w, d->k * d->n, "w"));
+  if (dw) MUON_TRY(check_ptr(d, x, d->rows * d->k, "x"));
+  const bool products = dx || dw;
+  const Pairs q = products ? pairs_of(d) : Pairs{};
+  const uint64_t head = !products ? 0 : q.on ? q.bytes() : dz_bytes(d);
+
+  // The workspace: dz, with pairs of rows x twice and the offsets of the pairs, then an area that the steps use in turn.
+  char* const at = static_cast<char*>(ws);
+  char* const x2 = q.on ? at + q.dz : nullptr;
+  int32_t* const offsets2 = q.on && offsets ? reinterpret_cast<int32_t*>(x2 + q.x2) : nullptr;
+  char* const rest = ws ? at + head : nullptr;
+  const void* dz = head ? ws : dy;
+  muon_linear_desc_t dd = q.on ? q.d : *d;
+  if (head) dd.ldg = d->n;
+  const int32_t* const off = q.on ? offsets2 : offsets;
+  Product pi, pw;
+  bool tb = false;
+  if (dx) pi = q.on ? pairs_input(q, dz, w, &tb) : input_product(&dd, dz, w, &tb);
+  if (dw) pw = weight_product(&dd, q.on ? x2 : x, dz);
+  const uint64_t most = std::max({db ? col_sum_bytes(d) : 0, dx ? pi.need() : 0, dw ? pw.need() : 0});
+  MUON_TRY(check_workspace(head + most, ws, ws_bytes));
+
+  if (head || db) MUON_TRY(run_grad_act(d, offsets, dy, z, head ? ws : nullptr, offsets2, q.on, db, rest, stream, what));
+  if (dx) {
+    pi.g.offsets = off;
+    pi.g.c = dx;
+    pi.g.ldc = d->k;
+    MUON_TRY(run_product(&pi, d->dtype, false, tb, rest, stream, what));
   }
-  char* rest = static_cast<char*>(ws) + (ws ? dzb : 0);
-  muon_linear_desc_t dd = *d;
-  const void* dz = dy;
-  if (dzb || db)
-    MUON_TRY(muon_linear_grad_act(d, offsets, dy, z, dzb ? ws : nullptr, db, rest, ws_bytes - dzb, stream));
-  if (dzb) {
-    dz = ws;
-    dd.ldg = d->n;
+  if (dw) {
+    if (q.on) {
+      muon::AlignArgs twice = q.x;
+      twice.src = x;
+      twice.dst = x2;
+      MUON_TRY(hip_result(muon::launch_align(twice, static_cast<hipStream_t>(stream)), what));
+    }
+    pw.g.offsets = off;
+    pw.g.c = dw;
+    pw.g.ldc = pw.g.n;
+    MUON_TRY(run_product(&pw, d->dtype, true, true, rest, stream, what));
   }
-  if (dx) MUON_TRY(muon_linear_grad_input(&dd, offsets, dz, w, dx, rest, ws_bytes - dzb, stream));
-  if (dw) MUON_TRY(muon_linear_grad_weight(&dd, offsets, x, dz, dw, rest, ws_bytes - dzb, stream));
   return set_error(MUON_OK, "%s", "");
 }
 

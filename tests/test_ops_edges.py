@@ -2,6 +2,7 @@
 
 from __future__ import annotations
 
+import ctypes
 import os
 
 import pytest
@@ -77,3 +78,47 @@ def test_tracing_of_a_sort_is_refused(on_cpu):
     from torch.fx.experimental.proxy_tensor import make_fx
     with pytest.raises(RuntimeError, match="cannot be traced"):
         make_fx(lambda ids: on_cpu.route(ids, 4).order)(torch.zeros(3, 2, dtype=torch.int64))
+
+
+def _desc(ops, **kw):
+    d = dict(dtype=1, act=2, groups=0, w_layout=0, rows=4, k=8, n=8, ldx=0, ldw=0, w_stride=0, ldr=8, ldg=0)
+    d.update(kw)
+    d.update(ldx=d["k"], ldw=d["n"], ldg=d["n"])
+    return ops.LinearDesc(*[d[f[0]] for f in ops.LinearDesc._fields_])
+
+
+# What a call that got past its checks says here, where there is no GPU to launch on.
+LAUNCHED = 3
+BACKWARD_SHAPES = [dict(rows=4), dict(rows=64, k=64, n=16384), dict(rows=200, k=64, n=16384), dict(rows=2100, k=1001, n=2003),
+                   dict(rows=300, act=0, k=64, n=4096), dict(dtype=0, rows=300, k=640, n=520),
+                   dict(rows=40, groups=3, w_stride=64), dict(rows=4000, groups=3, k=64, n=72, w_stride=64 * 72)]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are made up: nothing may be launched on them")
+@pytest.mark.parametrize("kw", BACKWARD_SHAPES, ids=str)
+def test_backward_checks_before_it_launches(ops, kw):
+    """Whatever is wrong with a pointer or the workspace is said before the first launch, for any outputs asked for."""
+    lib, d, need = ops.load_ops(), _desc(ops, **kw), ctypes.c_uint64(0)
+    assert lib.muon_linear_workspace(ctypes.byref(d), 4, ctypes.byref(need)) == 0
+    a = 1 << 32                                              # never read
+
+    def call(offsets=a if d.groups else None, x=a, w=a, z=a, dy=a, dx=a, dw=a, db=a, ws=a, size=need.value):
+        return lib.muon_linear_backward(ctypes.byref(d), offsets, x, w, z, dy, dx, dw, db, ws, size, None)
+    assert call() == LAUNCHED
+    bad = [dict(w=None), dict(x=None), dict(dy=None), dict(w=a + 1), dict(x=a + 1), dict(dy=a + 1), dict(dx=a + 1),
+           dict(dw=a + 1), dict(db=a + 1), dict(offsets=None if d.groups else a), dict(ws=a + 8)]
+    bad += [dict(z=None)] if d.act else []
+    bad += [dict(ws=None), dict(size=0)] if need.value else []
+    for one in bad:
+        assert call(**one) == INVALID, one
+    # Only what the asked outputs need has to be there.
+    assert call(x=None, dw=None) == LAUNCHED and call(w=None, dx=None) == LAUNCHED
+    assert call(x=None, w=None, dx=None, dw=None) == LAUNCHED
+    # One byte less than is told is too little for pointers of some alignment, and no pointers need more.
+    worst = [call(x=a + p, w=a + q, dy=a + r, size=max(need.value - 1, 0)) for p in (0, 4) for q in (0, 4) for r in (0, 4)]
+    if d.dtype == 1:
+        worst += [call(x=a + p, w=a + q, dy=a + r, size=max(need.value - 1, 0)) for p in (0, 2) for q in (0, 2)
+                  for r in (0, 2)]
+    assert set(worst) <= {INVALID, LAUNCHED} and (INVALID in worst or not need.value)
+    for off in (0, 4):
+        assert call(x=a + off, w=a + off, dy=a + off) == LAUNCHED
