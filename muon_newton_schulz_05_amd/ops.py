@@ -435,6 +435,8 @@ def _check_routing(routing, t, rows, what):
     if t.shape[0] != rows:
         raise ValueError(f"{what} has {t.shape[0]} rows, expected {rows}")
     p, o = routing.position, routing.offsets
+    if o.device != p.device:
+        raise ValueError(f"the routing's offsets are on {o.device}, its positions on {p.device}")
     if p.dim() != 2 or p.dtype is not torch.int32 or o.dtype is not torch.int32 or not p.is_contiguous() \
             or not o.is_contiguous() or o.dim() != 1 or o.shape[0] < 2:
         raise ValueError("routing must be what route() returned")

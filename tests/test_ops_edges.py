@@ -122,3 +122,27 @@ def test_backward_checks_before_it_launches(ops, kw):
     assert set(worst) <= {INVALID, LAUNCHED} and (INVALID in worst or not need.value)
     for off in (0, 4):
         assert call(x=a + off, w=a + off, dy=a + off) == LAUNCHED
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it lives on a GPU and has no memory: for the binding's checks."""
+
+    @staticmethod
+    def __new__(cls, *shape, dtype=torch.float32):
+        return torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device="cuda")
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise NotImplementedError(str(func))
+
+
+def test_routing_with_offsets_on_the_host_is_refused(ops):
+    """The kernels would read them through a host pointer."""
+    r = ops.Routing(torch.tensor([0, 3, 6], dtype=torch.int32), Elsewhere(6, dtype=torch.int32),
+                    Elsewhere(3, 2, dtype=torch.int32))
+    x, ys, w = Elsewhere(3, 8), Elsewhere(6, 8), Elsewhere(3, 2)
+    for call in [lambda: ops.dispatch(x, r), lambda: ops.dispatch_forward(x, r), lambda: ops.dispatch_backward(ys, r),
+                 lambda: ops.combine(ys, r, w), lambda: ops.combine_forward(ys, r, w),
+                 lambda: ops.combine_backward(x, ys, r, w)]:
+        with pytest.raises(ValueError, match="offsets"):
+            call()
