@@ -43,8 +43,8 @@ typedef enum {
  * apart, and calls take `offsets`, groups + 1 int32 on the device, non
  * decreasing from 0 to <= rows: rows offsets[e] .. offsets[e + 1] meet weight e;
  * rows past offsets[groups] give zero.  (Offsets that break this give
- * unspecified values, never an access outside the tensors.)  Strides are in elements; a row's elements are
- * contiguous. */
+ * unspecified values, never an access outside the tensors.)  Sizes go up to 2^31 - 1024.  Strides are in
+ * elements; a row's elements are contiguous. */
 typedef struct {
   int32_t dtype;     /* muon_dtype_t of x, W, b, r, y, z and their gradients */
   int32_t act;       /* muon_act_t                                            */

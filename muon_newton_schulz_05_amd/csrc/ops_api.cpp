@@ -14,6 +14,8 @@ namespace {
 using muon::set_error;
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// A layer's kernels count rows in 32 bits and step up to one block (256 rows) past their end.
+constexpr int64_t kMaxLayer = (int64_t(1) << 31) - 1024;
 constexpr int kCus = 256;
 
 int bad(const char* what) { return set_error(MUON_ERR_INVALID_ARGUMENT, "%s", what); }
@@ -37,8 +39,8 @@ int check_desc(const muon_linear_desc_t* d) {
   if (d->act < MUON_ACT_NONE || d->act > MUON_ACT_GELU_TANH) return bad("unknown activation");
   if (d->groups < 0 || d->groups > 65535) return bad("groups outside [0, 65535]");
   if (d->w_layout != 0 && d->w_layout != 1) return bad("w_layout must be 0 or 1");
-  if (d->rows < 0 || d->k < 0 || d->n < 0 || d->rows > kMaxDim || d->k > kMaxDim || d->n > kMaxDim)
-    return bad("a size is negative or over 2^31 - 1");
+  if (d->rows < 0 || d->k < 0 || d->n < 0 || d->rows > kMaxLayer || d->k > kMaxLayer || d->n > kMaxLayer)
+    return bad("a size is negative or over 2^31 - 1024");
   if (d->ldx < 0 || d->ldw < 0 || d->w_stride < 0 || d->ldr < 0 || d->ldg < 0) return bad("a stride is negative");
   return MUON_OK;
 }

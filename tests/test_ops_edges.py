@@ -146,3 +146,16 @@ def test_routing_with_offsets_on_the_host_is_refused(ops):
                  lambda: ops.combine_backward(x, ys, r, w)]:
         with pytest.raises(ValueError, match="offsets"):
             call()
+
+
+@pytest.mark.parametrize("size", ["rows", "k", "n"])
+def test_linear_sizes_end_short_of_32_bits(ops, size):
+    """The kernels step a block past a size in 32 bits: the last sizes below 2^31 are refused."""
+    lib, need = ops.load_ops(), ctypes.c_uint64(0)
+    for value, rc in (((1 << 31) - 1024, 0), ((1 << 31) - 1023, INVALID), ((1 << 31) - 1, INVALID)):
+        d = _desc(ops, **{**dict(rows=1, k=1, n=1), size: value})
+        for op in range(5):
+            assert lib.muon_linear_workspace(ctypes.byref(d), op, ctypes.byref(need)) == rc, (value, op)
+        if rc:
+            a = 1 << 32
+            assert lib.muon_linear_backward(ctypes.byref(d), None, a, a, a, a, a, a, a, a, 1 << 40, None) == INVALID
