@@ -85,6 +85,11 @@ __device__ __forceinline__ void group_range(const int32_t* offsets, int groups, 
   hi = e == groups ? r : max(lo, min(offsets[e + 1], r));
 }
 
+// A sum of block counts.  Groups that overlap, by offsets that do not ascend, can
+// have more blocks than 32 bits hold: the sum then stays at a bound that no valid
+// offsets reach.
+__device__ __forceinline__ int add_blocks(int a, int b) { return min(a + b, (1 << 30) - 1); }
+
 // Every group's rows cut into blocks of `block`: each lane counts its share of the
 // groups' blocks, and a wave-wide prefix sum places the shares.  Results are
 // uniform over the wave.
@@ -101,19 +106,20 @@ struct GroupBlocks {
     for (int i = e0; i < e1; ++i) {
       int lo, hi;
       group_range(offsets, groups, rows, i, lo, hi);
-      count += (hi - lo + block - 1) / block;
+      count = add_blocks(count, (hi - lo + block - 1) / block);
     }
     int incl = count;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += v;
+      if (lane >= d) incl = add_blocks(incl, v);
     }
     before = incl - count;
     total = __builtin_amdgcn_readlane(incl, 63);
   }
 
-  // The group e of block b (0 <= b < total), its first row and its group's end.
+  // The group e of block b (0 <= b < total), its first row and its group's end; no rows
+  // where offsets that do not ascend leave the block without a group.
   __device__ __forceinline__ void find(const int32_t* offsets, int groups, int64_t rows, int block, int b, int& e,
                                        int& row0, int& end) const {
     int left = b - before, fe = 0, f0 = 0, f1 = 0;
@@ -133,7 +139,7 @@ struct GroupBlocks {
         left -= c;
       }
     }
-    const int src = __builtin_ctzll(hit);
+    const int src = hit ? __builtin_ctzll(hit) : 0;
     e = __builtin_amdgcn_readlane(fe, src);
     row0 = __builtin_amdgcn_readlane(f0, src);
     end = __builtin_amdgcn_readlane(f1, src);

@@ -299,8 +299,9 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
     // The grid is an upper bound: what the groups really fill is counted here, so
     // that every XCD gets its share of it.
     const GroupBlocks gb(g.offsets, g.groups, g.m, BM);
-    if (b >= gb.total * g.tiles_n) return;  // uniform, before any barrier
-    stripe(xcd_place(b, gb.total * g.tiles_n), gb.total, g.tiles_n, tm, tn);
+    const int total = min(gb.total, g.tiles_m);  // the bound itself, where offsets do not ascend
+    if (b >= total * g.tiles_n) return;          // uniform, before any barrier
+    stripe(xcd_place(b, total * g.tiles_n), total, g.tiles_n, tm, tn);
     int lo, hi;
     gb.find(g.offsets, g.groups, g.m, BM, tm, e, lo, hi);
     row0 = lo;

@@ -151,16 +151,16 @@ __global__ __launch_bounds__(256) void k_col_join(ActGradArgs a, int blocks) {
       int lo, hi;
       group_range(a.offsets, a.groups, a.rows, i, lo, hi);
       const int k = (hi - lo + a.block - 1) / a.block;
-      if (i < e) before += k;
+      if (i < e) before = add_blocks(before, k);
       else mine = k;
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) {
-      before += __shfl_xor(before, d, 64);
-      mine += __shfl_xor(mine, d, 64);
+      before = add_blocks(before, __shfl_xor(before, d, 64));
+      mine = add_blocks(mine, __shfl_xor(mine, d, 64));
     }
     b0 = min(before, blocks);
-    b1 = min(before + mine, blocks);
+    b1 = min(add_blocks(before, mine), blocks);
   }
   float s = 0.f;
   if (c < a.n) {

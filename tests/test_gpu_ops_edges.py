@@ -67,3 +67,23 @@ def test_experts_gradients_of_infinite_operands(muon, counts, act):
         lo, hi = offsets[i], offsets[i + 1]
         same_non_finite(dx[lo:hi], dz[lo:hi] @ w[i].double().t())
         same_non_finite(dw[i], x[lo:hi].double().t() @ dz[lo:hi])
+
+
+# ------------------------------------------------------------------ offsets that do not ascend
+
+
+def test_experts_with_overlapping_offsets_stay_inside(muon):
+    """Half of 65535 experts claim every row, more blocks than 32 bits count: values are unspecified, what follows
+    is not touched."""
+    e, rows, k, n = 65535, (1 << 22) + 64, 8, 8
+    x, w, b = (normal(s, BF16, i).cuda() for i, s in enumerate(((rows, k), (e, k, n), (e, n))))
+    bad = torch.zeros(e + 1, dtype=torch.int32)
+    bad[1::2] = rows
+    y, z = muon.linear_forward(x, w, b, "silu", offsets=bad.cuda(), keep_z=True)
+    dx, _, db = muon.linear_backward(y, x, w, z, "silu", offsets=bad.cuda(), needs=(True, False, True))
+    assert y.shape == (rows, n) and dx.shape == x.shape and db.shape == (e, n)
+    torch.cuda.synchronize()
+    good = torch.full((e + 1,), 64, dtype=torch.int32)
+    good[0] = 0
+    y = muon.linear_forward(x[:64], w, b, "silu", offsets=good.cuda())[0].cpu()
+    ref.check("y", y, ref.linear64(x[:64].cpu(), w[0].cpu(), b[0].cpu(), None, None, "silu")["y"])
