@@ -159,3 +159,14 @@ def test_linear_sizes_end_short_of_32_bits(ops, size):
         if rc:
             a = 1 << 32
             assert lib.muon_linear_backward(ctypes.byref(d), None, a, a, a, a, a, a, a, a, 1 << 40, None) == INVALID
+
+
+def test_backward_of_few_rows_carries_the_rest_of_dz_where_there_is_one(ops):
+    """relu's slope is 0 or 1: dz is exact in bf16, and takes no more than for many rows."""
+    lib, need = ops.load_ops(), ctypes.c_uint64(0)
+
+    def bytes_of(**kw):
+        assert lib.muon_linear_workspace(ctypes.byref(_desc(ops, rows=64, k=24, n=72, **kw)), 4, ctypes.byref(need)) == 0
+        return need.value
+    assert bytes_of(act=2) >= 2 * 64 * (2 * 72 + 2 * 24)
+    assert bytes_of(act=1) < 2 * 64 * 72 + 64 * 72
