@@ -95,8 +95,10 @@ int muon_linear_grad_weight(const muon_linear_desc_t* desc, const int32_t* offse
                             void* dw, void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* The three steps above in one call: dx, dw and db, each NULL where not wanted,
- * from x, W, z and dy; dz stays in the workspace.  For up to 64 bf16 rows dz
- * keeps what its rounding loses, which the three steps alone do not. */
+ * from x, W, z and dy; dz stays in the workspace.  In bf16 dz is rounded for the
+ * products, so that dx and dW carry one rounding more than their own; up to 64 rows,
+ * or 16 for each group on average, what that loses is kept and added, which the three
+ * steps alone do not do. */
 int muon_linear_backward(const muon_linear_desc_t* desc, const int32_t* offsets, const void* x, const void* w,
                          const void* z, const void* dy, void* dx, void* dw, void* db, void* workspace,
                          uint64_t workspace_bytes, void* stream);

@@ -312,15 +312,20 @@ int check_ptr(const muon_linear_desc_t* d, const void* p, int64_t count, const c
 // A bf16 layer's dz is rounded to bf16 for the products that follow, like every
 // operand of the matrix instructions: dx and dW are then about 1.4 times as far
 // off in the norm as their own rounding, which for a few rows may be 1.9 times
-// (an error that few values share is not averaged).  Up to 64 rows, where the
-// products wait for the weight, what the rounding lost is kept too: dz has two rows
-// for each, the rounded one and the rest, dx adds the pairs of its rows in float32,
-// and dW multiplies each row of x twice.  An infinite operand meets the rounded row
-// alone: dx drops the rest of a sum that is not finite, and the row of x for the
-// rest has zeros there.  (relu's slope is 0 or 1: its dz loses nothing.)  The whole backward pass without and with:
-// 1 x 4096 x 16384 77 and 81 us, 16 x 4096 x 4096 40 and 44, 64 x 1024 x 4096 30
-// and 39; 128 x 4096 x 16384 would take 124 and 167.
-constexpr int64_t kPairRows = 64;
+// (an error that few values share is not averaged).  Where a weight meets few rows,
+// and the products wait for the weight, what the rounding lost is kept too: dz has
+// two rows for each, the rounded one and the rest, dx adds the pairs of its rows in
+// float32, and dW multiplies each row of x twice.  An infinite operand meets the
+// rounded row alone: dx drops the rest of a sum that is not finite, and the row of x
+// for the rest has zeros there.  (relu's slope is 0 or 1: its dz loses nothing.)
+// The whole backward pass without and with, in us:
+//  - one weight, up to 64 rows: 1 x 4096 x 16384 77 and 81, 16 x 4096 x 4096 40 and 44,
+//    64 x 1024 x 4096 30 and 39; 128 x 4096 x 16384 would take 124 and 167.
+//  - experts, up to 16 rows each on average (the host knows no more): 64 x [2048,
+//    1408] with 2 rows each 217 and 226, with 16 245 and 262; with 32 it would be 251
+//    and 302, with 64 288 and 358.  16 x [1024, 1024] with 16: 36 and 42, with 32 36 and 51.
+//    An expert with few rows among experts with many has its dz rounded like theirs.
+constexpr int64_t kPairRows = 64, kPairRowsEach = 16;
 struct Pairs {
   bool on = false;
   muon_linear_desc_t d{};            // the layer of twice the rows
@@ -330,7 +335,8 @@ struct Pairs {
 };
 Pairs pairs_of(const muon_linear_desc_t* d) {
   Pairs q;
-  q.on = d->dtype == MUON_BF16 && d->act > MUON_ACT_RELU && d->rows > 0 && d->rows <= kPairRows && d->k > 0 && d->n > 0;
+  q.on = d->dtype == MUON_BF16 && d->act > MUON_ACT_RELU && d->rows > 0 && d->k > 0 && d->n > 0 &&
+         d->rows <= std::max(kPairRows, kPairRowsEach * d->groups);
   if (!q.on) return q;
   q.x = muon::AlignArgs{nullptr, nullptr, 2, d->k, 0, d->ldx, (d->k + 7) / 8 * 8, (int32_t)d->rows, 1};
   q.d = *d;

@@ -87,3 +87,40 @@ def test_experts_with_overlapping_offsets_stay_inside(muon):
     good[0] = 0
     y = muon.linear_forward(x[:64], w, b, "silu", offsets=good.cuda())[0].cpu()
     ref.check("y", y, ref.linear64(x[:64].cpu(), w[0].cpu(), b[0].cpu(), None, None, "silu")["y"])
+
+
+# ------------------------------------------------------------------ the accuracy of an expert's gradient
+
+
+def experts_backward(muon, counts, k, n, act):
+    e, rows = len(counts), sum(counts)
+    offsets = torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    x, w, dy = normal((rows, k), BF16, 1), normal((e, k, n), BF16, 2, k ** -0.5), normal((rows, n), BF16, 3)
+    z = muon.linear_forward(x.cuda(), w.cuda(), activation=act, offsets=offsets.cuda(), keep_z=True)[1]
+    dx, dw, _ = muon.linear_backward(dy.cuda(), x.cuda(), w.cuda(), z, act, offsets=offsets.cuda())
+    dz = dy.double() * ref.act64(z.cpu().double(), act)[1]
+    for i in range(e):
+        lo, hi = offsets[i], offsets[i + 1]
+        yield counts[i], ((dx[lo:hi], dz[lo:hi], w[i].double().t()), (dw[i], x[lo:hi].double().t(), dz[lo:hi]))
+
+
+@pytest.mark.parametrize("counts", [[3] * 64, [1, 40, 0, 7, 30, 2, 16, 32], [200] + [0, 1, 4] * 9], ids=["even", "uneven", "one"])
+@pytest.mark.parametrize("k,n", [(64, 72), (200, 1000), (37, 21)])
+def test_experts_of_few_rows_keep_what_dz_loses(muon, counts, k, n):
+    """Up to 16 rows an expert dx and dW are one rounding off, whatever the number of experts."""
+    u, terms = ref.unit(BF16), 2 * max(n, max(counts)) + 4
+    for _, parts in experts_backward(muon, counts, k, n, "silu"):
+        for got, a, b in parts:
+            want, size = a @ b, a.abs() @ b.abs()
+            err = (terms + 32) * ref.U32 * size + u * u * size   # float32 sums and slopes; dz after two roundings
+            ref.check("", got, (want, err + u * (want.abs() + err) + 1e-37))
+
+
+def test_an_expert_of_few_rows_among_many_is_two_roundings_off(muon):
+    """With more rows an expert on average, dz is rounded once for all: dx and dW stay within two roundings' norm."""
+    for rows, parts in experts_backward(muon, [400, 3, 1, 300, 2], 200, 264, "silu"):
+        for got, a, b in parts:
+            want = a @ b
+            # The first rounding moves each product by u of itself at most, in a norm of u |a| |b|; on average
+            # over many products it is u / sqrt 3 of the result, as is the second.
+            assert (got.double().cpu() - want).norm() <= 2 * ref.unit(BF16) * want.norm(), rows

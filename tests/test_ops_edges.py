@@ -170,3 +170,13 @@ def test_backward_of_few_rows_carries_the_rest_of_dz_where_there_is_one(ops):
         return need.value
     assert bytes_of(act=2) >= 2 * 64 * (2 * 72 + 2 * 24)
     assert bytes_of(act=1) < 2 * 64 * 72 + 64 * 72
+
+
+def test_backward_of_experts_counts_the_rows_of_each(ops):
+    """The rest of dz is carried up to 16 rows an expert on average, and up to 64 in all."""
+    lib, need = ops.load_ops(), ctypes.c_uint64(0)
+    for groups, rows, on in ((0, 64, True), (0, 65, False), (2, 64, True), (2, 65, False), (8, 128, True), (8, 129, False),
+                             (64, 1024, True), (64, 1025, False)):
+        d = _desc(ops, rows=rows, groups=groups, k=24, n=72, w_stride=24 * 72)
+        assert lib.muon_linear_workspace(ctypes.byref(d), 4, ctypes.byref(need)) == 0
+        assert (need.value >= 2 * rows * (2 * 72 + 2 * 24 + 4 * 24)) == on, (groups, rows)
