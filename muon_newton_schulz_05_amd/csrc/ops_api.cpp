@@ -124,9 +124,16 @@ bool align_operands(Product* p, int dtype, bool ta, bool tb, const int (&have)[2
 //  - 256 x 256 has the best rate (about 1400 TFLOP/s at 8192^3) once every unit has
 //    a tile: 4096^3 takes 113 / 109 / 110, with 256 x 128 130 / 127 / 134, with
 //    128 x 128 134 / 134 / 129.
-//  - 256 x 256 split in two where that just fills the card, 16384 deep and more:
-//    2048 x 16384 x 4096 forward 224, with 256 x 128 234, with 128 x 128 257
-//    (8192 deep the join costs more than it gives: 124 against 117).
+//  - 256 x 256 split in two for more than 64 such tiles (64 are 256 of 128 x 128, one a
+//    unit) and up to 128, from 12288 deep: below, the join costs what the split
+//    gives.  Time against the rules below, forward / dx / dW:
+//       tiles      8192 deep            10240               12288               16384
+//        64   1.20 / 1.23 / 1.17            -         1.05 / 1.02 / 1.11   1.05 / 1.04 / 1.09
+//        66    .90 /  .89 / 1.03   .87 / .88 / .99     .87 /  .85 /  .97    .85 /  .84 /  .93
+//        80    .93 /  .93 / 1.10   .93 / .93 / 1.08    .91 /  .90 / 1.03    .89 /  .89 /  .98
+//       100    .95 /  .92 / 1.03   .93 / .88 / .97     .89 /  .86 /  .95    .87 /  .85 /  .88
+//       120    .97 /  .95 / 1.02   .94 / .93 / 1.02    .91 /  .90 / 1.00    .87 /  .84 /  .99
+//       128   1.05 / 1.02 /  .99  1.00 / 1.00 / .93    .96 /  .97 /  .92    .99 /  .96 /  .87
 //  - 256 x 128 where only it fills the card (2048 x 8192 x 4096: 117).
 //  - 128 x 128 down to half a card of tiles (2048^3: 29 / 28 / 30, with 256 x 128
 //    51, with 64 x 64 31) and for groups of fewer than 256 rows (64 experts over
@@ -160,8 +167,8 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   const int64_t m_each = gk || !grouped ? g.m : g.m / groups;
   const bool f32 = dtype == MUON_F32;
   const int64_t t256 = tiles(muon::kTile256);
-  const bool halves = !f32 && !grouped && m_each >= 256 && g.n >= 256 && 2 * t256 <= kCus && 16 * t256 >= 7 * kCus &&
-                      g.k >= 16384;
+  const bool halves = !f32 && !grouped && m_each >= 256 && g.n >= 256 && 4 * t256 > kCus && 2 * t256 <= kCus &&
+                      g.k >= 12288;
   p->loads = loads;
   if (loads != muon::kDirect16) {
     p->tile = muon::kTile64;

@@ -124,3 +124,24 @@ def test_an_expert_of_few_rows_among_many_is_two_roundings_off(muon):
             # The first rounding moves each product by u of itself at most, in a norm of u |a| |b|; on average
             # over many products it is u / sqrt 3 of the result, as is the second.
             assert (got.double().cpu() - want).norm() <= 2 * ref.unit(BF16) * want.norm(), rows
+
+
+# ------------------------------------------------------------------ paths that only some shapes reach
+
+
+@pytest.mark.parametrize("w_t", [False, True], ids=["kn", "nk"])
+def test_linear_large_tiles_split_in_two(muon, w_t):
+    """70 ragged 256-wide tiles over 12296 of contraction, forward and dW."""
+    m, k, n = 1100, 12296, 3400
+    x, w = normal((m, k), BF16, 1), normal((n, k) if w_t else (k, n), BF16, 2, k ** -0.5)
+    gw = w.cuda().t() if w_t else w.cuda()
+    y = muon.linear(x.cuda(), gw, activation="silu")
+    rows = torch.tensor([0, 255, 256, 1023, 1024, 1099])
+    want = ref.linear64(x[rows], w.t() if w_t else w, None, None, None, "silu")
+    ref.check("y", y[rows.cuda()], want["y"], 2 * ref.unit(BF16))
+    a, dy = normal((k, m), BF16, 3), normal((k, n), BF16, 4)
+    v = normal((n, m) if w_t else (m, n), BF16, 5).cuda()
+    _, dw, _ = muon.linear_backward(dy.cuda(), a.cuda(), v.t() if w_t else v, needs=(False, True, False))
+    want, size = a[:, rows].double().t() @ dy.double(), a[:, rows].double().abs().t() @ dy.double().abs()
+    err = (k + 2) * ref.U32 * size
+    ref.check("dw", dw[rows.cuda()], (want, err + ref.unit(BF16) * (want.abs() + err)), 2 * ref.unit(BF16))
