@@ -308,23 +308,12 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
     end = hi;
     if (e == g.groups) k1 = 0;  // rows past the last group: zeros
   } else {
-    if (GK && g.share) {
-      // A group's tiles go to `share` of the 8 XCDs, whose L2s then read its
-      // operands once each; the groups are dealt to the sets of XCDs in turn.
-      const int sets = 8 / g.share, x = b & 7, i = b >> 3, chunk = (tiles + g.share - 1) / g.share;
-      e = i / chunk;
-      b = (x % g.share) * chunk + i - e * chunk;
-      e = e * sets + x / g.share;
-      if (e >= g.groups || b >= tiles) return;  // uniform, before any barrier
-      stripe(b, g.tiles_m, g.tiles_n, tm, tn);
-    } else {
-      // Splits, then groups, then tiles.
-      const int e_split = b / tiles;
-      b -= e_split * tiles;
-      split = e_split / g.groups;
-      e = e_split - split * g.groups;
-      stripe(xcd_place(b, tiles), g.tiles_m, g.tiles_n, tm, tn);
-    }
+    // Splits, then groups, then tiles.
+    const int e_split = b / tiles;
+    b -= e_split * tiles;
+    split = e_split / g.groups;
+    e = e_split - split * g.groups;
+    stripe(xcd_place(b, tiles), g.tiles_m, g.tiles_n, tm, tn);
     int64_t per = g.k_per;
     if (GK && g.offsets) {
       int lo, hi;
@@ -580,8 +569,7 @@ __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs g) {
 template <typename T, int BM, int BN, int WGM, int WGN, int WGK, int NS, int LOADS>
 hipError_t launch_tile(const GemmArgs& g, bool ta, bool tb, hipStream_t s) {
   const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
-  const int64_t blocks = g.share ? 8 * ((tiles + g.share - 1) / g.share) * (((int64_t)g.groups * g.share + 7) / 8)
-                                 : tiles * g.splits * (ta && tb && g.offsets ? g.groups : 1);
+  const int64_t blocks = tiles * g.splits * (ta && tb && g.offsets ? g.groups : 1);
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(64 * WGM * WGN * WGK);

@@ -35,7 +35,6 @@ struct GemmArgs {
                            // contraction's splits go by each group's length
   int32_t tiles_m, tiles_n;
   int32_t pairs;           // join: row r of the result is row 2r and, where that is finite, row 2r + 1
-  int32_t share;           // grouped contraction: XCDs that share a group's tiles; 0: all
 };
 
 enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTile64, kTile32x64, kTileRows32, kTileRows32K };

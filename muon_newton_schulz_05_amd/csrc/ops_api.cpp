@@ -197,10 +197,6 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
   const int64_t t = tiles(p->tile);
   const bool sets = p->tile == muon::kTileRows32K;
   const int64_t k_each = grouped && gk ? g.k / groups : g.k;
-  // dW of 64 [2048, 1408] experts over 49152 rows: 352 - 357 us with a group on four
-  // XCDs, 362 - 401 on all; of 16 experts 157 against 148 (too few to balance),
-  // of 32 [24, 10240] ones over 8192 rows 36 against 33 (short contractions).
-  g.share = gk && groups >= 32 && k_each >= 512 ? 4 : 0;
   const int64_t below = sets ? kCus / 2 : grouped ? 2 * kCus : kCus, want = sets ? kCus : grouped ? 4 * kCus : 2 * kCus;
   if ((gk || !grouped) && t > 0 && t < below && k_each >= 1024) {
     int64_t s = std::min<int64_t>((want + t - 1) / t, k_each / 512);
@@ -208,7 +204,6 @@ void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups
     if (s > 1) {
       g.k_per = ((g.k + s - 1) / s + 63) / 64 * 64;
       g.splits = (int32_t)(grouped ? s : (g.k + g.k_per - 1) / g.k_per);
-      g.share = 0;
       p->ws = (uint64_t)g.splits * g.groups * g.m * g.n * 4;
     }
   }
