@@ -57,3 +57,26 @@ def test_activations_keep_their_tails(muon, act, dtype):
     cdf = want / z.double()
     terms = cdf.abs() + (slope - cdf).abs()
     ref.check("dx", dx[:, 0], (slope, 2 * (rel + 4 * ref.U32) * terms + (2 * u + 8 * ref.U32) * slope.abs() + 1e-37))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_keep_what_they_add_to_one(muon, act, dtype):
+    """z from 0 to 12: act'(z) = 1 - act'(-z), whose small part is made of factors that grow with z^3 and must not be
+    multiplied by the error of a difference from one."""
+    z = torch.logspace(-4, math.log2(12), 2000, base=2.0).to(dtype)
+    if act == "gelu_tanh":
+        z = z[z < 9]
+    dy = torch.full((z.numel(), 8), 0.125, dtype=dtype, device="cuda")
+    x = z[:, None].cuda()
+    w = torch.ones(1, 8, device="cuda", dtype=dtype)
+    dx, _, _ = muon.linear_backward(dy, x, w, x.expand(-1, 8).contiguous(), act)
+    value, slope = tail64(-z.double(), act)
+    expo = {"silu": z, "gelu": z * z / 2, "gelu_tanh": 1.6 * (z + 0.044715 * z ** 3)}[act].double()
+    cdf = value / -z.double()
+    small = cdf.abs() + (slope - cdf).abs()
+    want = 1 - slope
+    # The small part relative to itself, as for negative z; one more rounding or two of what is near one.
+    err = 2 * ((3 * expo + 10) * ref.U32 + 4 * ref.U32) * small + 4 * ref.U32
+    u = ref.unit(dtype)
+    ref.check("dx", dx[:, 0], (want, err + (2 * u + 8 * ref.U32) * want.abs()))
