@@ -129,7 +129,14 @@ def _ld(t):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    """The address of a tensor that may be left out.  Null means just that to the C functions, so a tensor that has
+    no memory of its own (a wrapper subclass) must not pass for it."""
+    if t is None:
+        return None
+    at = t.data_ptr()
+    if not at and t.numel():
+        raise ValueError(f"a {type(t).__name__} has no memory of its own: pass the tensor it wraps")
+    return at
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \

@@ -180,3 +180,10 @@ def test_backward_of_experts_counts_the_rows_of_each(ops):
         d = _desc(ops, rows=rows, groups=groups, k=24, n=72, w_stride=24 * 72)
         assert lib.muon_linear_workspace(ctypes.byref(d), 4, ctypes.byref(need)) == 0
         assert (need.value >= 2 * rows * (2 * 72 + 2 * 24 + 4 * 24)) == on, (groups, rows)
+
+
+def test_optional_tensors_without_memory_are_refused(ops):
+    """A wrapper's null address would read as "not given" behind the C interface: a bias left out without a word."""
+    assert ops._ptr(None) is None and ops._ptr(torch.empty(0)) == 0 and ops._ptr(torch.zeros(1)) != 0
+    with pytest.raises(ValueError, match="memory"):
+        ops._ptr(Elsewhere(8))
