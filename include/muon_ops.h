@@ -17,7 +17,7 @@
  *
  * Errors: as in muon.h; arguments are checked before anything is enqueued.
  * Sums, activations and weights' products are float32; what is stored in
- * bf16 is rounded to nearest even once.  No result depends on the order in
+ * bf16 (z and dz among it) is rounded to nearest even once.  No result depends on the order in
  * which workgroups run.
  */
 #ifndef MUON_OPS_H
@@ -147,7 +147,7 @@ int muon_combine_grad(const muon_move_desc_t* desc, const int32_t* offsets, cons
 /* y = keep x 65536 / (65536 - D) + residual with D = 65536 p rounded to the nearest (ties to even), over n
  * contiguous elements.  Element i is kept when lane i mod 8 (16 bits, low half
  * of word 0 first) of Philox4x32-10 with counter (i div 8, offset) and key
- * `seed` is at least D.  state: NULL, or two uint64 on the device {seed, offset}
+ * `seed` is at least D.  D = 65536 is refused.  state: NULL, or two uint64 on the device {seed, offset}
  * that take their place (so that a captured call can be given new ones).
  * The gradient of x is the same call on dy without a residual. */
 int muon_dropout(int32_t dtype, int64_t n, const void* x, const void* residual, void* y, double p, uint64_t seed,

@@ -6,8 +6,8 @@
 // eight 16-bit lanes of block b, so the mask follows from the element's
 // flat index alone and the gradient makes it again instead of storing it.
 //
-// Bound by memory: [16384, 4096] in bf16 takes 116 us forward with a residual and
-// backward together, 5.8 TB/s.  One generator call serves eight elements
+// Bound by memory: [16384, 4096] in bf16 takes 108 - 117 us forward with a residual and
+// backward together, 5.7 - 6.2 TB/s.  One generator call serves eight elements
 // (16 bits each, so probabilities go in steps of 2^-16); with 32 bits an element
 // its 20 wide multiplications a call would take as long as the memory.
 #include "act.h"

@@ -20,10 +20,10 @@
 //    the chunk with their k.  float32: 16 lanes read 16 consecutive values of
 //    each of four k, no transposition.
 //
-// What bounds it.  bf16, 256 x 256 tiles, 8192^3: 1400 TFLOP/s forward and dW,
-// 1430 dx; the matrix cores are busy 70 - 73% of the cycles, at about 1.9 GHz
-// under the card's power limit (the best library kernel measured: 1574, 87% at
-// 1.74 GHz).  The rest is waiting at the slices' barriers.  Four waves of
+// What bounds it.  bf16, 256 x 256 tiles, 8192^3: 1270 - 1420 TFLOP/s by card and
+// layout (one run of the three: forward 1268, dx 1383, dW 1409); the matrix cores are
+// busy 70 - 73% of the cycles, at about 1.9 GHz under the card's power limit (the best
+// library kernel measured: 1574, 87% at 1.74 GHz).  The rest is waiting at the slices' barriers.  Four waves of
 // 128 x 128 read a third less from LDS and were 7 - 12% slower; half slices, four
 // or five deep, were equal for operands along their rows and 8% slower for
 // operands along k, whose loads then take half lines.  With few slices a tile
@@ -227,6 +227,9 @@ struct Panel {
 };
 
 // z = v + bias (stored where asked), y = act(z) + res, eight columns of one row.
+// y comes from the float32 z.  What is kept of z for the gradient has the layer's type: in
+// bf16 half the bytes of float32, which a large layer would write and read once
+// more, for a slope taken at most half a step of z away.
 template <typename T>
 __device__ __forceinline__ void finish8(const GemmArgs& g, float (&v)[8], const float (&bias)[8], int64_t e, int64_t row,
                                         int col, int n) {
@@ -427,8 +430,8 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
             read(st, s);
             multiply(s + 1);  // of the other parity: substep s - 1
             // The loads go out over the first half of the substep's products: at 8192^3
-            // 1416 / 1419 / 1411 TFLOP/s (forward, dx, dW) against 1388 / 1392 /
-            // 1345 over all of them and 1407 / 1371 / 1406 over the first quarter.
+            // on one card 1416 / 1419 / 1411 TFLOP/s (forward, dx, dW) against 1388 /
+            // 1392 / 1345 over all of them and 1407 / 1371 / 1406 over the first quarter.
             if (s == 0) interleave<RD, L, MM / 2, MM>();
             else interleave<RD, 0, 1, MM>();
           }

@@ -79,18 +79,18 @@ struct Product {
 // A larger bf16 product whose operands no 16-byte loads reach first copies them
 // into rows that they do, padded with zeros, which add nothing.  Without and with
 // the copies, in us (forward / dx / dW, weight [K, N]):
-//    4001 x 2001 x 4003   227 / 197 / 337    79 / 97 / 95
-//    2001 x 1001 x 2003    47 /  39 /  75    31 / 38 / 36
-//    1031 x 1001 x 1003    31 /  21 /  33    23 / 21 / 18
-//  - From 2 GFLOP on that pays, or costs nothing (513 x 2001 x 1003: 28 / 22 / 21,
-//    27 / 24 / 20), except where both operands lie along the contraction (dx here):
+//    4001 x 2001 x 4003   204 / 182 / 333    77 / 85 / 85
+//    2001 x 1001 x 2003    43 /  35 /  72    30 / 36 / 34
+//    1031 x 1001 x 1003    29 /  20 /  32    21 / 20 / 19
+//  - From 2 GFLOP on that pays, or costs nothing (513 x 2001 x 1003: 28 / 21 / 20,
+//    27 / 22 / 19), except where both operands lie along the contraction (dx here):
 //    the other loads serve those better, and it takes 8 GFLOP.
 //  - A copy has to be used often enough: 100001 x 101 x 101 (100 FLOP per byte
 //    copied) 33 and 38 forward, 64 experts of 1001 x 999 over 2000 rows (30) 84 and
 //    98, 129 x 4001 x 4003 (124) 52 and 42.  dW, whose other loads are the slowest,
-//    gains at any rate (100001 x 101 x 101: 133 and 78).
-//  - Float32 is bound by its matrix instructions either way: 583 and 556 at the
-//    first of these, 79 and 89 at the second.
+//    gains at any rate (100001 x 101 x 101: 142 and 87).
+//  - Float32 is bound by its matrix instructions either way: forward 583 without and 556
+//    with copies at the first of these, 79 and 89 at the second.
 bool align_operands(Product* p, int dtype, bool ta, bool tb, const int (&have)[2], int groups) {
   muon::GemmArgs& g = p->g;
   const double flop = 2.0 * g.m * g.n * g.k;
@@ -145,9 +145,9 @@ bool align_operands(Product* p, int dtype, bool ta, bool tb, const int (&have)[2
 //    contraction shared by four sets of waves (16 x 4096 x 16384: 25 / 27, with
 //    32 x 128 and a join 27 / 30; [24, 10240] experts over 8192 rows, dx from
 //    memory: 71, with 32 x 128 84).
-//  - Operands that no 16-byte loads reach: 64 x 64, whose staging hides better
-//    behind other workgroups (4001 x 2001 x 4003: 184 / 226 / 324, with 128 x 128
-//    204 / 272 / 472).
+//  - Operands that no 16-byte loads reach and that are not copied: 64 x 64, whose staging
+//    hides better behind other workgroups (4001 x 2001 x 4003, before such sizes were
+//    copied: 184 / 226 / 324 against 204 / 272 / 472 with 128 x 128).
 //  - float32 products are bound by their lower matrix rate, not by operand
 //    traffic: 64 x 64, or 32 x 64 while 64 x 64 fills the card at most twice
 //    (777 x 1001 x 1343: 38 / 37 / 35 against 45 / 37 / 37).
@@ -321,8 +321,8 @@ int check_ptr(const muon_linear_desc_t* d, const void* p, int64_t count, const c
 // rounded row alone: dx drops the rest of a sum that is not finite, and the row of x
 // for the rest has zeros there.  (relu's slope is 0 or 1: its dz loses nothing.)
 // The whole backward pass without and with, in us:
-//  - one weight, up to 64 rows: 1 x 4096 x 16384 77 and 81, 16 x 4096 x 4096 40 and 44,
-//    64 x 1024 x 4096 30 and 39; 128 x 4096 x 16384 would take 124 and 167.
+//  - one weight, up to 64 rows: 1 x 4096 x 16384 73 and 78, 16 x 4096 x 4096 37 and 43,
+//    64 x 1024 x 4096 30 and 39; 128 x 4096 x 16384 would take 116 and 161.
 //  - experts, up to 16 rows each on average (the host knows no more): 64 x [2048,
 //    1408] with 2 rows each 217 and 226, with 16 245 and 262; with 32 it would be 251
 //    and 302, with 64 288 and 358.  16 x [1024, 1024] with 16: 36 and 42, with 32 36 and 51.

@@ -7,8 +7,9 @@
 // The moves are bound by memory.  They are cut by tokens, not by sorted rows:
 // a token's row (or its gradient) is read once and meets its `top` rows
 // from registers, and each sum over them runs in the order of the choices.
-// 16384 tokens x 8 of 64 experts at h = 2048 in bf16: sort 21 us, dispatch 114,
-// combine and dispatch's gradient 116 each, combine's gradient 249 (4.6 - 5.3 TB/s).
+// 16384 tokens x 8 of 64 experts at h = 2048 in bf16: sort 17 - 21 us, dispatch 103 - 116,
+// combine and dispatch's gradient 114 - 117 each, combine's gradient 234 - 250, back to
+// back and in a trace from cold clocks (4.6 - 5.9 TB/s).
 // Up to 4096 entries the sort is one launch (64 tokens x 6: 3.5 us).
 #include "act.h"
 #include "device_common.h"
@@ -375,8 +376,8 @@ void move_rows(const MoveArgs& a, unsigned blocks, hipStream_t s) {
   else hipLaunchKernelGGL((k_dispatch<T, FULL, false>), dim3(blocks), dim3(256), 0, s, a);
 }
 // Four rows in flight, eight where there are more than four choices (16384
-// tokens x 8: combine's gradient 226 us against 237; with three choices four are
-// faster, 28 against 34, the others being read for nothing).
+// tokens x 8: combine's gradient 5% faster; with three choices four are faster, 28
+// us against 34, the others being read for nothing).
 template <typename T, int U, bool FULL>
 void gather(const MoveArgs& a, unsigned blocks, hipStream_t s) {
   if (streams<T>(a)) hipLaunchKernelGGL((k_gather_sum<T, U, FULL, true>), dim3(blocks), dim3(256), 0, s, a);

@@ -367,7 +367,13 @@ def linear(x, weight, bias=None, *, activation="none", residual=None):
     x [..., K], weight [K, N] (or the transposed view of a [N, K] tensor, read
     in place), bias [N], residual [..., N].  activation: "none", "relu", "silu",
     "gelu" or "gelu_tanh".  Differentiable in every tensor (once); for
-    the gradient, z = x W + b is kept in x's type."""
+    the gradient, z = x W + b is kept in x's type.
+
+    bfloat16: y is rounded once, from float32.  With an activation the gradients are
+    taken at the rounded z and from the gradient of z rounded to bfloat16, so dx and dW
+    are about 1.4 times as far off as one rounding makes them, in the norm (2.4e-3
+    against 1.7e-3); up to 64 rows (16 an expert on average in ``expert_linear``), and
+    for "relu", they are not.  float32 tensors carry no such rounding."""
     if not _tracked(x, weight, bias, residual):
         return linear_forward(x, weight, bias, activation, residual)[0]
     _check_linear(x, weight, bias, residual, None)
@@ -633,7 +639,7 @@ class _Dropout(torch.autograd.Function):
 def dropout(x, p, *, seed=0, offset=0, residual=None, state=None):
     """x with each element zeroed with probability p and the others scaled by 1 / (1 - p), plus residual.
 
-    p is taken to the nearest of 65536 steps.  The mask follows from (seed,
+    p is taken to the nearest of 65536 steps; one that comes to 1 so is refused.  The mask follows from (seed,
     offset) and an element's flat index alone: calls that must differ get another
     seed or offset.  state: an int64 tensor [seed, offset] on the GPU used in
     their place, which a captured graph reads at every replay.  Differentiable
