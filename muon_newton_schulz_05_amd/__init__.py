@@ -5,7 +5,9 @@ The computation lives in hand-written HIP kernels behind the C ABI of
 marshals arguments.  Importing does not load the library; ``MuonPlan`` and the
 ``muon_*`` functions do, and fail loudly if it has not been built.  The layer
 operators (``linear``, ``expert_linear``, ``route``, ``dispatch``, ``combine``,
-``dropout``; ``ops.py``) need torch and are loaded at their first use.
+``dropout``; ``ops.py``), those around a block's products (``layer_norm``, ``rms_norm``, ``gate``,
+``balance_loss``; ``block.py``) and the layers in four bits (``mx_quantize``, ``mx_linear``,
+``mx_expert_linear``; ``mx.py``) need torch and are loaded at their first use.
 """
 
 from .binding import (  # noqa: F401
@@ -39,11 +41,22 @@ from .binding import (  # noqa: F401
 _OPS = ("linear", "expert_linear", "linear_forward", "linear_backward", "Routing", "route", "dispatch",
         "dispatch_forward", "dispatch_backward", "combine", "combine_forward", "combine_backward", "dropout",
         "dropout_forward")
+_BLOCK = ("layer_norm", "rms_norm", "norm_forward", "norm_backward", "Gating", "gate", "gate_forward", "gate_backward",
+          "Balance", "balance_loss", "balance_forward", "balance_backward")
+_MX = ("MxWeight", "mx_quantize", "mx_dequantize", "mx_linear", "mx_expert_linear")
 
 
 def __getattr__(name):
     if name in _OPS:
         from . import ops
         globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
+    if name in _BLOCK:
+        from . import block
+        globals().update({n: getattr(block, n) for n in _BLOCK})
+        return globals()[name]
+    if name in _MX:
+        from . import mx
+        globals().update({n: getattr(mx, n) for n in _MX})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmuon.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["api.cpp", "planner.cpp", "skinny.hip", "stream.hip", "stream_big.hip", "noalloc.hip",
-           "ops_api.cpp", "linear_bf16.hip", "linear_f32.hip", "route.hip", "dropout.hip"]
+           "ops_api.cpp", "linear_bf16.hip", "linear_f32.hip", "route.hip", "dropout.hip",
+           "block_api.cpp", "norm.hip", "gate.hip", "mx.hip", "linear_mx.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,359 @@
+// block_api.cpp -- the C ABI of the operators around a block's products (include/muon_block.h): argument
+// checks, workspaces and launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/muon_block.h"
+#include "api_common.h"
+#include "gate.h"
+#include "mx.h"
+#include "norm.h"
+#include "product.h"
+
+namespace {
+
+using muon::aligned;
+using muon::bad;
+using muon::elem;
+using muon::hip_result;
+using muon::set_error;
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;  // as a layer's
+constexpr int64_t kMaxCols = int64_t(1) << 24;           // a norm's: its kernels count columns in 32 bits
+constexpr int64_t kMaxMx = int64_t(1) << 23;             // 256 rows of four-bit values stay below 2^31 bytes
+
+int check_dtype(int32_t dtype) {
+  return dtype == MUON_F32 || dtype == MUON_BF16 ? MUON_OK : bad("dtype must be MUON_F32 or MUON_BF16");
+}
+// A pointer that has to be there (`count` elements of `size` bytes behind it), or may be null (count 0).
+int check_at(const void* p, int64_t count, int size, const char* name) {
+  if (count > 0 && !p) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is null", name);
+  if (!aligned(p, size)) return set_error(MUON_ERR_INVALID_ARGUMENT, "%s is not %d-byte aligned", name, size);
+  return MUON_OK;
+}
+int check_space(uint64_t need, const void* ws, uint64_t bytes) {
+  if (bytes < need || (need && !ws)) return bad("the workspace is smaller than the operator's workspace call says");
+  return aligned(ws, 16) ? MUON_OK : bad("the workspace is not 16-byte aligned");
+}
+
+// ---- norms
+
+int check_norm(const muon_norm_desc_t* d) {
+  if (!d) return bad("desc is null");
+  MUON_TRY(check_dtype(d->dtype));
+  if (d->kind != MUON_NORM_LAYER && d->kind != MUON_NORM_RMS) return bad("unknown norm");
+  if (d->rows < 0 || d->rows > kMaxRows) return bad("rows outside [0, 2^31 - 1024]");
+  if (d->cols < 0 || d->cols > kMaxCols) return bad("cols outside [0, 2^24]");
+  if (d->ldx < 0 || d->ldr < 0 || d->ldg < 0) return bad("a stride is negative");
+  if (!(d->eps >= 0.0 && d->eps < 1e30)) return bad("eps is negative or not finite");
+  return MUON_OK;
+}
+uint64_t norm_bytes(const muon_norm_desc_t* d) { return (uint64_t)muon::norm_parts(d->rows, d->cols) * 2 * d->cols * 4; }
+
+// ---- gate and balance
+
+int check_gate(const muon_gate_desc_t* d) {
+  if (!d) return bad("desc is null");
+  MUON_TRY(check_dtype(d->dtype));
+  if (d->experts < 1 || d->experts > muon::kGateMaxExperts) return bad("experts outside [1, 1024]");
+  if (d->top < 1 || d->top > d->experts) return bad("top outside [1, experts]");
+  if (d->tokens < 0 || d->tokens > kMaxRows) return bad("tokens outside [0, 2^31 - 1024]");
+  if (d->ldz < 0) return bad("a stride is negative");
+  return MUON_OK;
+}
+// Counts are held in 32 bits, so the balance loss ends where they would.
+int check_balance(const muon_gate_desc_t* d) {
+  if (d && d->top >= 1 && d->tokens > kMaxRows / d->top) return bad("tokens * top is over 2^31 - 1024");
+  // An id list may be longer than there are experts (a token's choices need not differ here).
+  muon_gate_desc_t one = d ? *d : muon_gate_desc_t{};
+  if (d && one.top > one.experts) one.top = one.experts;
+  return check_gate(d ? &one : nullptr);
+}
+uint64_t balance_bytes(const muon_gate_desc_t* d) {
+  return (uint64_t)muon::balance_blocks(d->tokens, d->experts) * (2 * d->experts + 1) * 4;
+}
+muon::GateArgs gate_args(const muon_gate_desc_t* d, const void* logits, const uint8_t* mask) {
+  muon::GateArgs a{};
+  a.logits = logits;
+  a.mask = mask;
+  a.tokens = d->tokens;
+  a.ldz = d->ldz;
+  a.experts = d->experts;
+  a.top = d->top;
+  a.normalize = d->normalize;
+  return a;
+}
+muon::BalanceArgs balance_args(const muon_gate_desc_t* d, const void* logits, const uint8_t* mask) {
+  muon::BalanceArgs a{};
+  a.logits = logits;
+  a.mask = mask;
+  a.tokens = d->tokens;
+  a.ldz = d->ldz;
+  a.experts = d->experts;
+  a.top = d->top;
+  return a;
+}
+
+// ---- four bits
+
+int check_mx(const muon_mx_desc_t* d) {
+  if (!d) return bad("desc is null");
+  MUON_TRY(check_dtype(d->dtype));
+  if (d->act < MUON_ACT_NONE || d->act > MUON_ACT_GELU_TANH) return bad("unknown activation");
+  if (d->groups < 0 || d->groups > 65535) return bad("groups outside [0, 65535]");
+  if (d->w_layout != 0 && d->w_layout != 1) return bad("w_layout must be 0 or 1");
+  if (d->rows < 0 || d->rows > kMaxRows) return bad("rows outside [0, 2^31 - 1024]");
+  if (d->k < 0 || d->n < 0 || d->k > kMaxMx || d->n > kMaxMx) return bad("k or n outside [0, 2^23]");
+  if (d->ldx < 0 || d->ldw < 0 || d->w_stride < 0 || d->ldr < 0) return bad("a stride is negative");
+  return MUON_OK;
+}
+int64_t mx_weights(const muon_mx_desc_t* d) { return std::max(d->groups, 1); }
+int check_mx_weight(const muon_mx_desc_t* d, const uint8_t* values, const uint8_t* scales) {
+  MUON_TRY(check_at(values, d->k * d->n, 16, "values"));
+  return check_at(scales, d->k * d->n, 16, "scales");
+}
+muon::MxArgs mx_args(const muon_mx_desc_t* d) {
+  muon::MxArgs a{};
+  a.rows = d->n;
+  a.k = d->k;
+  a.ld = d->ldw;
+  a.step = d->w_stride;
+  a.groups = (int32_t)mx_weights(d);
+  a.t = d->w_layout == 0;
+  return a;
+}
+uint64_t up16(uint64_t n) { return (n + 15) / 16 * 16; }
+uint64_t x_values(const muon_mx_desc_t* d) { return (uint64_t)d->rows * muon::mx_row_bytes(d->k); }
+uint64_t x_scales(const muon_mx_desc_t* d) { return up16((uint64_t)muon::mx_scale_bytes(d->rows, d->k)); }
+
+// The product, planned as one of bf16 whose slices take the same bytes and matrix-core time (a quarter of the
+// contraction), in units of bytes.
+muon::Product mx_product(const muon_mx_desc_t* d) {
+  muon::Product p;
+  muon::GemmArgs& g = p.g;
+  g.m = d->rows;
+  g.n = d->n;
+  const int64_t bytes = muon::mx_row_bytes(d->k);
+  g.k = bytes / 2;
+  muon::plan_product(&p, MUON_BF16, false, false, muon::kDirect16, d->groups);
+  g.k = bytes;
+  g.k_per *= 2;
+  g.lda = g.ldb = bytes;
+  g.sb = (int64_t)bytes * d->n;
+  g.sscb = muon::mx_scale_bytes(d->n, d->k);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_norm_workspace(const muon_norm_desc_t* d, uint64_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  *bytes = 0;
+  MUON_TRY(check_norm(d));
+  *bytes = norm_bytes(d);
+  return set_error(MUON_OK, "%s", "");
+}
+
+int muon_norm_forward(const muon_norm_desc_t* d, const void* x, const void* residual, const void* w, const void* b,
+                      void* y, void* s, float* stats, void* stream) {
+  MUON_TRY(check_norm(d));
+  const int es = elem(d->dtype);
+  const int64_t count = d->rows * d->cols;
+  MUON_TRY(check_at(x, count, es, "x"));
+  MUON_TRY(check_at(residual, 0, es, "residual"));
+  MUON_TRY(check_at(w, 0, es, "w"));
+  MUON_TRY(check_at(b, 0, es, "b"));
+  MUON_TRY(check_at(y, count, es, "y"));
+  MUON_TRY(check_at(s, residual ? count : 0, es, "s"));
+  MUON_TRY(check_at(stats, 0, 4, "stats"));
+  if (s && !residual) return bad("s is given without a residual");
+  const muon::NormArgs a{x,       residual, w,      b,      y, s, stats, d->rows, d->cols, d->ldx, d->ldr, (float)d->eps,
+                         d->kind == MUON_NORM_LAYER};
+  return hip_result(muon::launch_norm(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_norm_forward");
+}
+
+int muon_norm_backward(const muon_norm_desc_t* d, const void* dy, const void* s, const void* w, const float* stats,
+                       const void* ds, void* dx, void* dw, void* db, void* ws, uint64_t ws_bytes, void* stream) {
+  MUON_TRY(check_norm(d));
+  if (!dx && !dw && !db) return set_error(MUON_OK, "%s", "");
+  const int es = elem(d->dtype);
+  const int64_t count = d->rows * d->cols;
+  MUON_TRY(check_at(dy, count, es, "dy"));
+  MUON_TRY(check_at(s, count, es, "s"));
+  MUON_TRY(check_at(w, 0, es, "w"));
+  MUON_TRY(check_at(stats, count, 4, "stats"));
+  MUON_TRY(check_at(ds, 0, es, "ds"));
+  MUON_TRY(check_at(dx, 0, es, "dx"));
+  MUON_TRY(check_at(dw, 0, es, "dw"));
+  MUON_TRY(check_at(db, 0, es, "db"));
+  if (dw || db) MUON_TRY(check_space(norm_bytes(d), ws, ws_bytes));
+  const muon::NormGradArgs a{dy, s, w, ds, stats, dx, dw, db, dw || db ? static_cast<float*>(ws) : nullptr,
+                             d->rows, d->cols, d->ldg, d->ldx, d->ldr, d->kind == MUON_NORM_LAYER};
+  return hip_result(muon::launch_norm_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_norm_backward");
+}
+
+int muon_gate_forward(const muon_gate_desc_t* d, const void* logits, const uint8_t* mask, float* weights, int32_t* ids,
+                      void* stream) {
+  MUON_TRY(check_gate(d));
+  MUON_TRY(check_at(logits, d->tokens, elem(d->dtype), "logits"));
+  MUON_TRY(check_at(weights, d->tokens, 4, "weights"));
+  MUON_TRY(check_at(ids, d->tokens, 4, "ids"));
+  muon::GateArgs a = gate_args(d, logits, mask);
+  a.weights = weights;
+  a.ids = ids;
+  return hip_result(muon::launch_gate(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_gate_forward");
+}
+
+int muon_gate_backward(const muon_gate_desc_t* d, const void* logits, const uint8_t* mask, const float* weights,
+                       const int32_t* ids, const float* dweights, void* dlogits, void* stream) {
+  MUON_TRY(check_gate(d));
+  MUON_TRY(check_at(logits, d->normalize ? 0 : d->tokens, elem(d->dtype), "logits"));
+  MUON_TRY(check_at(weights, d->tokens, 4, "weights"));
+  MUON_TRY(check_at(ids, d->tokens, 4, "ids"));
+  MUON_TRY(check_at(dweights, d->tokens, 4, "dweights"));
+  MUON_TRY(check_at(dlogits, d->tokens, elem(d->dtype), "dlogits"));
+  muon::GateArgs a = gate_args(d, logits, mask);
+  a.weights = const_cast<float*>(weights);
+  a.ids = const_cast<int32_t*>(ids);
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  return hip_result(muon::launch_gate_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_gate_backward");
+}
+
+int muon_balance_workspace(const muon_gate_desc_t* d, uint64_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  *bytes = 0;
+  MUON_TRY(check_balance(d));
+  *bytes = balance_bytes(d);
+  return set_error(MUON_OK, "%s", "");
+}
+
+int muon_balance_forward(const muon_gate_desc_t* d, const void* logits, const void* ids, int32_t ids_bytes,
+                         const uint8_t* mask, float* loss, int32_t* counts, float* shares, void* ws, uint64_t ws_bytes,
+                         void* stream) {
+  MUON_TRY(check_balance(d));
+  if (ids_bytes != 4 && ids_bytes != 8) return bad("ids_bytes must be 4 or 8");
+  MUON_TRY(check_at(logits, d->tokens, elem(d->dtype), "logits"));
+  MUON_TRY(check_at(ids, d->tokens, ids_bytes, "ids"));
+  MUON_TRY(check_at(loss, 1, 4, "loss"));
+  MUON_TRY(check_at(counts, 1, 4, "counts"));
+  MUON_TRY(check_at(shares, 1, 4, "shares"));
+  MUON_TRY(check_space(balance_bytes(d), ws, ws_bytes));
+  muon::BalanceArgs a = balance_args(d, logits, mask);
+  a.ids = ids;
+  a.ids64 = ids_bytes == 8;
+  a.loss = loss;
+  a.counts = counts;
+  a.shares = shares;
+  a.part = static_cast<float*>(ws);
+  a.part_counts = reinterpret_cast<int32_t*>(a.part + (int64_t)muon::balance_blocks(d->tokens, d->experts) * d->experts);
+  return hip_result(muon::launch_balance(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_balance_forward");
+}
+
+int muon_balance_backward(const muon_gate_desc_t* d, const void* logits, const uint8_t* mask, const float* shares,
+                          const float* dloss, void* dlogits, void* stream) {
+  MUON_TRY(check_balance(d));
+  MUON_TRY(check_at(logits, d->tokens, elem(d->dtype), "logits"));
+  MUON_TRY(check_at(shares, 1, 4, "shares"));
+  MUON_TRY(check_at(dloss, 1, 4, "dloss"));
+  MUON_TRY(check_at(dlogits, d->tokens, elem(d->dtype), "dlogits"));
+  muon::BalanceArgs a = balance_args(d, logits, mask);
+  a.shares = const_cast<float*>(shares);
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  return hip_result(muon::launch_balance_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_balance_backward");
+}
+
+int muon_mx_sizes(const muon_mx_desc_t* d, uint64_t* values_bytes, uint64_t* scales_bytes) {
+  if (!values_bytes || !scales_bytes) return bad("values_bytes or scales_bytes is null");
+  *values_bytes = *scales_bytes = 0;
+  MUON_TRY(check_mx(d));
+  *values_bytes = (uint64_t)mx_weights(d) * d->n * muon::mx_row_bytes(d->k);
+  *scales_bytes = (uint64_t)mx_weights(d) * muon::mx_scale_bytes(d->n, d->k);
+  return set_error(MUON_OK, "%s", "");
+}
+
+int muon_mx_quantize(const muon_mx_desc_t* d, const void* w, uint8_t* values, uint8_t* scales, void* stream) {
+  MUON_TRY(check_mx(d));
+  MUON_TRY(check_at(w, d->k * d->n, elem(d->dtype), "w"));
+  MUON_TRY(check_mx_weight(d, values, scales));
+  muon::MxArgs a = mx_args(d);
+  a.src = w;
+  a.values = values;
+  a.scales = scales;
+  return hip_result(muon::launch_mx_quantize(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_mx_quantize");
+}
+
+int muon_mx_dequantize(const muon_mx_desc_t* d, const uint8_t* values, const uint8_t* scales, void* w, void* stream) {
+  MUON_TRY(check_mx(d));
+  MUON_TRY(check_mx_weight(d, values, scales));
+  MUON_TRY(check_at(w, d->k * d->n, elem(d->dtype), "w"));
+  muon::MxArgs a = mx_args(d);
+  a.values = const_cast<uint8_t*>(values);
+  a.scales = const_cast<uint8_t*>(scales);
+  a.dst = w;
+  return hip_result(muon::launch_mx_dequantize(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_mx_dequantize");
+}
+
+int muon_mx_linear_workspace(const muon_mx_desc_t* d, uint64_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  *bytes = 0;
+  MUON_TRY(check_mx(d));
+  if (d->rows > 0 && d->n > 0) *bytes = x_values(d) + x_scales(d) + mx_product(d).ws;
+  return set_error(MUON_OK, "%s", "");
+}
+
+int muon_mx_linear(const muon_mx_desc_t* d, const int32_t* offsets, const void* x, const uint8_t* values,
+                   const uint8_t* scales, const void* bias, const void* residual, void* y, void* ws, uint64_t ws_bytes,
+                   void* stream) {
+  const char* what = "muon_mx_linear";
+  MUON_TRY(check_mx(d));
+  const int es = elem(d->dtype);
+  if (d->groups > 0 && !offsets) return bad("offsets is null");
+  if (d->groups == 0 && offsets) return bad("offsets given, but groups is 0");
+  MUON_TRY(check_at(offsets, 0, 4, "offsets"));
+  MUON_TRY(check_at(x, d->rows * d->k, es, "x"));
+  MUON_TRY(check_mx_weight(d, values, scales));
+  MUON_TRY(check_at(bias, 0, es, "bias"));
+  MUON_TRY(check_at(residual, 0, es, "residual"));
+  MUON_TRY(check_at(y, d->rows * d->n, es, "y"));
+  if (d->groups > 0 && residual) return bad("a grouped layer takes no residual");
+  if (d->rows == 0 || d->n == 0) return set_error(MUON_OK, "%s", "");
+  muon::Product p = mx_product(d);
+  MUON_TRY(check_space(x_values(d) + x_scales(d) + p.ws, ws, ws_bytes));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+
+  muon::MxArgs q{};
+  q.src = x;
+  q.values = static_cast<uint8_t*>(ws);
+  q.scales = q.values + x_values(d);
+  q.rows = d->rows;
+  q.k = d->k;
+  q.ld = d->ldx;
+  q.groups = 1;
+  MUON_TRY(hip_result(muon::launch_mx_quantize(q, d->dtype, s), what));
+
+  muon::GemmArgs& g = p.g;
+  g.a = q.values;
+  g.b = values;
+  g.sca = q.scales;
+  g.scb = scales;
+  g.offsets = offsets;
+  g.c = y;
+  g.bias = bias;
+  g.res = residual;
+  g.ldc = d->n;
+  g.ldr = d->ldr;
+  g.sbias = d->n;
+  g.act = d->act;
+  if (g.splits > 1) g.part = reinterpret_cast<float*>(q.scales + x_scales(d));
+  hipError_t e = muon::launch_gemm_mx(g, d->dtype, p.tile, s);
+  if (e == hipSuccess && g.splits > 1) e = muon::launch_gemm_join(g, d->dtype, s);
+  return hip_result(e, what);
+}
+
+}  // extern "C"
