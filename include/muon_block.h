@@ -105,8 +105,8 @@ typedef struct {
 } muon_mx_desc_t;
 
 /* Sizes of one weight's (times max(groups, 1)) four-bit form:
- *  values [n][16 ceil(k / 32)] bytes: row j holds the e2m1 values of column j, two a byte, lower half first;
- *  scales [ceil(k / 256)][n][8]: byte 2 (b mod 4) + b / 4 of a row is the e8m0 scale of block b of the slice.
+ *  values [ceil(k / 128)][n][64]: the e2m1 values of each column by slices of 128, two a byte, lower half first;
+ *  scales [ceil(k / 512)][n][16]: byte 4 g + s is the e8m0 scale of the 32 values g (0..3) of slice s (0..3) of 512.
  * Both 16-byte aligned; what pads k is zero. */
 int muon_mx_sizes(const muon_mx_desc_t* desc, uint64_t* values_bytes, uint64_t* scales_bytes);
 

@@ -10,7 +10,6 @@
 #include "gate.h"
 #include "mx.h"
 #include "norm.h"
-#include "product.h"
 
 namespace {
 
@@ -22,7 +21,8 @@ using muon::set_error;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;  // as a layer's
 constexpr int64_t kMaxCols = int64_t(1) << 24;           // a norm's: its kernels count columns in 32 bits
-constexpr int64_t kMaxMx = int64_t(1) << 23;             // 256 rows of four-bit values stay below 2^31 bytes
+constexpr int64_t kMaxMx = int64_t(1) << 23;             // k and n of a weight
+constexpr int kCus = 256;
 
 int check_dtype(int32_t dtype) {
   return dtype == MUON_F32 || dtype == MUON_BF16 ? MUON_OK : bad("dtype must be MUON_F32 or MUON_BF16");
@@ -124,26 +124,49 @@ muon::MxArgs mx_args(const muon_mx_desc_t* d) {
   a.t = d->w_layout == 0;
   return a;
 }
-uint64_t up16(uint64_t n) { return (n + 15) / 16 * 16; }
-uint64_t x_values(const muon_mx_desc_t* d) { return (uint64_t)d->rows * muon::mx_row_bytes(d->k); }
-uint64_t x_scales(const muon_mx_desc_t* d) { return up16((uint64_t)muon::mx_scale_bytes(d->rows, d->k)); }
+// A layer's product: its tile and split, and what it takes of the workspace.
+struct MxPlan {
+  muon::MxProduct p{};
+  int tile = 0, cols = 0;
+  uint64_t x_values = 0, x_scales = 0, partials = 0;  // bytes
+  bool few() const { return tile >= muon::kMxRows32; }
+  uint64_t bytes() const { return x_values + x_scales + partials; }
+};
 
-// The product, planned as one of bf16 whose slices take the same bytes and matrix-core time (a quarter of the
-// contraction), in units of bytes.
-muon::Product mx_product(const muon_mx_desc_t* d) {
-  muon::Product p;
-  muon::GemmArgs& g = p.g;
+MxPlan mx_plan(const muon_mx_desc_t* d) {
+  MxPlan q;
+  muon::GemmArgs& g = q.p.g;
+  const bool grouped = d->groups > 0;
   g.m = d->rows;
   g.n = d->n;
-  const int64_t bytes = muon::mx_row_bytes(d->k);
-  g.k = bytes / 2;
-  muon::plan_product(&p, MUON_BF16, false, false, muon::kDirect16, d->groups);
-  g.k = bytes;
-  g.k_per *= 2;
-  g.lda = g.ldb = bytes;
-  g.sb = (int64_t)bytes * d->n;
-  g.sscb = muon::mx_scale_bytes(d->n, d->k);
-  return p;
+  g.k = muon::mx_slices(d->k);
+  g.groups = std::max(d->groups, 1);
+  g.sb = muon::mx_value_bytes(d->n, d->k);
+  g.splits = 1;
+  g.k_per = g.k;
+  auto blocks_m = [&](int tile) { return muon::group_blocks(d->rows, d->groups, grouped, muon::mx_tile_m(tile)); };
+  auto tiles = [&](int tile) { return blocks_m(tile) * ((d->n + muon::mx_tile_n(tile, 0, 0) - 1) / muon::mx_tile_n(tile, 0, 0)); };
+  const int64_t m_each = grouped ? d->rows / d->groups : d->rows;
+  if (m_each <= 32) q.tile = m_each <= 16 ? muon::kMxRows16 : muon::kMxRows32;
+  else if (m_each >= 256 && tiles(muon::kMx256x128) >= kCus) q.tile = muon::kMx256x128;
+  else if (tiles(muon::kMx128) >= kCus) q.tile = muon::kMx128;
+  else q.tile = muon::kMx64;
+  q.cols = muon::mx_tile_n(q.tile, blocks_m(q.tile), d->n);
+  g.tiles_m = (int32_t)blocks_m(q.tile);
+  g.tiles_n = (int32_t)((d->n + q.cols - 1) / q.cols);
+  if (q.few()) return q;
+  q.x_values = (uint64_t)muon::mx_value_bytes(d->rows, d->k);
+  q.x_scales = (uint64_t)muon::mx_scale_bytes(d->rows, d->k);
+  const int64_t t = (int64_t)g.tiles_m * g.tiles_n, chunks = muon::mx_chunks(d->k);
+  if (!grouped && t > 0 && t < kCus && chunks >= 4) {
+    const int64_t s = std::min<int64_t>((2 * kCus + t - 1) / t, chunks / 2), per = (chunks + s - 1) / s;
+    if (per < chunks) {
+      g.k_per = 4 * per;
+      g.splits = (int32_t)((chunks + per - 1) / per);
+      q.partials = (uint64_t)g.splits * g.m * g.n * 4;
+    }
+  }
+  return q;
 }
 
 }  // namespace
@@ -272,7 +295,7 @@ int muon_mx_sizes(const muon_mx_desc_t* d, uint64_t* values_bytes, uint64_t* sca
   if (!values_bytes || !scales_bytes) return bad("values_bytes or scales_bytes is null");
   *values_bytes = *scales_bytes = 0;
   MUON_TRY(check_mx(d));
-  *values_bytes = (uint64_t)mx_weights(d) * d->n * muon::mx_row_bytes(d->k);
+  *values_bytes = (uint64_t)mx_weights(d) * muon::mx_value_bytes(d->n, d->k);
   *scales_bytes = (uint64_t)mx_weights(d) * muon::mx_scale_bytes(d->n, d->k);
   return set_error(MUON_OK, "%s", "");
 }
@@ -303,7 +326,7 @@ int muon_mx_linear_workspace(const muon_mx_desc_t* d, uint64_t* bytes) {
   if (!bytes) return bad("bytes is null");
   *bytes = 0;
   MUON_TRY(check_mx(d));
-  if (d->rows > 0 && d->n > 0) *bytes = x_values(d) + x_scales(d) + mx_product(d).ws;
+  if (d->rows > 0 && d->n > 0) *bytes = mx_plan(d).bytes();
   return set_error(MUON_OK, "%s", "");
 }
 
@@ -323,25 +346,29 @@ int muon_mx_linear(const muon_mx_desc_t* d, const int32_t* offsets, const void* 
   MUON_TRY(check_at(y, d->rows * d->n, es, "y"));
   if (d->groups > 0 && residual) return bad("a grouped layer takes no residual");
   if (d->rows == 0 || d->n == 0) return set_error(MUON_OK, "%s", "");
-  muon::Product p = mx_product(d);
-  MUON_TRY(check_space(x_values(d) + x_scales(d) + p.ws, ws, ws_bytes));
+  MxPlan p = mx_plan(d);
+  MUON_TRY(check_space(p.bytes(), ws, ws_bytes));
   hipStream_t s = static_cast<hipStream_t>(stream);
-
-  muon::MxArgs q{};
-  q.src = x;
-  q.values = static_cast<uint8_t*>(ws);
-  q.scales = q.values + x_values(d);
-  q.rows = d->rows;
-  q.k = d->k;
-  q.ld = d->ldx;
-  q.groups = 1;
-  MUON_TRY(hip_result(muon::launch_mx_quantize(q, d->dtype, s), what));
-
-  muon::GemmArgs& g = p.g;
-  g.a = q.values;
+  muon::GemmArgs& g = p.p.g;
+  if (!p.few()) {
+    muon::MxArgs q{};
+    q.src = x;
+    q.values = static_cast<uint8_t*>(ws);
+    q.scales = q.values + p.x_values;
+    q.rows = d->rows;
+    q.k = d->k;
+    q.ld = d->ldx;
+    q.groups = 1;
+    MUON_TRY(hip_result(muon::launch_mx_quantize(q, d->dtype, s), what));
+    g.a = q.values;
+    p.p.sca = q.scales;
+    if (g.splits > 1) g.part = reinterpret_cast<float*>(q.scales + p.x_scales);
+  }
+  p.p.x = x;
+  p.p.ldx = d->ldx;
+  p.p.kx = d->k;
+  p.p.scb = scales;
   g.b = values;
-  g.sca = q.scales;
-  g.scb = scales;
   g.offsets = offsets;
   g.c = y;
   g.bias = bias;
@@ -350,8 +377,7 @@ int muon_mx_linear(const muon_mx_desc_t* d, const int32_t* offsets, const void* 
   g.ldr = d->ldr;
   g.sbias = d->n;
   g.act = d->act;
-  if (g.splits > 1) g.part = reinterpret_cast<float*>(q.scales + x_scales(d));
-  hipError_t e = muon::launch_gemm_mx(g, d->dtype, p.tile, s);
+  hipError_t e = muon::launch_mx_product(p.p, d->dtype, p.tile, p.cols, s);
   if (e == hipSuccess && g.splits > 1) e = muon::launch_gemm_join(g, d->dtype, s);
   return hip_result(e, what);
 }

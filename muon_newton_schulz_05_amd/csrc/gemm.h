@@ -97,31 +97,7 @@ template <> struct Mma<float> {
   }
 };
 
-// Four-bit operands (e2m1 values, two a byte, along k) of a product whose result has type O.  A byte is the unit
-// of k: a lane's fragment is 16 of them, 32 values that share one e8m0 scale, so a slice and its
-// fragments lie in LDS as bf16's do and the matrix cores take as long for them, for four times the work.
-template <typename O> struct Mx4 {
-  uint8_t pair;
-};
-template <typename O> struct Mma<Mx4<O>> {
-  static constexpr int N = 1;
-  typedef u32x4_t Frag;   // 32 values of one row: k = 128 s + 32 (lane / 16) + 0..31
-  // sa, sb: the fragments' scales, bytes BA and BB of them.
-  template <int BA, int BB>
-  static __device__ __forceinline__ f32x4_t mul(Frag a, Frag b, f32x4_t c, uint32_t sa, uint32_t sb) {
-    typedef int i32x8_t __attribute__((ext_vector_type(8)));
-    const i32x8_t a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};  // four bits read the first half
-    const i32x8_t b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    constexpr int kE2m1 = 4;
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, kE2m1, kE2m1, BA, (int)sa, BB, (int)sb);
-  }
-};
-template <typename T> struct Operand { typedef T Out; static constexpr bool MX = false; };
-template <typename O> struct Operand<Mx4<O>> { typedef O Out; static constexpr bool MX = true; };
-
 constexpr int KB = 128;  // bytes of a k-slice's row
-// Scales of a row in one slice: byte 2 g + s is that of substep s in lanes 16 g .. 16 g + 15.
-constexpr int kScaleRow = 8;
 
 // One operand's tile: R rows x one k-slice, loaded by NW waves (PD: slices held in
 // registers ahead of LDS where loads are not direct).
@@ -299,12 +275,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   typedef Panel<T, BM, TA, NW, LOADS, PD> PA;
   typedef Panel<T, BN, TB, NW, LOADS, PD> PB;
   typedef typename Mma<T>::Frag Frag;
-  typedef typename Operand<T>::Out O;
-  constexpr bool MX = Operand<T>::MX;
-  static_assert(!MX || (LOADS == kDirect16 && !TA && !TB), "four bits: both operands along k, in whole pieces");
-  // Scales reach LDS in loads of 32 rows, SL for each wave (those past the tiles' rows write zeros).
-  constexpr int SL = MX ? ((BM + BN) / 32 + NW - 1) / NW : 0, SCALES = SL * NW * 32 * kScaleRow;
-  constexpr int BK = PA::BK, SUB = KB / 64, STAGE = PA::BYTES + PB::BYTES + SCALES;
+  constexpr int BK = PA::BK, SUB = KB / 64, STAGE = PA::BYTES + PB::BYTES;
   constexpr int STRIDE = WN * 4 + 16;  // bytes of a staged epilogue row: 16 rows at one column fall on distinct 16-byte bank groups
   constexpr int LDS = WGK * (NS * STAGE > NW * 32 * STRIDE ? NS * STAGE : NW * 32 * STRIDE);
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
@@ -373,23 +344,6 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
     pa.init(reinterpret_cast<const char*>(A), g.lda * (int64_t)sizeof(T), rows_a, wave, lane);
     pb.init(reinterpret_cast<const char*>(B), g.ldb * (int64_t)sizeof(T), rows_b, wave, lane);
   }
-  // This wave's loads of scales: the first slice's address, the step from one slice to the next and the lane's offset.
-  const char* scale_at[MX ? SL : 1];
-  int64_t scale_step[MX ? SL : 1];
-  uint32_t scale_off[MX ? SL : 1];
-  if constexpr (MX) {
-#pragma unroll
-    for (int u = 0; u < SL; ++u) {
-      const int r = (wave + NW * u) * 32;  // of the tile's rows of A, then B
-      const bool of_a = r < BM;
-      const int64_t rows = of_a ? g.m : g.n, at = of_a ? row0 + r : (int64_t)tn * BN + r - BM;
-      const int left = r < BM + BN ? (of_a ? rows_a - r : rows_b - (r - BM)) : 0;
-      scale_step[u] = rows * kScaleRow;
-      scale_at[u] = static_cast<const char*>(of_a ? g.sca : g.scb) + (of_a || k1 == 0 ? 0 : e * g.sscb) +
-                    (k0 / KB) * scale_step[u] + at * kScaleRow;
-      scale_off[u] = lane / 2 < left ? 4 * lane : kNoLoad;
-    }
-  }
 
   f32x4_t acc[FM][FN];
 #pragma unroll
@@ -419,29 +373,6 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
 
   // Fragments of two substeps: one being read while the other is multiplied.
   Frag af[2][FM] = {}, bf[2][FN] = {};
-  // Scales of a slice, two blocks of rows a register (bytes 2 (block & 1) + substep): those being read, and those in use.
-  uint32_t sa[2][MX ? FM / 2 : 1] = {}, sb[2][MX ? (FN + 1) / 2 : 1] = {};
-  auto read_scales = [&](const char* st) __attribute__((always_inline)) {
-    if constexpr (MX) {
-      const char* p = st + PA::BYTES + PB::BYTES + (lane & 15) * kScaleRow + (lane >> 4) * 2;
-      auto two = [&](int r, bool second) __attribute__((always_inline)) {
-        const uint32_t lo = *reinterpret_cast<const uint16_t*>(p + r * kScaleRow);
-        return second ? lo | (uint32_t)*reinterpret_cast<const uint16_t*>(p + (r + 16) * kScaleRow) << 16 : lo;
-      };
-#pragma unroll
-      for (int i = 0; i < FM; i += 2) sa[1][i / 2] = two(wm * WM + 16 * i, true);
-#pragma unroll
-      for (int j = 0; j < FN; j += 2) sb[1][j / 2] = two(BM + wn * WN + 16 * j, j + 1 < FN);
-    }
-  };
-  auto use_scales = [&] __attribute__((always_inline)) {
-    if constexpr (MX) {
-#pragma unroll
-      for (int i = 0; i < FM / 2; ++i) sa[0][i] = sa[1][i];
-#pragma unroll
-      for (int j = 0; j < (FN + 1) / 2; ++j) sb[0][j] = sb[1][j];
-    }
-  };
   auto read = [&](const char* st, int s) __attribute__((always_inline)) {
     af[s & 1][0] = PA::frag(st, wm * WM, s, lane);
 #pragma unroll
@@ -457,25 +388,11 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          if constexpr (!MX) {
-            acc[i][j] = Mma<T>::mul(bf[s & 1][j], af[s & 1][i], acc[i][j], q);
-          } else {
-            auto mul = [&](auto bi, auto bj) __attribute__((always_inline)) {
-              constexpr int I = decltype(bi)::value, J = decltype(bj)::value;
-              return s & 1 ? Mma<T>::template mul<2 * J + 1, 2 * I + 1>(bf[1][j], af[1][i], acc[i][j], sb[0][j / 2], sa[0][i / 2])
-                           : Mma<T>::template mul<2 * J, 2 * I>(bf[0][j], af[0][i], acc[i][j], sb[0][j / 2], sa[0][i / 2]);
-            };
-            typedef std::integral_constant<int, 0> Zero;
-            typedef std::integral_constant<int, 1> One;
-            acc[i][j] = i & 1 ? (j & 1 ? mul(One{}, One{}) : mul(One{}, Zero{}))
-                              : (j & 1 ? mul(Zero{}, One{}) : mul(Zero{}, Zero{}));
-          }
-        }
+        for (int j = 0; j < FN; ++j) acc[i][j] = Mma<T>::mul(bf[s & 1][j], af[s & 1][i], acc[i][j], q);
   };
 
   if constexpr (DIRECT) {
-    constexpr int L = PA::LI + PB::LI + SL;
+    constexpr int L = PA::LI + PB::LI;
     char* stages = lds + set * NS * STAGE;
     const int its = (nk + WGK - 1) / WGK;  // slices of a set (those past the end are zeros)
     auto issue = [&](int it, char* fill) __attribute__((always_inline)) {
@@ -483,12 +400,6 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
       const int k_left = (int)max((int64_t)0, min((int64_t)BK, kk - (int64_t)kt * BK));
       pa.issue(kt, k_left, fill, wave, lane);
       pb.issue(kt, k_left, fill + PA::BYTES, wave, lane);
-      if constexpr (MX) {
-#pragma unroll
-        for (int u = 0; u < SL; ++u)
-          load_to_lds<4>(scale_at[u] + kt * scale_step[u], k_left > 0 ? scale_off[u] : kNoLoad,
-                         fill + PA::BYTES + PB::BYTES + (wave + NW * u) * 32 * kScaleRow);
-      }
     };
     if (nk > 0) {
 #pragma unroll
@@ -517,13 +428,11 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
 #pragma unroll
           for (int s = 0; s < SUB; ++s) {
             read(st, s);
-            if (MX && s == 0) read_scales(st);
-            if (MX && s == 1) use_scales();  // the slice before has been multiplied
             multiply(s + 1);  // of the other parity: substep s - 1
             // The loads go out over the first half of the substep's products: at 8192^3
             // on one card 1416 / 1419 / 1411 TFLOP/s (forward, dx, dW) against 1388 /
             // 1392 / 1345 over all of them and 1407 / 1371 / 1406 over the first quarter.
-            if (s == 0) interleave<RD + (MX ? FM + FN : 0), L, MM / 2, MM>();
+            if (s == 0) interleave<RD, L, MM / 2, MM>();
             else interleave<RD, 0, 1, MM>();
           }
         };
@@ -584,7 +493,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
   const int n_in = (int)min((int64_t)8, g.n - col);
   float bias[8] = {};
   if (g.bias && n_in > 0 && !g.part && !(!GK && e == g.groups && g.offsets))
-    load8(static_cast<const O*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n_in, bias);
+    load8(static_cast<const T*>(g.bias) + (GK ? 0 : e * g.sbias) + col, n_in, bias);
   // Where n is a multiple of 8 every piece is whole: no branch between the loads and
   // stores of a strip.
   auto strips = [&](auto full_tag) __attribute__((always_inline)) {
@@ -620,7 +529,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK) void k_gemm(GemmArgs g) {
         const int64_t row = row0 + wm * WM + 32 * i + lr;
         if (pr < ROWS && row < end && n_in > 0) {
           if (g.part) store8(g.part + (((int64_t)split * (GK ? g.groups : 1) + (GK ? e : 0)) * g.m + row) * g.n + col, n, v);
-          else finish8<O>(g, v, bias, GK ? e : 0, row, col, n);
+          else finish8<T>(g, v, bias, GK ? e : 0, row, col, n);
         }
       }
       if constexpr (WGK == 1) wave_fence();
@@ -667,12 +576,7 @@ hipError_t launch_tile(const GemmArgs& g, bool ta, bool tb, hipStream_t s) {
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(64 * WGM * WGN * WGK);
-  if constexpr (Operand<T>::MX) {
-    if (ta || tb) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, false, false, LOADS>), grid, block, 0, s, g);
-    return hipGetLastError();
-  }
-  else if (ta && tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, true, true, LOADS>), grid, block, 0, s, g);
+  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, true, true, LOADS>), grid, block, 0, s, g);
   else if (tb) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, false, true, LOADS>), grid, block, 0, s, g);
   else if (!ta) hipLaunchKernelGGL((k_gemm<T, BM, BN, WGM, WGN, WGK, NS, false, false, LOADS>), grid, block, 0, s, g);
   else return hipErrorInvalidValue;

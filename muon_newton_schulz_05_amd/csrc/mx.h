@@ -4,24 +4,49 @@
 
 namespace muon {
 
-// R rows of K values: e2m1 values two a byte (the lower bits first), rows of K rounded up to 32 values; and one
-// e8m0 scale for each 32 of a row.  Scales lie by slices of 256 values, [slice][row][8], so that the rows of a
-// tile are one stretch of a slice; byte 2 (b mod 4) + b / 4 of a row's eight is that of the slice's block b,
-// which puts the two substeps of one lane group side by side.  What pads a row is zero.
-constexpr int kMxBlock = 32, kMxSlice = 256;
-inline int64_t mx_row_bytes(int64_t k) { return (k + kMxBlock - 1) / kMxBlock * (kMxBlock / 2); }
-inline int64_t mx_scale_bytes(int64_t rows, int64_t k) { return (k + kMxSlice - 1) / kMxSlice * rows * 8; }
+// R rows of K values, by slices of 128 values (64 bytes) of every row: values [slice][row][64], e2m1 two a byte, the
+// lower bits first; and by chunks of four slices the e8m0 scales, [chunk][row][16]: byte 4 g + s of a row is that
+// of the 32 values g (0..3) of the chunk's slice s.  The rows of a tile are so one stretch of a slice, whole lines
+// for any tile; 16 rows of a slice are, in order, what the lanes of a wave hand to a matrix
+// instruction; and four bytes are a lane's scales for a chunk.  What pads K is zero.
+constexpr int kMxBlock = 32, kMxSlice = 128, kMxSliceBytes = 64, kMxChunk = 512, kMxChunkBytes = 16;
+inline __host__ __device__ int64_t mx_slices(int64_t k) { return (k + kMxSlice - 1) / kMxSlice; }
+inline __host__ __device__ int64_t mx_chunks(int64_t k) { return (k + kMxChunk - 1) / kMxChunk; }
+inline int64_t mx_value_bytes(int64_t rows, int64_t k) { return mx_slices(k) * rows * kMxSliceBytes; }
+inline int64_t mx_scale_bytes(int64_t rows, int64_t k) { return mx_chunks(k) * rows * kMxChunkBytes; }
 
 struct MxArgs {
   const void* src;       // element (r, j) at r ld + j, or where t at j ld + r; one group's `step` behind another's
-  uint8_t* values;       // [groups][rows][row bytes]
-  uint8_t* scales;       // [groups][slices][rows][8]
-  void* dst;             // dequantised rows of k
+  uint8_t* values;       // of each group
+  uint8_t* scales;
+  void* dst;             // dequantised rows of k, contiguous
   int64_t rows, k, ld, step;
   int32_t groups, t;
 };
 hipError_t launch_mx_quantize(const MxArgs& a, int dtype, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxArgs& a, int dtype, hipStream_t s);
-hipError_t launch_gemm_mx(const GemmArgs& g, int dtype, int tile, hipStream_t s);
+
+// C = act(A B^T + bias) + res of A [m, k] and B [groups][n, k] in four bits; k and k_per of `g` count slices, k_per
+// a multiple of four.
+struct MxProduct {
+  GemmArgs g;
+  const uint8_t* sca;    // scales of A
+  const uint8_t* scb;
+  const void* x;         // kMxRows16 and kMxRows32: A itself, taken to four bits on the way
+  int64_t ldx, kx;
+};
+enum MxTile { kMx256x128 = 0, kMx128, kMx64, kMxRows32, kMxRows16 };
+inline int mx_tile_m(int tile) {
+  constexpr int rows[] = {256, 128, 64, 32, 16};
+  return rows[tile];
+}
+// Columns of a workgroup: fixed for the tiles in LDS; for few rows, as few as it takes to occupy every compute unit.
+inline int mx_tile_n(int tile, int64_t blocks_m, int64_t n) {
+  if (tile <= kMx64) return tile == kMx64 ? 64 : 128;
+  int cols = 64;
+  while (cols > 16 && blocks_m * ((n + cols - 1) / cols) < 256) cols /= 2;
+  return cols;
+}
+hipError_t launch_mx_product(const MxProduct& a, int dtype, int tile, int cols, hipStream_t s);
 
 }  // namespace muon

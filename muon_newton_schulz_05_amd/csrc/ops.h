@@ -35,10 +35,6 @@ struct GemmArgs {
                            // contraction's splits go by each group's length
   int32_t tiles_m, tiles_n;
   int32_t pairs;           // join: row r of the result is row 2r and, where that is finite, row 2r + 1
-  // four-bit operands (k in bytes of two values): the scales of A and B, [slices of 128 bytes][rows][8]
-  const void* sca;
-  const void* scb;
-  int64_t sscb;            // scales of one group's B
 };
 
 enum GemmTile { kTile128 = 0, kTile256, kTile256x128, kTile64, kTile32x64, kTileRows32, kTileRows32K };

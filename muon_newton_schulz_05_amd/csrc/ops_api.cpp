@@ -7,7 +7,7 @@
 
 #include "../../include/muon_ops.h"
 #include "api_common.h"
-#include "product.h"
+#include "ops.h"
 
 namespace {
 
@@ -15,7 +15,6 @@ using muon::aligned;
 using muon::bad;
 using muon::elem;
 using muon::hip_result;
-using muon::Product;
 using muon::set_error;
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
@@ -53,6 +52,18 @@ int both_loads(int a, int b) {
   if (a == muon::kStaged || b == muon::kStaged) return muon::kStaged;
   return a == muon::kDirect16 && b == muon::kDirect16 ? muon::kDirect16 : muon::kDirect4;
 }
+
+struct Product {
+  muon::GemmArgs g{};
+  int tile = muon::kTile128;
+  int loads = muon::kStaged;
+  uint64_t ws = 0;            // partials of a split contraction
+  muon::AlignArgs copy[2]{};  // of A and B, where copy_bytes > 0
+  uint64_t copy_bytes[2] = {0, 0};
+  bool pairs = false;         // rows 2r and 2r + 1 are added to one row of C
+  uint64_t total() const { return ws + copy_bytes[0] + copy_bytes[1]; }
+  uint64_t need() const { return g.m == 0 || g.n == 0 ? 0 : total(); }  // nothing to compute: nothing is used
+};
 
 // A larger bf16 product whose operands no 16-byte loads reach first copies them
 // into rows that they do, padded with zeros, which add nothing.  Without and with
@@ -134,9 +145,7 @@ bool align_operands(Product* p, int dtype, bool ta, bool tb, const int (&have)[2
 // number at least the groups with rows.  A grouped contraction has groups of
 // unlike length, and is split until the card is filled four times (three
 // experts' [678, 520] over 31936 rows, float32 dW: 345 against 383).
-}  // namespace
-
-void muon::plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups) {
+void plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int groups) {
   muon::GemmArgs& g = p->g;
   const bool gk = ta && tb, grouped = groups > 0;
   auto tiles = [&](int t) {
@@ -189,12 +198,10 @@ void muon::plan_product(Product* p, int dtype, bool ta, bool tb, int loads, int 
   }
 }
 
-namespace {
-
 void plan_aligned(Product* p, int dtype, bool ta, bool tb, int la, int lb, int groups) {
   int loads = both_loads(la, lb);
   if (loads != muon::kDirect16 && align_operands(p, dtype, ta, tb, {la, lb}, groups)) loads = muon::kDirect16;
-  muon::plan_product(p, dtype, ta, tb, loads, groups);
+  plan_product(p, dtype, ta, tb, loads, groups);
 }
 
 int check_workspace(uint64_t need, const void* ws, uint64_t ws_bytes) {

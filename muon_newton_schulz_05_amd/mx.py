@@ -22,22 +22,23 @@ MX_MAX_SIZE = 1 << 23
 class MxWeight(NamedTuple):
     """A weight [K, N] or [E, K, N] in four bits.
 
-    values [..., N, 16 ceil(K / 32)] uint8: each column's values along K, two a byte, the lower half first;
-    scales [..., ceil(K / 256), N, 8] uint8: byte 2 (b mod 4) + b / 4 of eight is the power of two (+ 127) of block b of
-    256 values; k is K."""
+    values [..., ceil(K / 128), N, 64] uint8: each column's values by slices of 128 along K, two a byte, the lower half
+    first; scales [..., ceil(K / 512), N, 16] uint8: byte 4 g + s is the power of two (+ 127) of the 32 values g of
+    slice s of 512; k is K."""
     values: torch.Tensor
     scales: torch.Tensor
     k: int
 
     @property
     def shape(self):
-        return torch.Size((*self.values.shape[:-2], self.k, self.values.shape[-2]))
+        return torch.Size((*self.values.shape[:-3], self.k, self.values.shape[-2]))
 
 
 def _check_weight(q):
     v, s, k = q
-    if v.dim() not in (2, 3) or v.dtype is not torch.uint8 or s.dtype is not torch.uint8 or not 0 <= k <= MX_MAX_SIZE \
-            or v.shape[-1] != (k + 31) // 32 * 16 or s.shape != (*v.shape[:-2], (k + 255) // 256, v.shape[-2], 8) \
+    if v.dim() not in (3, 4) or v.dtype is not torch.uint8 or s.dtype is not torch.uint8 or not 0 <= k <= MX_MAX_SIZE \
+            or v.shape[-3] != (k + 127) // 128 or v.shape[-1] != 64 \
+            or s.shape != (*v.shape[:-3], (k + 511) // 512, v.shape[-2], 16) \
             or not v.is_contiguous() or not s.is_contiguous():
         raise ValueError("the weight must be what mx_quantize() returned")
     _gpu(v, "the weight")
@@ -71,8 +72,8 @@ def mx_quantize(weight):
         layout, ld = 1, w.stride(-1) if n > 1 else max(k, 1)
     d = _plan(MxDesc, None, code, 0, groups, layout, 0, k, n, 0, ld, w.stride(0) if groups else 0, 0)[0]
     lead = weight.shape[:-2]
-    values = torch.empty((*lead, n, (k + 31) // 32 * 16), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((*lead, (k + 255) // 256, n, 8), dtype=torch.uint8, device=w.device)
+    values = torch.empty((*lead, (k + 127) // 128, n, 64), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((*lead, (k + 511) // 512, n, 16), dtype=torch.uint8, device=w.device)
     _call("muon_mx_quantize", w, d, w.data_ptr(), values.data_ptr(), scales.data_ptr())
     return MxWeight(values, scales, k)
 
@@ -81,7 +82,7 @@ def mx_dequantize(weight, dtype=torch.float32):
     """The values that an ``MxWeight`` stands for, exactly: [K, N] or [E, K, N], contiguous along K."""
     _check_weight(weight)
     values, scales, k = weight
-    n, lead = values.shape[-2], values.shape[:-2]
+    n, lead = values.shape[-2], values.shape[:-3]
     out = torch.empty((*lead, n, k), dtype=dtype, device=values.device)
     d = _plan(MxDesc, None, _dtype(out, "dtype"), 0, lead[0] if lead else 0, 0, 0, k, n, 0, n, 0, 0)[0]
     _call("muon_mx_dequantize", values, d, values.data_ptr(), scales.data_ptr(), out.data_ptr())

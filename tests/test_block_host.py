@@ -221,7 +221,7 @@ def test_balance_checks_every_pointer(block):
 @no_gpu
 @pytest.mark.parametrize("groups", [0, 3])
 def test_mx_checks_every_pointer(block, groups):
-    lib, d = block.load_block(), mx_desc(block, groups=groups, w_stride=64 * 32)
+    lib, d = block.load_block(), mx_desc(block, groups=groups, w_stride=64 * 32, rows=200)
     need = ctypes.c_uint64(0)
     for f in (lib.muon_mx_quantize, lib.muon_mx_dequantize):
         order = (lambda w, v, s: (w, v, s)) if f is lib.muon_mx_quantize else (lambda w, v, s: (v, s, w))
@@ -253,7 +253,7 @@ def test_mx_sizes(block):
     for groups, k, n in ((0, 1, 1), (0, 32, 5), (0, 33, 5), (2, 257, 3), (0, 0, 4), (7, 4096, 16384)):
         assert lib.muon_mx_sizes(ctypes.byref(mx_desc(block, groups=groups, k=k, n=n)), ctypes.byref(v), ctypes.byref(s)) == 0
         e = max(groups, 1)
-        assert v.value == e * n * -(-k // 32) * 16 and s.value == e * -(-k // 256) * n * 8
+        assert v.value == e * n * -(-k // 128) * 64 and s.value == e * -(-k // 512) * n * 16
 
 
 # ------------------------------------------------------------------ the binding
@@ -275,8 +275,8 @@ def calls(x):
     return {"layer_norm": lambda: muon.layer_norm(x, w, w), "layer_norm, residual": lambda: muon.layer_norm(
         torch.ones_like(x.detach()), w, residual=x), "rms_norm": lambda: muon.rms_norm(x, w),
         "gate": lambda: muon.gate(x, 2), "balance_loss": lambda: muon.balance_loss(x, ids),
-        "mx_linear": lambda: muon.mx_linear(x, muon.MxWeight(torch.zeros(4, 16, dtype=torch.uint8),
-                                                             torch.zeros(1, 4, 8, dtype=torch.uint8), 8))}
+        "mx_linear": lambda: muon.mx_linear(x, muon.MxWeight(torch.zeros(1, 4, 64, dtype=torch.uint8),
+                                                             torch.zeros(1, 4, 16, dtype=torch.uint8), 8))}
 
 
 NAMES = ("layer_norm", "layer_norm, residual", "rms_norm", "gate", "balance_loss", "mx_linear")
@@ -370,12 +370,13 @@ def test_the_binding_refuses_weights_that_do_not_fit(block, mx):
     U8, G = torch.uint8, Elsewhere
 
     def weight(k=40, n=4, lead=(), values=None, scales=None):
-        return muon.MxWeight(G(*lead, n, (k + 31) // 32 * 16, dtype=U8) if values is None else values,
-                             G(*lead, (k + 255) // 256, n, 8, dtype=U8) if scales is None else scales, k)
+        return muon.MxWeight(G(*lead, (k + 127) // 128, n, 64, dtype=U8) if values is None else values,
+                             G(*lead, (k + 511) // 512, n, 16, dtype=U8) if scales is None else scales, k)
     x, off = G(3, 40), G(3, dtype=torch.int32)
-    for w in (weight(values=G(4, 16, dtype=U8)), weight(values=G(4, 32)), weight(scales=G(2, 4, 8, dtype=U8)),
-              weight(scales=G(1, 4, 8)), weight(scales=G(1, 5, 8, dtype=U8)), weight(values=torch.zeros(4, 32, dtype=U8)),
-              weight(scales=torch.zeros(1, 4, 8, dtype=U8)), muon.MxWeight(G(4, 0, dtype=U8), G(0, 4, 8, dtype=U8), -1)):
+    for w in (weight(values=G(2, 4, 64, dtype=U8)), weight(values=G(1, 4, 32, dtype=U8)), weight(values=G(1, 4, 64)),
+              weight(values=G(4, 64, dtype=U8)), weight(scales=G(2, 4, 16, dtype=U8)), weight(scales=G(1, 4, 16)),
+              weight(scales=G(1, 5, 16, dtype=U8)), weight(values=torch.zeros(1, 4, 64, dtype=U8)),
+              weight(scales=torch.zeros(1, 4, 16, dtype=U8)), muon.MxWeight(G(0, 4, 64, dtype=U8), G(0, 4, 16, dtype=U8), -1)):
         for call in (lambda: muon.mx_linear(x, w), lambda: muon.mx_dequantize(w)):
             with pytest.raises(ValueError):
                 call()

@@ -29,18 +29,19 @@ def normal(shape, dtype, seed, std=1.0):
 
 
 def held(codes):
-    """values [N, bytes] from codes [N, padded K], the lower half of a byte first."""
-    return (codes[:, ::2] | codes[:, 1::2] << 4).to(torch.uint8)
+    """values [slices, N, 64] from codes [N, padded K], the lower half of a byte first."""
+    n = codes.shape[0]
+    full = torch.zeros(n, -(-codes.shape[1] // 128) * 128, dtype=torch.int64)
+    full[:, :codes.shape[1]] = codes
+    return (full[:, ::2] | full[:, 1::2] << 4).to(torch.uint8).view(n, -1, 64).transpose(0, 1)
 
 
 def placed(scales, k):
-    """scales [slices, N, 8] from [N, blocks]: byte 2 (b mod 4) + b / 4 is block b's of a slice."""
+    """scales [chunks, N, 16] from [N, blocks]: byte 4 g + s is that of the 32 values g of slice s of 512."""
     n, nb = scales.shape
-    ns = -(-k // 256)
-    out = torch.zeros(ns, n, 8, dtype=torch.uint8)
+    out = torch.zeros(-(-k // 512), n, 16, dtype=torch.uint8)
     for b in range(nb):
-        q, i = divmod(b, 8)
-        out[q, :, 2 * (i % 4) + i // 4] = scales[:, b].to(torch.uint8)
+        out[b // 16, :, 4 * (b % 4) + b // 4 % 4] = scales[:, b].to(torch.uint8)
     return out
 
 
@@ -88,7 +89,7 @@ def test_quantize_borders_and_extremes(muon, dtype):
         q = muon.mx_quantize(g)
         assert torch.equal(q.scales.cpu(), placed(scales, 32))
         ok = scales[:, 0] != 255
-        assert torch.equal(q.values.cpu()[ok], held(codes)[ok])
+        assert torch.equal(q.values.cpu()[:, ok], held(codes)[:, ok])
         back = muon.mx_dequantize(q, dtype).double().cpu().t()
         assert torch.equal(back[ok], values[ok]) and back[~ok].isnan().all()
 
