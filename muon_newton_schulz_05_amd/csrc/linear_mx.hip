@@ -34,13 +34,10 @@ __device__ __forceinline__ f32x4_t multiply4(u32x4_t a, u32x4_t b, f32x4_t c, ui
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kRsrcFlags);
 }
-// N loads of 1 KiB, one behind the other in memory and in LDS (an instruction's offset counts for both).
-template <int N, int U = 0>
+// Load U of 1 KiB of those that lie one behind the other in memory and in LDS (an instruction's offset counts for both).
+template <int U>
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, char* dst) {
-  if constexpr (U < N) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void LDS_PTR*)dst, 16, off, 0, U * 1024, 0);
-    to_lds<N, U + 1>(rs, off, dst);
-  }
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void LDS_PTR*)dst, 16, off, 0, U * 1024, 0);
 }
 
 // What all lanes share, in scalar registers.
@@ -49,6 +46,15 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
   return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
+}
+
+// f of 0 .. N - 1, as constants.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void counted(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    counted<N, I + 1>(f);
+  }
 }
 
 // The workgroup's place: its rows [row0, end) of group e, its column tile, its slices [s0, s0 + steps).
@@ -87,12 +93,23 @@ struct Place {
   }
 };
 
-// Eight columns of one row leave: partial sums, or through the epilogue.
-template <typename O>
-__device__ __forceinline__ void leave8(const GemmArgs& g, const Place& at, float (&v)[8], const float (&bias)[8], int64_t row,
-                                       int col, int n) {
-  if (g.part) store8(g.part + ((int64_t)at.split * g.m + row) * g.n + col, n, v);
-  else finish8<O>(g, v, bias, 0, row, col, n);
+// The activation of N pieces of eight, chosen once for all of them.
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&v)[N][8]) {
+#pragma unroll
+  for (int p = 0; p < N; ++p)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[p][u] = act_f(v[p][u], ACT);
+}
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N][8], int act) {
+  switch (act) {
+    case MUON_ACT_RELU: return act_all<MUON_ACT_RELU>(v);
+    case MUON_ACT_SILU: return act_all<MUON_ACT_SILU>(v);
+    case MUON_ACT_GELU: return act_all<MUON_ACT_GELU>(v);
+    case MUON_ACT_GELU_TANH: return act_all<MUON_ACT_GELU_TANH>(v);
+    default: return;
+  }
 }
 template <typename O>
 __device__ __forceinline__ void bias8(const GemmArgs& g, const Place& at, int col, int n, float (&bias)[8]) {
@@ -129,11 +146,14 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void k_mx_tile(MxProduct a) {
   const uint8_t* const A_wave = A + wave * LA * 1024;
   const uint8_t* const B_wave = B + wave * LB * 1024;
   const int bytes_a = max(0, rows_a * SB - wave * LA * 1024), bytes_b = max(0, rows_b * SB - wave * LB * 1024);
-  auto issue = [&](int h, char* st) __attribute__((always_inline)) {
+  // Load U of slice h: A's, then B's.
+  auto issue = [&](int h, char* st, auto which) __attribute__((always_inline)) {
+    constexpr int U = decltype(which)::value;
     const bool in = h < steps;
-    to_lds<LA>(descriptor(A_wave + (int64_t)h * g.m * SB, in ? bytes_a : 0), from, st + wave * LA * 1024);
-    to_lds<LB>(descriptor(B_wave + (int64_t)h * g.n * SB, in ? bytes_b : 0), from, st + BM * SB + wave * LB * 1024);
+    if constexpr (U < LA) to_lds<U>(descriptor(A_wave + (int64_t)h * g.m * SB, in ? bytes_a : 0), from, st + wave * LA * 1024);
+    else to_lds<U - LA>(descriptor(B_wave + (int64_t)h * g.n * SB, in ? bytes_b : 0), from, st + BM * SB + wave * LB * 1024);
   };
+  auto issue_all = [&](int h, char* st) __attribute__((always_inline)) { counted<L>([&](auto u) { issue(h, st, u); }); };
   // This wave's loads of scales: where the first chunk's are, the step to the next one's, and their bytes.
   const uint8_t* scale_from[SL];
   int64_t scale_step[SL];
@@ -150,7 +170,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void k_mx_tile(MxProduct a) {
   auto issue_scales = [&](int chunk) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < SL; ++u)
-      to_lds<1>(descriptor(scale_from[u] + chunk * scale_step[u], 4 * chunk < steps ? scale_bytes[u] : 0), 16 * lane,
+      to_lds<0>(descriptor(scale_from[u] + chunk * scale_step[u], 4 * chunk < steps ? scale_bytes[u] : 0), 16 * lane,
                 scales + (wave * SL + u) * 1024);
   };
 
@@ -172,19 +192,24 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void k_mx_tile(MxProduct a) {
     for (int i = 0; i < FM; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(scale_at + (wm * WM + 16 * i) * kMxChunkBytes);
   };
   // Multiplies slice S of its chunk (products of B by A: a block's register u in a lane is row lane mod 16 and column 4
-  // (lane / 16) + u) and reads the next slice, from st, in its place.  The order is kept as written: left to itself the
-  // compiler holds fragments of three slices, and spills.
-  auto multiply = [&](auto slice, const char* st, auto more) __attribute__((always_inline)) {
+  // (lane / 16) + u) and, with MORE, reads the next slice from st in its place and lets slice h's loads to `fill` out, one
+  // behind each block's products: together they would hold up the wave.  The order is kept as written: left to
+  // itself the compiler holds fragments of three slices, and spills.
+  auto multiply = [&](auto slice, auto more, const char* st, int h, char* fill) __attribute__((always_inline)) {
     constexpr int S = decltype(slice)::value, Q = S & 1;
     constexpr bool MORE = decltype(more)::value;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      if (MORE && i < FN) bf[Q ^ 1][i] = *reinterpret_cast<const u32x4_t*>(st + (BM + wn * WN + 16 * i) * SB);
+    counted<FM>([&](auto row) __attribute__((always_inline)) {
+      constexpr int i = decltype(row)::value;
+      if constexpr (MORE && i < FN) bf[Q ^ 1][i] = *reinterpret_cast<const u32x4_t*>(st + (BM + wn * WN + 16 * i) * SB);
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = multiply4<S>(bf[Q][j], af[i], acc[i][j], sb[j], sa[i]);
-      if (MORE) af[i] = *reinterpret_cast<const u32x4_t*>(st + (wm * WM + 16 * i) * SB);
+      if constexpr (MORE) {
+        af[i] = *reinterpret_cast<const u32x4_t*>(st + (wm * WM + 16 * i) * SB);
+        static_assert(L <= FM, "loads of a slice");
+        if constexpr (i < L) issue(h, fill, row);
+      }
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
   };
 
   const bool idle = wm * WM >= rows_a || wn * WN >= rows_b;  // nothing of C: such a wave only loads
@@ -199,11 +224,13 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void k_mx_tile(MxProduct a) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if constexpr (P == 2) issue_scales((h >> 2) + 1);
-    issue(h + NS - 1, lds + (stage == 0 ? NS - 1 : stage - 1) * STAGE);
-    if constexpr (!decltype(idle_tag)::value) {
+    char* const fill = lds + (stage == 0 ? NS - 1 : stage - 1) * STAGE;
+    if constexpr (decltype(idle_tag)::value) {
+      issue_all(h + NS - 1, fill);
+    } else {
       if constexpr (P == 1) read_scales();
       __builtin_amdgcn_sched_barrier(0);
-      multiply(std::integral_constant<int, (P + 3) & 3>{}, frag_at + stage * STAGE, std::true_type{});
+      multiply(std::integral_constant<int, (P + 3) & 3>{}, std::true_type{}, frag_at + stage * STAGE, h + NS - 1, fill);
     }
     stage = stage == NS - 1 ? 0 : stage + 1;
   };
@@ -215,14 +242,14 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void k_mx_tile(MxProduct a) {
       step(h + 2, std::integral_constant<int, 2>{}, idle_tag);
       step(h + 3, std::integral_constant<int, 3>{}, idle_tag);
     }
-    if constexpr (!decltype(idle_tag)::value) multiply(std::integral_constant<int, 3>{}, nullptr, std::false_type{});
+    if constexpr (!decltype(idle_tag)::value) multiply(std::integral_constant<int, 3>{}, std::false_type{}, nullptr, 0, nullptr);
   };
   if (steps > 0) {
     // As the steps ahead of the first would have: scales two steps ahead of it, with the slice of that step.
 #pragma unroll
     for (int p = 0; p < NS - 1; ++p) {
       if (p == NS - 3) issue_scales(0);
-      issue(p, lds + p * STAGE);
+      issue_all(p, lds + p * STAGE);
     }
     if (idle) run(std::true_type{});
     else run(std::false_type{});
@@ -268,23 +295,40 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void k_mx_tile(MxProduct a) {
         const f32x4_t x = src[0], y = src[1];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[p][u] = u < 4 ? x[u & 3] : y[u & 3];
-        if constexpr (RES) {
+      }
+      if (!g.part) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[p][u] = act_f(v[p][u] + bias[u], g.act);
+        for (int p = 0; p < PS; ++p)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[p][u] += bias[u];
+        activate(v, g.act);
+      }
+      if constexpr (RES) {
+#pragma unroll
+        for (int p = 0; p < PS; ++p)
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             if constexpr (sizeof(O) == 2) v[p][u] += u & 1 ? bf16_hi(res[p][0][u / 2]) : bf16_lo(res[p][0][u / 2]);
             else v[p][u] += __uint_as_float(res[p][u / 4][u & 3]);
           }
-        }
+        if (i + 1 < WM / 32) fetch(i + 1);
       }
-      if (i + 1 < WM / 32) fetch(i + 1);
 #pragma unroll
       for (int p = 0; p < PS; ++p) {
         const int64_t row = row0 + wm * WM + 32 * i + p * RPP + lane / LPR;
         if (row < at.end && n_in > 0) {
-          if constexpr (RES) store8(static_cast<O*>(g.c) + row * g.ldc + col, 8, v[p]);
-          else leave8<O>(g, at, v[p], bias, row, col, FULL ? 8 : n_in);
+          const int n = FULL ? 8 : n_in;
+          if (g.part) {
+            store8(g.part + ((int64_t)at.split * g.m + row) * g.n + col, n, v[p]);
+          } else {
+            if (!FULL && g.res) {
+              float r[8];
+              load8(static_cast<const O*>(g.res) + row * g.ldr + col, n, r);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) v[p][u] += r[u];
+            }
+            store8(static_cast<O*>(g.c) + row * g.ldc + col, n, v[p]);
+          }
         }
       }
       wave_fence();
@@ -399,7 +443,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_rows(MxProduct a) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) v[u] += sums[(w * BM + lr) * STRIDE + c8 + u];
   bias8<O>(g, at, col, n, bias);
-  leave8<O>(g, at, v, bias, at.row0 + lr, col, n);
+  finish8<O>(g, v, bias, 0, at.row0 + lr, col, n);
 }
 
 template <typename O>
