@@ -114,74 +114,99 @@ __global__ __launch_bounds__(kThreads(TPR)) void k_norm(NormArgs a) {
   }
 }
 
+// Eight elements as they lie in memory, so that a load can be in flight while other work goes on.
+template <typename T> struct Raw {
+  u32x4_t r[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if (n >= 8) {
+#pragma unroll
+      for (int q = 0; q < (int)sizeof(T) / 2; ++q) r[q] = load16(p + q * (16 / sizeof(T)));
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < (int)sizeof(T) / 2; ++q) r[q] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 4) r[i >> 2][i & 3] = __float_as_uint(p[i]);
+        else r[0][i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+      }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i >> 2][i & 3]);
+    else return i & 1 ? bf16_hi(r[0][i >> 1]) : bf16_lo(r[0][i >> 1]);
+  }
+};
+
+// Eight columns a thread; a workgroup walks its rows with the next one's loads in flight.
 // a.part: [workgroups][2][cols], dw's sums and db's.
-template <typename T, int TPR, int CH>
+template <typename T, int TPR>
 __global__ __launch_bounds__(kThreads(TPR)) void k_norm_grad(NormGradArgs a) {
   constexpr int NT = kThreads(TPR), RPB = NT / TPR;
   __shared__ float red[2][RPB][2 * 16];
-  __shared__ float sums[RPB > 1 ? NT * CH * 8 : 1];
-  const int l = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  __shared__ float sums[RPB > 1 ? NT * 8 : 1];
+  const int l = threadIdx.x % TPR, sub = threadIdx.x / TPR, col = l * 8;
   const float per = 1.f / (float)a.cols;
-  int n[CH];
-  float w[CH][8], dw[CH][8] = {}, db[CH][8] = {};
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int col = (c * TPR + l) * 8;
-    n[c] = (int)max((int64_t)0, min((int64_t)8, a.cols - col));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[c][i] = 1.f;
-    if (a.w) load8(static_cast<const T*>(a.w) + col, n[c], w[c]);
-  }
+  const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - col));
+  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, dw[8] = {}, db[8] = {};
+  if (a.w) load8(static_cast<const T*>(a.w) + col, n, w);
+  Raw<T> rx, rg, rd;
+  float mean = 0.f, rstd = 0.f;
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    const bool in = row < a.rows;
+    const int m = in ? n : 0;
+    rx.load(static_cast<const T*>(a.s) + row * a.lds + col, m);
+    rg.load(static_cast<const T*>(a.dy) + row * a.ldg + col, m);
+    if (a.ds) rd.load(static_cast<const T*>(a.ds) + row * a.ldd + col, m);
+    mean = in && a.layer ? a.stats[2 * row] : 0.f;
+    rstd = in ? a.stats[2 * row + 1] : 0.f;
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
+  fetch((int64_t)blockIdx.x * RPB + sub);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += step, turn ^= 1) {
     const int64_t row = r0 + sub;
     const bool in = row < a.rows;
-    const float mean = in && a.layer ? a.stats[2 * row] : 0.f, rstd = in ? a.stats[2 * row + 1] : 0.f;
-    float x[CH][8], g[CH][8], d[CH][8] = {}, t[2] = {0.f, 0.f};
+    const Raw<T> cx = rx, cg = rg, cd = rd;
+    const float mu = mean, rs = rstd;
+    fetch(row + step);
+    float x[8], g[8], t[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (c * TPR + l) * 8, m = in ? n[c] : 0;
-      load8(static_cast<const T*>(a.s) + row * a.lds + col, m, x[c]);
-      load8(static_cast<const T*>(a.dy) + row * a.ldg + col, m, g[c]);
-      if (a.ds) load8(static_cast<const T*>(a.ds) + row * a.ldd + col, m, d[c]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[c][i] = i < m ? (x[c][i] - mean) * rstd : 0.f;
-        dw[c][i] += g[c][i] * x[c][i];
-        db[c][i] += g[c][i];
-        g[c][i] *= w[c][i];
-        t[0] += g[c][i];
-        t[1] += g[c][i] * x[c][i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      x[i] = in && i < n ? (cx.at(i) - mu) * rs : 0.f;
+      g[i] = cg.at(i);
+      dw[i] += g[i] * x[i];
+      db[i] += g[i];
+      g[i] *= w[i];
+      t[0] += g[i];
+      t[1] += g[i] * x[i];
     }
     if (!a.dx) continue;  // uniform
     row_sum<TPR>(t, red[turn][sub]);
     const float m1 = a.layer ? t[0] * per : 0.f, m2 = t[1] * per;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
+    for (int i = 0; i < 8; ++i) g[i] = rs * (g[i] - m1 - x[i] * m2);
+    if (a.ds) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[c][i] += rstd * (g[c][i] - m1 - x[c][i] * m2);
-      store8(static_cast<T*>(a.dx) + row * a.cols + (c * TPR + l) * 8, in ? n[c] : 0, d[c]);
+      for (int i = 0; i < 8; ++i) g[i] += cd.at(i);
     }
+    store8(static_cast<T*>(a.dx) + row * a.cols + col, in ? n : 0, g);
   }
   if (!a.part) return;
   // The workgroup's rows of threads are added in order.
-  auto leave = [&](float (&v)[CH][8], int which) {
+  auto leave = [&](const float (&v)[8], int which) {
     float* to = a.part + ((int64_t)blockIdx.x * 2 + which) * a.cols;
     if constexpr (RPB == 1) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) store8(to + (c * TPR + l) * 8, n[c], v[c]);
+      store8(to + col, n, v);
     } else {
       __syncthreads();
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sums[sub * TPR * CH * 8 + (c * TPR + l) * 8 + i] = v[c][i];
+      for (int i = 0; i < 8; ++i) sums[sub * TPR * 8 + col + i] = v[i];
       __syncthreads();
-      for (int col = threadIdx.x; col < a.cols; col += NT) {
+      for (int c = threadIdx.x; c < a.cols; c += NT) {
         float t = 0.f;
-        for (int q = 0; q < RPB; ++q) t += sums[q * TPR * CH * 8 + col];
-        to[col] = t;
+        for (int q = 0; q < RPB; ++q) t += sums[q * TPR * 8 + c];
+        to[c] = t;
       }
     }
   };
@@ -190,7 +215,6 @@ __global__ __launch_bounds__(kThreads(TPR)) void k_norm_grad(NormGradArgs a) {
 }
 
 // Rows longer than the registers of a workgroup hold: read three times.
-// (A gradient's row takes more registers: 1024 threads would not hold 16 of its columns each.)
 constexpr int kWide = 1024, kWideCols = 16384, kWideGradCols = 8192;
 
 template <typename T>
@@ -335,33 +359,32 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormGradArgs a, int parts) {
   static_cast<T*>(which ? a.db : a.dw)[col] = cvt_x<T>(t);
 }
 
-// Threads of a row: enough for eight columns each up to 512, then 16 each.
-int threads_of_row(int64_t cols) {
+// The fewest threads, a power of two from 8 on, that hold a row with `each` columns a thread.
+int threads_of_row(int64_t cols, int each) {
   int t = 8;
-  while (t < 64 && (int64_t)t * 8 < cols) t *= 2;
-  while (t * 16 < cols) t *= 2;
+  while ((int64_t)t * each < cols) t *= 2;
   return t;
 }
-template <int MOST, typename F>
-void by_width(int64_t cols, F&& f) {
-  switch (threads_of_row(cols)) {
-    case 8: return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-    case 16: return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    case 32: return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-    case 64:
-      if (cols <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-      return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-    case 128: return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{});
-    case 256: return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-    case 512: return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
-    default:
-      if constexpr (MOST > 8192) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+template <typename F>
+void by_threads(int threads, F&& f) {
+  switch (threads) {
+    case 8: return f(std::integral_constant<int, 8>{});
+    case 16: return f(std::integral_constant<int, 16>{});
+    case 32: return f(std::integral_constant<int, 32>{});
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 256: return f(std::integral_constant<int, 256>{});
+    case 512: return f(std::integral_constant<int, 512>{});
+    default: return f(std::integral_constant<int, 1024>{});
   }
 }
-int64_t row_groups(int64_t rows, int64_t cols) {
-  const int t = threads_of_row(cols), per = kThreads(t) / t;
+// Workgroups that have a row each (or as many rows as they have sets of threads).
+int64_t row_groups(int64_t rows, int threads) {
+  const int per = kThreads(threads) / threads;
   return (rows + per - 1) / per;
 }
+// Columns a thread of the forward pass: eight up to 512 columns, then 16.
+int forward_columns(int64_t cols) { return cols <= 512 ? 8 : 16; }
 
 template <typename T>
 hipError_t forward(const NormArgs& a, hipStream_t s) {
@@ -369,10 +392,17 @@ hipError_t forward(const NormArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_norm_wide<T>), dim3((unsigned)a.rows), dim3(kWide), 0, s, a);
     return hipGetLastError();
   }
-  const unsigned grid = (unsigned)std::min<int64_t>(row_groups(a.rows, a.cols), 2048);
-  by_width<kWideCols>(a.cols, [&](auto tpr, auto ch) {
-    constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
-    hipLaunchKernelGGL((k_norm<T, TPR, CH>), dim3(grid), dim3(kThreads(TPR)), 0, s, a);
+  const int each = forward_columns(a.cols), threads = threads_of_row(a.cols, each);
+  const unsigned grid = (unsigned)std::min<int64_t>(row_groups(a.rows, threads), 2048);
+  by_threads(threads, [&](auto tpr) {
+    constexpr int TPR = decltype(tpr)::value;
+    const dim3 block(kThreads(TPR));
+    if constexpr (TPR <= 64) {
+      if (each == 8) hipLaunchKernelGGL((k_norm<T, TPR, 1>), dim3(grid), block, 0, s, a);
+    }
+    if constexpr (TPR >= 64) {
+      if (each == 16) hipLaunchKernelGGL((k_norm<T, TPR, 2>), dim3(grid), block, 0, s, a);
+    }
   });
   return hipGetLastError();
 }
@@ -388,9 +418,9 @@ hipError_t backward(const NormGradArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((k_norm_cols<T>), dim3((unsigned)((a.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s, a,
                          (a.rows + parts - 1) / parts);
   } else if (a.rows > 0) {
-    by_width<kWideGradCols>(a.cols, [&](auto tpr, auto ch) {
-      constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
-      hipLaunchKernelGGL((k_norm_grad<T, TPR, CH>), dim3((unsigned)parts), dim3(kThreads(TPR)), 0, s, a);
+    by_threads(threads_of_row(a.cols, 8), [&](auto tpr) {
+      constexpr int TPR = decltype(tpr)::value;
+      hipLaunchKernelGGL((k_norm_grad<T, TPR>), dim3((unsigned)parts), dim3(kThreads(TPR)), 0, s, a);
     });
   }
   if ((e = hipGetLastError()) != hipSuccess || !(a.dw || a.db)) return e;
@@ -403,7 +433,8 @@ hipError_t backward(const NormGradArgs& a, hipStream_t s) {
 
 int64_t norm_parts(int64_t rows, int64_t cols) {
   if (cols > kWideGradCols) return std::min<int64_t>((rows + 15) / 16, 64);
-  return std::min<int64_t>(row_groups(rows, cols), 512);
+  const int threads = threads_of_row(cols, 8);
+  return std::min<int64_t>(row_groups(rows, threads), 256 * 1024 / kThreads(threads));
 }
 
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s) {
