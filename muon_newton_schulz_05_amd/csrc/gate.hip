@@ -20,6 +20,7 @@
 #include "act.h"
 #include "gate.h"
 #include "group.h"
+#include "raw.h"
 
 namespace muon {
 namespace {
@@ -51,14 +52,19 @@ struct Row {
     l = threadIdx.x & (L - 1);
     n = min(max(experts - l * V, 0), V);
   }
+  // The lane's logits as they lie in memory, and as values: -inf where there is no expert, or no token.
+  __device__ __forceinline__ void fetch(const T* row, bool in, Raw<T> (&raw)[V / 8]) const {
+#pragma unroll
+    for (int c = 0; c < V; c += 8) raw[c / 8].load(row + l * V + c, in ? min(n - c, 8) : 0);
+  }
+  __device__ __forceinline__ void values(const Raw<T> (&raw)[V / 8], bool in, float (&z)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = in && i < n ? raw[i / 8].at(i % 8) : -kInf;
+  }
   __device__ __forceinline__ void load(const T* row, bool in, float (&z)[V]) const {
-#pragma unroll
-    for (int c = 0; c < V; c += 8) {
-      float v[8];
-      load8(row + l * V + c, in ? min(n - c, 8) : 0, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[c + i] = in && c + i < n ? v[i] : -kInf;
-    }
+    Raw<T> raw[V / 8];
+    fetch(row, in, raw);
+    values(raw, in, z);
   }
   __device__ __forceinline__ void store(T* row, bool in, const float (&z)[V]) const {
 #pragma unroll
@@ -69,19 +75,21 @@ struct Row {
       store8(row + l * V + c, in ? min(n - c, 8) : 0, v);
     }
   }
-  // z to probabilities; all zero where every logit is -inf.
+  // z to probabilities; all zero where every logit is -inf.  (The largest value leaves NaN out, which comes back in
+  // through its own exponential and the sum.)
   __device__ __forceinline__ void softmax(float (&z)[V]) const {
-    float m = -kInf, sum = 0.f;
+    float m = z[0], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = z[i] > m || z[i] != z[i] ? z[i] : m;
+    for (int i = 1; i < V; ++i) m = fmaxf(m, z[i]);
     m = group_max<L>(m);
+    m = m == -kInf ? 0.f : m;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      z[i] = m == -kInf ? 0.f : exp_f(z[i] - m);
+      z[i] = exp_f(z[i] - m);
       sum += z[i];
     }
     sum = group_sum<L>(sum);
-    const float inv = m == -kInf ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int i = 0; i < V; ++i) z[i] *= inv;
   }
@@ -211,7 +219,7 @@ __device__ void finish_balance(const BalanceArgs& a, int n, double* sums, int* c
   const int per = (n + parts - 1) / parts, b0 = min(n, part * per), b1 = part < parts ? min(n, b0 + per) : b0;
   double p = 0.0;
   int c = 0;
-#pragma unroll 8
+#pragma unroll 32
   for (int b = b0; b < b1; ++b) {
     p += (double)a.part[(int64_t)b * a.experts + e];
     c += a.part_counts[(int64_t)b * (a.experts + 1) + e];
@@ -269,11 +277,22 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a, int64_t stretch
   const int64_t t0 = blockIdx.x * stretch, t1 = min(a.tokens, t0 + stretch);
   float p[V] = {};
   int seen = 0;
+  // The next token's logits are in flight while this one's are worked on; those of a masked one are read and not used.
+  Raw<T> next[V / 8];
+  bool next_on = false;
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    next_on = t < t1 && (!a.mask || a.mask[t]);
+    r.fetch(static_cast<const T*>(a.logits) + t * a.ldz, t < t1, next);
+  };
+  fetch(t0 + tid / L);
   for (int64_t base = t0; base < t1; base += 1024 / L) {
-    const int64_t t = base + tid / L;
-    const bool on = t < t1 && (!a.mask || a.mask[t]);
     float z[V];
-    r.load(static_cast<const T*>(a.logits) + t * a.ldz, on, z);
+    const bool on = next_on;
+    Raw<T> now[V / 8];
+#pragma unroll
+    for (int c = 0; c < V / 8; ++c) now[c] = next[c];
+    fetch(base + 1024 / L + tid / L);
+    r.values(now, on, z);
     r.softmax(z);
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] += z[i];
@@ -308,11 +327,23 @@ __global__ __launch_bounds__(256) void k_balance_grad(BalanceArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) f[i] = i < r.n ? a.shares[r.l * V + i] : 0.f;
   const float scale = *a.dloss * a.shares[a.experts];
-  for (int64_t base = (int64_t)blockIdx.x * (256 / L); base < a.tokens; base += (int64_t)gridDim.x * (256 / L)) {
+  const int64_t step = (int64_t)gridDim.x * (256 / L);
+  Raw<T> next[V / 8];
+  bool next_on = false;
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    next_on = t < a.tokens && (!a.mask || a.mask[t]);
+    r.fetch(static_cast<const T*>(a.logits) + t * a.ldz, t < a.tokens, next);
+  };
+  fetch((int64_t)blockIdx.x * (256 / L) + threadIdx.x / L);
+  for (int64_t base = (int64_t)blockIdx.x * (256 / L); base < a.tokens; base += step) {
     const int64_t t = base + threadIdx.x / L;
-    const bool in = t < a.tokens, on = in && (!a.mask || a.mask[t]);
+    const bool in = t < a.tokens, on = next_on;
     float z[V], mean = 0.f;
-    r.load(static_cast<const T*>(a.logits) + t * a.ldz, on, z);
+    Raw<T> now[V / 8];
+#pragma unroll
+    for (int c = 0; c < V / 8; ++c) now[c] = next[c];
+    fetch(t + step);
+    r.values(now, on, z);
     r.softmax(z);
 #pragma unroll
     for (int i = 0; i < V; ++i) mean += z[i] * f[i];

@@ -34,15 +34,11 @@ __device__ __forceinline__ float group_sum(float v) {
   if constexpr ((1 << S) < L) return group_sum<L, S + 1>(v + partner<S>(v));
   else return v;
 }
-// The largest value; NaN where there is one.
+// The largest value, NaN left out.
 template <int L, int S = 0>
 __device__ __forceinline__ float group_max(float v) {
-  if constexpr ((1 << S) < L) {
-    const float o = partner<S>(v);
-    return group_max<L, S + 1>(o > v || o != o ? o : v);
-  } else {
-    return v;
-  }
+  if constexpr ((1 << S) < L) return group_max<L, S + 1>(fmaxf(v, partner<S>(v)));
+  else return v;
 }
 
 }  // namespace muon

@@ -19,40 +19,50 @@ __device__ __forceinline__ int64_t value_place(int64_t rows, int64_t r, int64_t 
   return ((piece >> 4) * rows + r) * kMxSliceBytes + 4 * (piece & 15);
 }
 
-// A workgroup takes four rows by a chunk of 512 values, a wave one of its slices and a lane eight values of one row: loads
-// are 256 bytes of a row, stores 256 bytes of a slice, and four lanes share a block.
+// A workgroup takes U sets of four rows by a chunk of 512 values, a wave one of its slices and a lane eight values of one
+// row of each set: loads are 256 bytes of a row, stores 256 bytes of a slice, and four lanes share a block.
 struct Piece8 {
-  int64_t row, chunk;
-  int piece;  // of the chunk
-  __device__ __forceinline__ Piece8(int64_t chunks) {
-    const int64_t b = blockIdx.x, four = b / chunks;
-    chunk = b - four * chunks;
-    row = four * 4 + ((threadIdx.x >> 4) & 3);
+  int64_t row, chunk;  // row of the first set; the next one's is four further
+  int piece;           // of the chunk
+  __device__ __forceinline__ Piece8(int64_t chunks, int sets) {
+    const int64_t b = blockIdx.x, r = b / chunks;
+    chunk = b - r * chunks;
+    row = r * 4 * sets + ((threadIdx.x >> 4) & 3);
     piece = (threadIdx.x >> 6) * 16 + (threadIdx.x & 15);
   }
 };
 
-template <typename T>
+template <typename T, int U>
 __global__ __launch_bounds__(256) void k_quantize_rows(MxArgs a) {
-  const int64_t chunks = mx_chunks(a.k);
-  const Piece8 p(chunks);
-  // The rows of all groups, one behind the other.
-  if (p.row >= a.rows * a.groups) return;
-  const int64_t e = a.groups > 1 ? p.row / a.rows : 0, r = p.row - e * a.rows;
-  float v[8];
+  const int64_t chunks = mx_chunks(a.k), slices = mx_slices(a.k), all = a.rows * a.groups;
+  const Piece8 p(chunks, U);
   const int64_t at = p.chunk * 64 + p.piece, col = at * 8;
-  load8(static_cast<const T*>(a.src) + e * a.step + r * a.ld + col, (int)max((int64_t)0, min((int64_t)8, a.k - col)), v);
-  uint32_t m = 0;
+  const int n = (int)max((int64_t)0, min((int64_t)8, a.k - col));
+  int64_t e[U], r[U];
+  float v[U][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, magnitude(v[i]));
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));  // lanes i and i ^ 1
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));  // and i ^ 2
-  const int scale = scale_of(m);
-  if ((at >> 4) < mx_slices(a.k))
-    *reinterpret_cast<uint32_t*>(a.values + e * mx_slices(a.k) * a.rows * kMxSliceBytes + value_place(a.rows, r, at)) =
-        pack8(v, scale);
-  if ((p.piece & 3) == 0)
-    a.scales[e * chunks * a.rows * kMxChunkBytes + scale_place(a.rows, r, at >> 2)] = (uint8_t)scale;
+  for (int u = 0; u < U; ++u) {
+    // The rows of all groups, one behind the other.
+    const int64_t row = p.row + 4 * u;
+    e[u] = a.groups > 1 ? row / a.rows : 0;
+    r[u] = row - e[u] * a.rows;
+    load8(static_cast<const T*>(a.src) + e[u] * a.step + r[u] * a.ld + col, row < all ? n : 0, v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (p.row + 4 * u >= all) return;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, magnitude(v[u][i]));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));  // lanes i and i ^ 1
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));  // and i ^ 2
+    const int scale = scale_of(m);
+    if ((at >> 4) < slices)
+      *reinterpret_cast<uint32_t*>(a.values + e[u] * slices * a.rows * kMxSliceBytes + value_place(a.rows, r[u], at)) =
+          pack8(v[u], scale);
+    if ((p.piece & 3) == 0)
+      a.scales[e[u] * chunks * a.rows * kMxChunkBytes + scale_place(a.rows, r[u], at >> 2)] = (uint8_t)scale;
+  }
 }
 
 // Rows that lie across memory (a weight [K, N]): a lane takes 16 bytes of 32 lines, one block of each of its C rows; the
@@ -116,7 +126,7 @@ __global__ __launch_bounds__(256) void k_quantize_cols(MxArgs a, int tiles) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_dequantize(MxArgs a) {
   const int64_t chunks = mx_chunks(a.k);
-  const Piece8 p(chunks);
+  const Piece8 p(chunks, 1);
   const int64_t at = p.chunk * 64 + p.piece, col = at * 8;
   if (p.row >= a.rows * a.groups || col >= a.k) return;
   const int64_t e = a.groups > 1 ? p.row / a.rows : 0, r = p.row - e * a.rows;
@@ -157,7 +167,9 @@ hipError_t quantize(const MxArgs& a, hipStream_t s) {
     unsigned blocks = 0;
     const hipError_t e = row_blocks(a, &blocks);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_quantize_rows<T>), dim3(blocks), dim3(256), 0, s, a);
+    // Four sets a workgroup where there are plenty.
+    if (blocks < 8192) hipLaunchKernelGGL((k_quantize_rows<T, 1>), dim3(blocks), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_quantize_rows<T, 4>), dim3((unsigned)((a.rows * a.groups + 15) / 16 * mx_chunks(a.k))), dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
