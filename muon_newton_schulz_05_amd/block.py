@@ -16,11 +16,13 @@ autograd, for code that captures them into a HIP graph.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
-from .ops import _call, _check, _dtype, _flat, _gpu, _ld, _ptr, _rows, _same, _tracked, load_ops
+from .ops import _dtype, _gpu, _same, _traced, _tracked, load_ops
 
 GATE_MAX_EXPERTS = 1024
 NORMS = {"layer": 0, "rms": 1}
@@ -80,23 +82,31 @@ def load_block():
     return lib
 
 
-_plans = {}
+_module = None
 
 
-def _plan(desc_type, size_call, *args):
-    """(descriptor, workspace bytes) of a call, by what its descriptor holds."""
-    key = (desc_type, size_call, args)
-    got = _plans.get(key)
-    if got is None:
-        lib = load_block()
-        d = desc_type(*args)
-        need = ctypes.c_uint64(0)
-        if size_call:
-            _check(getattr(lib, size_call)(ctypes.byref(d), ctypes.byref(need)), size_call)
-        if len(_plans) >= 4096:
-            _plans.clear()
-        got = _plans[key] = (ctypes.byref(d), need.value)
-    return got
+def _nodes(what):
+    """The module that allocates, launches and ties the calls to autograd (csrc/block_nodes.cpp); raises if it is not
+    built, or while a tracer records, which would see the outputs' allocation alone."""
+    global _module
+    if _traced():
+        raise RuntimeError(f"{what} cannot be traced: a tracer would record its outputs' allocation alone")
+    if _module is None:
+        load_block()
+        try:
+            from . import _nodes as module
+        except ImportError as e:
+            raise RuntimeError("_nodes.so is not built: run `python -m muon_newton_schulz_05_amd.build`") from e
+        _module = module
+    return _module
+
+
+def _refuse_tangents(what, **tensors):
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    for name, t in tensors.items():
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{what} has no forward-mode derivative, and {name} carries a tangent")
 
 
 # ------------------------------------------------------------------ norms
@@ -117,39 +127,10 @@ def _check_norm(x, weight, bias, residual):
         raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
 
 
-def _whole(t):
-    return t if t is None or t.is_contiguous() else t.contiguous()
-
-
-def _norm_forward(x, weight, bias, residual, eps, kind, keep):
-    """y, s, stats and the rows that the gradient reads, of checked arguments."""
-    cols = x.shape[-1]
-    x2, r2 = _flat(x, cols), _flat(residual, cols)
-    w, b = _whole(weight), _whole(bias)
-    rows = x2.shape[0]
-    d, _ = _plan(NormDesc, None, _dtype(x, "x"), kind, rows, cols, _ld(x2), 0 if r2 is None else _ld(r2), 0, eps)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    s = None if r2 is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    stats = torch.empty((rows, 2), dtype=torch.float32, device=x.device) if keep else None
-    _call("muon_norm_forward", x, d, x2.data_ptr(), _ptr(r2), _ptr(w), _ptr(b), y.data_ptr(), _ptr(s), _ptr(stats))
-    return y, s, stats, x2 if s is None else s.view(rows, cols), w
-
-
-def _norm_backward(dy, s, weight, stats, ds, kind, need_x, need_w, need_b):
-    rows, cols = s.shape
-    dtype, dev = s.dtype, s.device
-    g, d2 = _flat(dy, cols), _flat(ds, cols)
-    d, size = _plan(NormDesc, "muon_norm_workspace", _dtype(s, "s"), kind, rows, cols, _ld(s),
-                    0 if d2 is None else _ld(d2), _ld(g), 0.0)
-    dx = torch.empty((rows, cols), dtype=dtype, device=dev) if need_x else None
-    dw = torch.empty((cols,), dtype=dtype, device=dev) if need_w else None
-    db = torch.empty((cols,), dtype=dtype, device=dev) if need_b else None
-    if not (need_w or need_b):
-        size = 0
-    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    _call("muon_norm_backward", s, d, g.data_ptr(), s.data_ptr(), _ptr(weight), stats.data_ptr(), _ptr(d2), _ptr(dx),
-          _ptr(dw), _ptr(db), _ptr(ws), size)
-    return dx, dw, db
+def _eps(eps):
+    if not 0.0 <= eps < 1e30:
+        raise ValueError(f"eps is {eps}: at least 0, and finite")
+    return eps
 
 
 def _norm_kind(kind):
@@ -165,7 +146,7 @@ def norm_forward(x, weight=None, bias=None, *, eps=1e-5, residual=None, kind="la
     1 / sqrt(var + eps) for ``norm_backward``."""
     code = _norm_kind(kind)
     _check_norm(x, weight, bias, residual)
-    y, s, stats, *_ = _norm_forward(x, weight, bias, residual, eps, code, True)
+    y, s, stats = _nodes("norm_forward").norm_forward(x, weight, bias, residual, _eps(eps), code)
     return y, x if s is None else s, stats
 
 
@@ -178,42 +159,18 @@ def norm_backward(dy, s, weight, stats, *, kind="layer", ds=None, needs=(True, T
     _same(s, ds=ds)
     if ds is not None and ds.shape != s.shape:
         raise ValueError(f"ds has shape {tuple(ds.shape)}, s {tuple(s.shape)}")
-    s2 = _flat(s, s.shape[-1])
-    if stats.dtype is not torch.float32 or stats.shape != (s2.shape[0], 2) or stats.device != s.device \
+    rows = math.prod(s.shape[:-1])
+    if stats.dtype is not torch.float32 or stats.shape != (rows, 2) or stats.device != s.device \
             or not stats.is_contiguous():
         raise ValueError("stats must be what norm_forward returned")
-    dx, dw, db = _norm_backward(dy, s2, _whole(weight), stats, ds, code, *needs)
-    return None if dx is None else dx.view(s.shape), dw, db
-
-
-class _Norm(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, bias, residual, eps, kind):
-        y, s, stats, rows, w = _norm_forward(x, weight, bias, residual, eps, kind, True)
-        ctx.save_for_backward(rows, w, stats)
-        ctx.kind, ctx.x_shape = kind, x.shape
-        ctx.set_materialize_grads(False)
-        return y if s is None else (y, s)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy, ds=None):
-        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
-        if dy is None:  # only s was used
-            return ds if need_x else None, None, None, ds if need_r else None, None, None
-        rows, w, stats = ctx.saved_tensors
-        dx, dw, db = _norm_backward(dy, rows, w, stats, ds, ctx.kind, need_x or need_r, need_w, need_b)
-        if dx is not None:
-            dx = dx.view(ctx.x_shape)
-        return dx if need_x else None, dw, db, dx if need_r else None, None, None
+    return tuple(_nodes("norm_backward").norm_backward(dy, s, weight, stats, ds, code, *needs))
 
 
 def _norm(x, weight, bias, residual, eps, kind):
     _check_norm(x, weight, bias, residual)
-    if not _tracked(x, weight, bias, residual):
-        y, s, *_ = _norm_forward(x, weight, bias, residual, eps, kind, False)
-        return y if s is None else (y, s)
-    return _Norm.apply(x, weight, bias, residual, eps, kind)
+    _refuse_tangents("a norm", x=x, weight=weight, bias=bias, residual=residual)
+    out = _nodes("a norm").norm(x, weight, bias, residual, _eps(eps), kind, _tracked(x, weight, bias, residual))
+    return out[0] if residual is None else (out[0], out[1])
 
 
 def layer_norm(x, weight=None, bias=None, *, eps=1e-5, residual=None):
@@ -254,29 +211,6 @@ def _check_logits(logits, mask):
             raise ValueError(f"mask is on {mask.device}, logits on {logits.device}")
 
 
-def _gate_plan(logits, top, normalize):
-    return _plan(GateDesc, None, _dtype(logits, "logits"), logits.shape[1], top, normalize, logits.shape[0],
-                 _ld(logits))[0]
-
-
-def _gate_forward(logits, top, normalize, mask):
-    z, m = _rows(logits), _whole(mask)
-    shape = (z.shape[0], top)
-    weights = torch.empty(shape, dtype=torch.float32, device=z.device)
-    ids = torch.empty(shape, dtype=torch.int32, device=z.device)
-    _call("muon_gate_forward", z, _gate_plan(z, top, normalize), z.data_ptr(), _ptr(m), weights.data_ptr(),
-          ids.data_ptr())
-    return weights, ids, z, m
-
-
-def _gate_backward(dweights, z, weights, ids, normalize, mask):
-    dw = _whole(dweights)
-    dz = torch.empty(z.shape, dtype=z.dtype, device=z.device)
-    _call("muon_gate_backward", z, _gate_plan(z, ids.shape[1], normalize), z.data_ptr(), _ptr(mask),
-          weights.data_ptr(), ids.data_ptr(), dw.data_ptr(), dz.data_ptr())
-    return dz
-
-
 def _check_gate(logits, top, mask):
     _check_logits(logits, mask)
     if not 1 <= top <= logits.shape[1]:
@@ -286,7 +220,7 @@ def _check_gate(logits, top, mask):
 def gate_forward(logits, top, *, normalize=True, mask=None):
     """``gate`` without autograd."""
     _check_gate(logits, top, mask)
-    return Gating(*_gate_forward(logits, top, int(bool(normalize)), mask)[:2])
+    return Gating(*_nodes("gate_forward").gate(logits, top, int(bool(normalize)), mask, False))
 
 
 def gate_backward(dweights, logits, gating, *, normalize=True, mask=None):
@@ -303,23 +237,7 @@ def gate_backward(dweights, logits, gating, *, normalize=True, mask=None):
     for t, name in ((weights, "weights"), (ids, "ids"), (dweights, "dweights")):
         if t.device != logits.device:
             raise ValueError(f"{name} is on {t.device}, logits on {logits.device}")
-    return _gate_backward(dweights, _rows(logits), weights, ids, int(bool(normalize)), _whole(mask))
-
-
-class _Gate(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, top, normalize, mask):
-        weights, ids, z, m = _gate_forward(logits, top, normalize, mask)
-        ctx.save_for_backward(z, weights, ids, m)
-        ctx.normalize = normalize
-        ctx.mark_non_differentiable(ids)
-        return weights, ids
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dweights, _):
-        z, weights, ids, m = ctx.saved_tensors
-        return _gate_backward(dweights, z, weights, ids, ctx.normalize, m), None, None, None
+    return _nodes("gate_backward").gate_backward(dweights, logits, weights, ids, int(bool(normalize)), mask)
 
 
 def gate(logits, top, *, normalize=True, mask=None):
@@ -332,10 +250,8 @@ def gate(logits, top, *, normalize=True, mask=None):
     expert whose logit is -inf is never chosen: -1 and 0 stand where too few are left.
     ``route(ids, E)`` and ``combine(..., weights)`` take these as they are.  Differentiable in logits."""
     _check_gate(logits, top, mask)
-    code = int(bool(normalize))
-    if not _tracked(logits):
-        return Gating(*_gate_forward(logits, top, code, mask)[:2])
-    return Gating(*_Gate.apply(logits, top, code, mask))
+    _refuse_tangents("gate", logits=logits)
+    return Gating(*_nodes("gate").gate(logits, top, int(bool(normalize)), mask, _tracked(logits)))
 
 
 # ------------------------------------------------------------------ balance loss
@@ -357,34 +273,10 @@ def _check_balance(logits, ids, mask):
         raise ValueError(f"expert_ids is on {ids.device}, logits on {logits.device}")
 
 
-def _balance_plan(z, top):
-    return _plan(GateDesc, "muon_balance_workspace", _dtype(z, "logits"), z.shape[1], top, 0, z.shape[0], _ld(z))
-
-
-def _balance_forward(logits, ids, mask):
-    z, i, m = _rows(logits), _whole(ids), _whole(mask)
-    e, dev = z.shape[1], z.device
-    d, size = _balance_plan(z, i.shape[1])
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    counts = torch.empty((e,), dtype=torch.int32, device=dev)
-    shares = torch.empty((e + 1,), dtype=torch.float32, device=dev)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    _call("muon_balance_forward", z, d, z.data_ptr(), i.data_ptr(), i.element_size(), _ptr(m), loss.data_ptr(),
-          counts.data_ptr(), shares.data_ptr(), _ptr(ws), size)
-    return loss, counts, shares, z, m
-
-
-def _balance_backward(dloss, z, top, shares, mask):
-    dz = torch.empty(z.shape, dtype=z.dtype, device=z.device)
-    _call("muon_balance_backward", z, _balance_plan(z, top)[0], z.data_ptr(), _ptr(mask), shares.data_ptr(),
-          dloss.data_ptr(), dz.data_ptr())
-    return dz
-
-
 def balance_forward(logits, expert_ids, *, mask=None):
     """``balance_loss`` without autograd: (loss, counts, shares); shares is for ``balance_backward``."""
     _check_balance(logits, expert_ids, mask)
-    return _balance_forward(logits, expert_ids, mask)[:3]
+    return _nodes("balance_forward").balance_forward(logits, expert_ids, mask)
 
 
 def balance_backward(dloss, logits, expert_ids, shares, *, mask=None):
@@ -395,23 +287,7 @@ def balance_backward(dloss, logits, expert_ids, shares, *, mask=None):
     if shares.dtype is not torch.float32 or shares.shape != (logits.shape[1] + 1,) or not shares.is_contiguous() \
             or shares.device != logits.device:
         raise ValueError("shares must be what balance_forward returned")
-    return _balance_backward(dloss, _rows(logits), expert_ids.shape[1], shares, _whole(mask))
-
-
-class _BalanceLoss(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, ids, mask):
-        loss, counts, shares, z, m = _balance_forward(logits, ids, mask)
-        ctx.save_for_backward(z, shares, m)
-        ctx.top = ids.shape[1]
-        ctx.mark_non_differentiable(counts)
-        return loss, counts
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dloss, _):
-        z, shares, m = ctx.saved_tensors
-        return _balance_backward(dloss, z, ctx.top, shares, m), None, None
+    return _nodes("balance_backward").balance_backward(dloss, logits, expert_ids.shape[1], shares, mask)
 
 
 def balance_loss(logits, expert_ids, *, mask: Optional[torch.Tensor] = None):
@@ -422,6 +298,5 @@ def balance_loss(logits, expert_ids, *, mask: Optional[torch.Tensor] = None):
     out count nowhere.  An id outside [0, E) (a dropped entry's -1) is not counted, but its place is: f_e is c_e / (T
     top).  Differentiable in logits, through P."""
     _check_balance(logits, expert_ids, mask)
-    if not _tracked(logits):
-        return Balance(*_balance_forward(logits, expert_ids, mask)[:2])
-    return Balance(*_BalanceLoss.apply(logits, expert_ids, mask))
+    _refuse_tangents("balance_loss", logits=logits)
+    return Balance(*_nodes("balance_loss").balance(logits, expert_ids, mask, _tracked(logits)))

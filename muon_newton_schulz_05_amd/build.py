@@ -1,4 +1,4 @@
-"""Build libmuon.so in-tree with hipcc for gfx950.
+"""Build libmuon.so in-tree with hipcc for gfx950, and _nodes.so, which binds part of it to torch.
 
     python -m muon_newton_schulz_05_amd.build            # compile (always)
 """
@@ -15,11 +15,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmuon.so")
+NODES = os.path.join(PKG, "_nodes.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["api.cpp", "planner.cpp", "skinny.hip", "stream.hip", "stream_big.hip", "noalloc.hip",
            "ops_api.cpp", "linear_bf16.hip", "linear_f32.hip", "route.hip", "dropout.hip",
            "block_api.cpp", "norm.hip", "gate.hip", "mx.hip", "linear_mx.hip"]
 
+NODES_SOURCE = "block_nodes.cpp"
+
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # Packed float32 instructions are switched off for the device code.
@@ -28,13 +32,25 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", os.path.
           "-Wno-unused-command-line-argument"]
 
 
-def _compile(src: str) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    lang = ["-x", "hip"] if src.endswith(".hip") else []
-    cmd = [HIPCC, *COMMON, *DEVICE_FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+def _run(what: str, cmd: list[str]) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{what} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+
+def _compile(src: str) -> str:
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+    if src == NODES_SOURCE:
+        import sysconfig
+
+        from torch.utils import cpp_extension
+        include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include"]
+        flags = ["-O2", "-std=c++17", "-fPIC", "-w", "-D__HIP_PLATFORM_AMD__", "-DTORCH_EXTENSION_NAME=_nodes",
+                 "-DUSE_ROCM", *[f"-I{d}" for d in include]]
+        _run("compile", [CXX, *flags, "-c", os.path.join(CSRC, src), "-o", obj])
+        return obj
+    lang = ["-x", "hip"] if src.endswith(".hip") else []
+    _run("compile", [HIPCC, *COMMON, *DEVICE_FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj])
     return obj
 
 
@@ -42,16 +58,19 @@ def build(verbose: bool = False) -> str:
     if not os.path.exists(HIPCC) and shutil.which("hipcc") is None:
         raise RuntimeError("hipcc not found")
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
-        objs = list(ex.map(_compile, SOURCES))
+    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
+        nodes, *objs = ex.map(_compile, [NODES_SOURCE, *SOURCES])
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    _run("link", [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    from torch.utils import cpp_extension
+    libs = [f"-L{d}" for d in cpp_extension.library_paths()]
+    tmp = NODES + ".tmp"
+    _run("link", [CXX, "-shared", "-o", tmp, nodes, *libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
+                  f"-L{PKG}", "-l:libmuon.so", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, NODES)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {NODES}")
     return LIB
 
 

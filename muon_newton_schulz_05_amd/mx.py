@@ -11,10 +11,9 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
-from torch.autograd import forward_ad
 
-from .block import MxDesc, _plan, _whole
-from .ops import _activation, _call, _check_linear, _dtype, _flat, _gpu, _layout_ok, _ld, _ptr
+from .block import _nodes, _refuse_tangents
+from .ops import _activation, _check_linear, _dtype, _gpu
 
 MX_MAX_SIZE = 1 << 23
 
@@ -55,7 +54,7 @@ def mx_quantize(weight):
     to nearest, ties to even, and saturate at 6 scales.  A block with an infinity or NaN becomes NaN.  Takes the weight's
     value: a parameter that requires a gradient may be given."""
     _gpu(weight, "weight")
-    code = _dtype(weight, "weight")
+    _dtype(weight, "weight")
     if weight.dim() not in (2, 3):
         raise ValueError(f"weight has {weight.dim()} dimensions, expected 2 or 3")
     k, n = weight.shape[-2:]
@@ -64,29 +63,15 @@ def mx_quantize(weight):
     groups = weight.shape[0] if weight.dim() == 3 else 0
     if weight.dim() == 3 and not 1 <= groups <= 65535:
         raise ValueError(f"{groups} experts: 1 to 65535 are supported")
-    w = weight.detach()
-    w = w if _layout_ok(w) else w.contiguous()
-    if w.stride(-1) == 1 and (k <= 1 or w.stride(-2) >= n):
-        layout, ld = 0, w.stride(-2) if k > 1 else max(n, 1)
-    else:
-        layout, ld = 1, w.stride(-1) if n > 1 else max(k, 1)
-    d = _plan(MxDesc, None, code, 0, groups, layout, 0, k, n, 0, ld, w.stride(0) if groups else 0, 0)[0]
-    lead = weight.shape[:-2]
-    values = torch.empty((*lead, (k + 127) // 128, n, 64), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((*lead, (k + 511) // 512, n, 16), dtype=torch.uint8, device=w.device)
-    _call("muon_mx_quantize", w, d, w.data_ptr(), values.data_ptr(), scales.data_ptr())
-    return MxWeight(values, scales, k)
+    return MxWeight(*_nodes("mx_quantize").mx_quantize(weight), k)
 
 
 def mx_dequantize(weight, dtype=torch.float32):
     """The values that an ``MxWeight`` stands for, exactly: [K, N] or [E, K, N], contiguous along K."""
     _check_weight(weight)
-    values, scales, k = weight
-    n, lead = values.shape[-2], values.shape[:-3]
-    out = torch.empty((*lead, n, k), dtype=dtype, device=values.device)
-    d = _plan(MxDesc, None, _dtype(out, "dtype"), 0, lead[0] if lead else 0, 0, 0, k, n, 0, n, 0, 0)[0]
-    _call("muon_mx_dequantize", values, d, values.data_ptr(), scales.data_ptr(), out.data_ptr())
-    return out.transpose(-1, -2)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype is {dtype}: float32 or bfloat16 is supported")
+    return _nodes("mx_dequantize").mx_dequantize(*weight, dtype is torch.bfloat16)
 
 
 class _Shape:
@@ -103,25 +88,13 @@ def _linear(x, weight, bias, residual, offsets, activation):
     act = _activation(activation)
     _check_weight(weight)
     _check_linear(x, _Shape(weight, x), bias, residual, offsets)
-    for name, t in (("x", x), ("bias", bias), ("residual", residual)):
-        if t is None:
-            continue
-        if torch.is_grad_enabled() and t.requires_grad:
-            raise RuntimeError(f"layers in four bits have no gradient, and {name} requires one: call them under "
-                               "torch.no_grad()")
-        if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
-            raise RuntimeError(f"layers in four bits have no forward-mode derivative, and {name} carries a tangent")
-    values, scales, k = weight
-    n = values.shape[-2]
-    x2, r2, b = _flat(x, k), _flat(residual, n), _whole(bias)
-    rows = x2.shape[0]
-    d, size = _plan(MxDesc, "muon_mx_linear_workspace", _dtype(x, "x"), act, 0 if offsets is None else values.shape[0], 0,
-                    rows, k, n, _ld(x2), 0, 0, 0 if r2 is None else _ld(r2))
-    y = torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=x.device)
-    ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
-    _call("muon_mx_linear", x, d, _ptr(offsets), x2.data_ptr(), values.data_ptr(), scales.data_ptr(), _ptr(b), _ptr(r2),
-          y.data_ptr(), _ptr(ws), size)
-    return y
+    if torch.is_grad_enabled():
+        for name, t in (("x", x), ("bias", bias), ("residual", residual)):
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"layers in four bits have no gradient, and {name} requires one: call them under "
+                                   "torch.no_grad()")
+    _refuse_tangents("a layer in four bits", x=x, bias=bias, residual=residual)
+    return _nodes("mx_linear").mx_linear(x, *weight, bias, residual, offsets, act)
 
 
 def mx_linear(x, weight, bias=None, *, activation="none", residual=None):
