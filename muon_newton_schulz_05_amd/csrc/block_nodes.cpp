@@ -64,7 +64,8 @@ variable_list once(variable_list grads) {
 // ------------------------------------------------------------------ norms
 
 struct Normed {
-  Tensor y, s, stats, rows, w;  // rows: s as [rows, cols], what the gradient reads
+  Tensor y, s, stats, w;
+  Tensor kept;  // what the gradient reads: s, or x (or its copy, where x has no contiguous rows)
 };
 Normed norm_run(const Tensor& x, const OptTensor& weight, const OptTensor& bias, const OptTensor& residual, double eps,
                 int64_t kind, bool keep) {
@@ -81,17 +82,17 @@ Normed norm_run(const Tensor& x, const OptTensor& weight, const OptTensor& bias,
   check(muon_norm_forward(&d, at_of(x2), at_of(r2), at_of(o.w), at_of(b), out_of(o.y), out_of(o.s),
                           static_cast<float*>(out_of(o.stats)), stream_of(x)),
         "muon_norm_forward");
-  o.rows = residual ? o.s.view({x2.size(0), cols}) : x2;
+  o.kept = residual ? o.s : x2.is_alias_of(x) ? x : x2;
   return o;
 }
-// dx as [rows, cols], dw, db; undefined where not needed.
-variable_list norm_grad(const Tensor& dy, const Tensor& rows, const Tensor& w, const Tensor& stats, const Tensor& ds,
+// dx like s, dw, db; undefined where not needed.
+variable_list norm_grad(const Tensor& dy, const Tensor& s, const Tensor& w, const Tensor& stats, const Tensor& ds,
                         int64_t kind, bool need_x, bool need_w, bool need_b) {
-  const c10::DeviceGuard guard(rows.device());
-  const int64_t cols = rows.size(1);
-  const Tensor g = flat(dy, cols), d2 = ds.defined() ? flat(ds, cols) : Tensor();
+  const c10::DeviceGuard guard(s.device());
+  const int64_t cols = s.size(-1);
+  const Tensor rows = flat(s, cols), g = flat(dy, cols), d2 = ds.defined() ? flat(ds, cols) : Tensor();
   Tensor dx, dw, db;
-  if (need_x) dx = at::empty(rows.sizes(), rows.options());
+  if (need_x) dx = at::empty(s.sizes(), rows.options());
   if (need_w) dw = at::empty({cols}, rows.options());
   if (need_b) db = at::empty({cols}, rows.options());
   const muon_norm_desc_t d{dtype_of(rows), (int32_t)kind, rows.size(0), cols, ld(rows), ds.defined() ? ld(d2) : 0, ld(g), 0.0};
@@ -108,9 +109,10 @@ struct NormNode : public Function<NormNode> {
   static variable_list forward(AutogradContext* ctx, const Tensor& x, const OptTensor& weight, const OptTensor& bias,
                                const OptTensor& residual, double eps, int64_t kind) {
     const Normed o = norm_run(x, weight, bias, residual, eps, kind, true);
-    ctx->save_for_backward({o.rows, o.w, o.stats});
-    if (x.dim() != 2) ctx->saved_data["shape"] = x.sizes().vec();
-    ctx->saved_data["given"] = int64_t((weight ? 1 : 0) | (bias ? 2 : 0) | (residual ? 4 : 0) | (x.dim() != 2 ? 8 : 0)) | kind << 8;
+    ctx->save_for_backward({o.kept, o.w, o.stats});
+    const bool reshaped = o.kept.dim() != x.dim();
+    if (reshaped) ctx->saved_data["shape"] = x.sizes().vec();
+    ctx->saved_data["given"] = int64_t((weight ? 1 : 0) | (bias ? 2 : 0) | (residual ? 4 : 0) | (reshaped ? 8 : 0)) | kind << 8;
     ctx->set_materialize_grads(false);
     if (residual) return {o.y, o.s};
     return {o.y};
@@ -157,8 +159,7 @@ std::tuple<Tensor, OptTensor, Tensor> norm_forward(const Tensor& x, const OptTen
 std::vector<OptTensor> norm_backward(const Tensor& dy, const Tensor& s, const OptTensor& weight, const Tensor& stats,
                                      const OptTensor& ds, int64_t kind, bool need_x, bool need_w, bool need_b) {
   const at::NoGradGuard no_grad;
-  variable_list g = norm_grad(dy, flat(s, s.size(-1)), whole(weight), stats, ds ? *ds : Tensor(), kind, need_x, need_w, need_b);
-  if (need_x) g[0] = g[0].view(s.sizes());
+  const variable_list g = norm_grad(dy, s, whole(weight), stats, ds ? *ds : Tensor(), kind, need_x, need_w, need_b);
   std::vector<OptTensor> out;
   for (const Tensor& t : g) out.push_back(t.defined() ? OptTensor(t) : OptTensor());
   return out;

@@ -107,10 +107,11 @@ __device__ __forceinline__ void group_best(uint32_t& key, int& at) {
   }
 }
 
+// The tokens of one workgroup, from `first` on.
 template <typename T, int L, int V>
-__global__ __launch_bounds__(256) void k_gate(GateArgs a) {
+__device__ __forceinline__ void gate_tokens(const GateArgs& a, int64_t first) {
   const Row<T, L, V> r(a.experts);
-  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int64_t t = first + threadIdx.x / L;
   const bool in = t < a.tokens, on = in && (!a.mask || a.mask[t]);
   float z[V];
   r.load(static_cast<const T*>(a.logits) + t * a.ldz, on, z);
@@ -170,12 +171,18 @@ __global__ __launch_bounds__(256) void k_gate(GateArgs a) {
 }
 
 template <typename T, int L, int V>
-__global__ __launch_bounds__(256) void k_gate_grad(GateArgs a) {
+__global__ __launch_bounds__(256) void k_gate(GateArgs a) {
+  for (int64_t first = (int64_t)blockIdx.x * (256 / L); first < a.tokens; first += (int64_t)gridDim.x * (256 / L))
+    gate_tokens<T, L, V>(a, first);
+}
+
+template <typename T, int L, int V>
+__device__ __forceinline__ void gate_grad_tokens(const GateArgs& a, int64_t first) {
   // The chosen experts' part, laid out by expert: a token's row is its own lanes' alone.
   __shared__ float rows[256 / L][L * V];
   const Row<T, L, V> r(a.experts);
   const int sub = threadIdx.x / L;
-  const int64_t t = (int64_t)blockIdx.x * (256 / L) + sub;
+  const int64_t t = first + sub;
   const bool in = t < a.tokens, on = in && (!a.mask || a.mask[t]);
 #pragma unroll
   for (int i = 0; i < V; ++i) rows[sub][r.l * V + i] = 0.f;
@@ -205,6 +212,13 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) d[i] = rows[sub][r.l * V + i] - d[i] * mean;
   r.store(static_cast<T*>(a.dlogits) + t * a.experts, in, d);
+  wave_fence();
+}
+
+template <typename T, int L, int V>
+__global__ __launch_bounds__(256) void k_gate_grad(GateArgs a) {
+  for (int64_t first = (int64_t)blockIdx.x * (256 / L); first < a.tokens; first += (int64_t)gridDim.x * (256 / L))
+    gate_grad_tokens<T, L, V>(a, first);
 }
 
 __device__ __forceinline__ int expert_at(const BalanceArgs& a, int64_t i) {
@@ -375,7 +389,9 @@ int lanes_of(int experts) {
 
 template <typename T>
 hipError_t gate(const GateArgs& a, bool grad, hipStream_t s) {
-  const unsigned blocks = (unsigned)((a.tokens + 256 / lanes_of(a.experts) - 1) / (256 / lanes_of(a.experts)));
+  // A launch holds fewer than 2^32 threads.
+  const int64_t per = 256 / lanes_of(a.experts);
+  const unsigned blocks = (unsigned)std::min<int64_t>((a.tokens + per - 1) / per, 1 << 22);
   by_experts(a.experts, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
     if (grad) hipLaunchKernelGGL((k_gate_grad<T, L, V>), dim3(blocks), dim3(256), 0, s, a);

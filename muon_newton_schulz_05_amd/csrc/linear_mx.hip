@@ -450,7 +450,6 @@ template <typename O>
 hipError_t launch(const MxProduct& a, int tile, int cols, hipStream_t s) {
   const int64_t blocks = (int64_t)a.g.tiles_m * a.g.tiles_n * a.g.splits;
   if (blocks <= 0) return hipSuccess;
-  if (blocks > 0x7fffff) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), few(64 * kFewWaves);
   switch (tile) {
     case kMx256x128: hipLaunchKernelGGL((k_mx_tile<O, 256, 128, 2, 2, 3>), grid, dim3(256), 0, s, a); break;

@@ -23,6 +23,9 @@ struct MxArgs {
   int64_t rows, k, ld, step;
   int32_t groups, t;
 };
+// Workgroups of the kernels over rows, and whether one launch holds them (2^32 threads).
+inline int64_t mx_row_blocks(int64_t rows, int64_t k) { return (rows + 3) / 4 * mx_chunks(k); }
+inline bool mx_rows_fit(int64_t rows, int64_t k) { return mx_row_blocks(rows, k) < (int64_t(1) << 24); }
 hipError_t launch_mx_quantize(const MxArgs& a, int dtype, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxArgs& a, int dtype, hipStream_t s);
 

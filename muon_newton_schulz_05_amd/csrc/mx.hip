@@ -148,25 +148,14 @@ __global__ __launch_bounds__(256) void k_dequantize(MxArgs a) {
   store8(static_cast<T*>(a.dst) + p.row * a.k + col, (int)min((int64_t)8, a.k - col), v);
 }
 
-// Workgroups over four rows and a chunk each, or an error where a grid does not hold them.
-hipError_t row_blocks(const MxArgs& a, unsigned* blocks) {
-  const int64_t n = (a.rows * a.groups + 3) / 4 * mx_chunks(a.k);
-  if (n >= (int64_t(1) << 24)) return hipErrorInvalidValue;
-  *blocks = (unsigned)n;
-  return hipSuccess;
-}
-
 template <typename T>
 hipError_t quantize(const MxArgs& a, hipStream_t s) {
   if (a.t) {
     constexpr int64_t kRows = 16 * 16 / sizeof(T);  // of a workgroup
     const int64_t tiles = (a.rows + kRows - 1) / kRows, blocks = tiles * mx_chunks(a.k) * a.groups;
-    if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_quantize_cols<T>), dim3((unsigned)blocks), dim3(256), 0, s, a, (int)tiles);
   } else {
-    unsigned blocks = 0;
-    const hipError_t e = row_blocks(a, &blocks);
-    if (e != hipSuccess) return e;
+    const unsigned blocks = (unsigned)mx_row_blocks(a.rows * a.groups, a.k);
     // Four sets a workgroup where there are plenty.
     if (blocks < 8192) hipLaunchKernelGGL((k_quantize_rows<T, 1>), dim3(blocks), dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_quantize_rows<T, 4>), dim3((unsigned)((a.rows * a.groups + 15) / 16 * mx_chunks(a.k))), dim3(256), 0, s, a);
@@ -183,9 +172,7 @@ hipError_t launch_mx_quantize(const MxArgs& a, int dtype, hipStream_t s) {
 
 hipError_t launch_mx_dequantize(const MxArgs& a, int dtype, hipStream_t s) {
   if (a.rows == 0 || a.k == 0 || a.groups == 0) return hipSuccess;
-  unsigned blocks = 0;
-  const hipError_t e = row_blocks(a, &blocks);
-  if (e != hipSuccess) return e;
+  const unsigned blocks = (unsigned)mx_row_blocks(a.rows * a.groups, a.k);
   if (dtype == MUON_BF16) hipLaunchKernelGGL(k_dequantize<uint16_t>, dim3(blocks), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(k_dequantize<float>, dim3(blocks), dim3(256), 0, s, a);
   return hipGetLastError();

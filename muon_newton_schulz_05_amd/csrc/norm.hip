@@ -193,12 +193,13 @@ __global__ __launch_bounds__(kThreads(TPR)) void k_norm_grad(NormGradArgs a) {
 
 // Rows longer than the registers of a workgroup hold: read three times.
 constexpr int kWide = 1024, kWideCols = 16384, kWideGradCols = 8192;
+constexpr int64_t kWideGrid = 1 << 20;  // a launch holds fewer than 2^32 threads
 
 template <typename T>
 __global__ __launch_bounds__(kWide) void k_norm_wide(NormArgs a) {
   __shared__ float red[2][16];
-  const int64_t row = blockIdx.x;
   const float per = 1.f / (float)a.cols;
+  int64_t row = blockIdx.x;
   auto get = [&](int64_t col, float (&v)[8]) {
     const int n = (int)min((int64_t)8, a.cols - col);
     load8(static_cast<const T*>(a.x) + row * a.ldx + col, n, v);
@@ -210,51 +211,54 @@ __global__ __launch_bounds__(kWide) void k_norm_wide(NormArgs a) {
     }
     return n;
   };
-  float v[8], mean = 0.f;
-  if (a.layer) {
+  for (; row < a.rows; row += gridDim.x) {
+    float v[8], mean = 0.f;
+    if (a.layer) {
+      float t[1] = {0.f};
+      for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
+        get(col, v);
+        float u = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u += v[i];
+        t[0] += u;
+      }
+      row_sum<kWide>(t, red[0]);
+      mean = t[0] * per;
+    }
     float t[1] = {0.f};
     for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
-      get(col, v);
+      const int n = get(col, v);
       float u = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u += v[i];
+      for (int i = 0; i < 8; ++i) u += i < n ? (v[i] - mean) * (v[i] - mean) : 0.f;
       t[0] += u;
     }
-    row_sum<kWide>(t, red[0]);
-    mean = t[0] * per;
-  }
-  float t[1] = {0.f};
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
-    const int n = get(col, v);
-    float u = 0.f;
+    row_sum<kWide>(t, red[1]);
+    const float rstd = 1.f / sqrtf(t[0] * per + a.eps);
+    if (a.stats && threadIdx.x == 0) {
+      a.stats[2 * row] = mean;
+      a.stats[2 * row + 1] = rstd;
+    }
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
+      const int n = get(col, v);
+      if (a.res) store8(static_cast<T*>(a.s) + row * a.cols + col, n, v);
+      float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, b[8] = {};
+      if (a.w) load8(static_cast<const T*>(a.w) + col, n, w);
+      if (a.b) load8(static_cast<const T*>(a.b) + col, n, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u += i < n ? (v[i] - mean) * (v[i] - mean) : 0.f;
-    t[0] += u;
-  }
-  row_sum<kWide>(t, red[1]);
-  const float rstd = 1.f / sqrtf(t[0] * per + a.eps);
-  if (a.stats && threadIdx.x == 0) {
-    a.stats[2 * row] = mean;
-    a.stats[2 * row + 1] = rstd;
-  }
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
-    const int n = get(col, v);
-    if (a.res) store8(static_cast<T*>(a.s) + row * a.cols + col, n, v);
-    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, b[8] = {};
-    if (a.w) load8(static_cast<const T*>(a.w) + col, n, w);
-    if (a.b) load8(static_cast<const T*>(a.b) + col, n, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fmaf((v[i] - mean) * rstd, w[i], b[i]);
-    store8(static_cast<T*>(a.y) + row * a.cols + col, n, v);
+      for (int i = 0; i < 8; ++i) v[i] = fmaf((v[i] - mean) * rstd, w[i], b[i]);
+      store8(static_cast<T*>(a.y) + row * a.cols + col, n, v);
+    }
+    __syncthreads();  // the sums have been read
   }
 }
 
 template <typename T>
 __global__ __launch_bounds__(kWide) void k_norm_grad_wide(NormGradArgs a) {
   __shared__ float red[2 * 16];
-  const int64_t row = blockIdx.x;
-  const float per = 1.f / (float)a.cols, mean = a.layer ? a.stats[2 * row] : 0.f, rstd = a.stats[2 * row + 1];
-  float x[8], g[8], t[2] = {0.f, 0.f};
+  const float per = 1.f / (float)a.cols;
+  int64_t row = blockIdx.x;
+  float mean = 0.f, rstd = 0.f, x[8], g[8];
   auto get = [&](int64_t col) {
     const int n = (int)min((int64_t)8, a.cols - col);
     load8(static_cast<const T*>(a.s) + row * a.lds + col, n, x);
@@ -268,26 +272,32 @@ __global__ __launch_bounds__(kWide) void k_norm_grad_wide(NormGradArgs a) {
     }
     return n;
   };
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
-    get(col);
-    float u[2] = {0.f, 0.f};
+  for (; row < a.rows; row += gridDim.x) {
+    mean = a.layer ? a.stats[2 * row] : 0.f;
+    rstd = a.stats[2 * row + 1];
+    float t[2] = {0.f, 0.f};
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
+      get(col);
+      float u[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u[0] += g[i];
-      u[1] += g[i] * x[i];
+      for (int i = 0; i < 8; ++i) {
+        u[0] += g[i];
+        u[1] += g[i] * x[i];
+      }
+      t[0] += u[0];
+      t[1] += u[1];
     }
-    t[0] += u[0];
-    t[1] += u[1];
-  }
-  row_sum<kWide>(t, red);
-  const float m1 = a.layer ? t[0] * per : 0.f, m2 = t[1] * per;
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
-    const int n = get(col);
-    float d[8] = {};
-    if (a.ds) load8(static_cast<const T*>(a.ds) + row * a.ldd + col, n, d);
+    row_sum<kWide>(t, red);
+    const float m1 = a.layer ? t[0] * per : 0.f, m2 = t[1] * per;
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += kWide * 8) {
+      const int n = get(col);
+      float d[8] = {};
+      if (a.ds) load8(static_cast<const T*>(a.ds) + row * a.ldd + col, n, d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] += rstd * (g[i] - m1 - x[i] * m2);
-    store8(static_cast<T*>(a.dx) + row * a.cols + col, n, d);
+      for (int i = 0; i < 8; ++i) d[i] += rstd * (g[i] - m1 - x[i] * m2);
+      store8(static_cast<T*>(a.dx) + row * a.cols + col, n, d);
+    }
+    __syncthreads();  // the sums have been read
   }
 }
 
@@ -366,7 +376,7 @@ int forward_columns(int64_t cols) { return cols <= 512 ? 8 : 16; }
 template <typename T>
 hipError_t forward(const NormArgs& a, hipStream_t s) {
   if (a.cols > kWideCols) {
-    hipLaunchKernelGGL((k_norm_wide<T>), dim3((unsigned)a.rows), dim3(kWide), 0, s, a);
+    hipLaunchKernelGGL((k_norm_wide<T>), dim3((unsigned)std::min<int64_t>(a.rows, kWideGrid)), dim3(kWide), 0, s, a);
     return hipGetLastError();
   }
   const int each = forward_columns(a.cols), threads = threads_of_row(a.cols, each);
@@ -389,7 +399,7 @@ hipError_t backward(const NormGradArgs& a, hipStream_t s) {
   const int64_t parts = norm_parts(a.rows, a.cols);
   hipError_t e = hipSuccess;
   if (a.cols > kWideGradCols) {
-    if (a.dx) hipLaunchKernelGGL((k_norm_grad_wide<T>), dim3((unsigned)a.rows), dim3(kWide), 0, s, a);
+    if (a.dx) hipLaunchKernelGGL((k_norm_grad_wide<T>), dim3((unsigned)std::min<int64_t>(a.rows, kWideGrid)), dim3(kWide), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.part && parts > 0)
       hipLaunchKernelGGL((k_norm_cols<T>), dim3((unsigned)((a.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s, a,

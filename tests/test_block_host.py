@@ -462,3 +462,26 @@ def test_four_bit_reference():
     assert ref.blocks64(torch.tensor([[float("inf")] + [1.0] * 31]))[2].item() == 255
     v = torch.randn(7, 75, generator=torch.Generator().manual_seed(1)) * 3
     assert torch.equal(ref.blocks64(v)[0], ref.fast_blocks64(v))
+
+
+@no_gpu
+def test_sizes_past_a_launch_are_refused_before_one(block):
+    """What one launch cannot hold is said with the arguments, not by the runtime half way through."""
+    lib = block.load_block()
+    for kw in (dict(rows=1 << 30, k=1 << 16, n=8, ldx=1 << 16), dict(rows=(1 << 31) - 1024, k=512, n=1 << 20, ldx=512)):
+        d = mx_desc(block, **kw)
+        assert lib.muon_mx_linear(ctypes.byref(d), None, A, A, A, None, None, A, A, (1 << 63), None) == INVALID
+    d = mx_desc(block, k=1 << 23, n=1 << 23, ldw=1 << 23)
+    assert lib.muon_mx_quantize(ctypes.byref(d), A, A, A, None) == INVALID
+    assert lib.muon_mx_dequantize(ctypes.byref(d), A, A, A, None) == INVALID
+
+
+def test_missing_nodes_are_said(block, monkeypatch):
+    """Without the module that launches there is an error, not another way round."""
+    import sys
+    monkeypatch.setattr(block, "_module", None)
+    monkeypatch.setitem(sys.modules, "muon_newton_schulz_05_amd._nodes", None)
+    import muon_newton_schulz_05_amd as pkg
+    monkeypatch.delattr(pkg, "_nodes", raising=False)
+    with pytest.raises(RuntimeError, match="not built"):
+        block._nodes("a norm")

@@ -520,3 +520,71 @@ def test_captured_autograd(muon):
         for a, b in zip(out, want):
             # torch's own sum of the squares may add in another order under capture
             assert torch.allclose(a, b, rtol=1e-5, atol=1e-7)
+
+
+# ------------------------------------------------------------------ autograd
+
+
+def test_what_a_gradient_needs_must_not_change(muon):
+    """A tensor kept for the gradient and written to since is refused, as torch's own operators refuse it."""
+    x, w = normal((8, 64), F32, 1).cuda().requires_grad_(), torch.ones(64, device="cuda", requires_grad=True)
+    y, s = muon.layer_norm(x, w, residual=normal((8, 64), F32, 2).cuda())
+    with torch.no_grad():
+        s.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    z = normal((8, 64), F32, 3).cuda().requires_grad_()
+    weights, _ = muon.gate(z, 3, normalize=False)
+    loss = muon.balance_loss(z, torch.zeros(8, 2, dtype=torch.int32, device="cuda")).loss
+    with torch.no_grad():
+        z.mul_(2)
+    for out in (weights.sum(), loss):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.backward()
+
+
+def test_each_operator_is_differentiable_once(muon):
+    z = normal((8, 16), F32, 1).cuda().requires_grad_()
+    ids = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    for out in (muon.rms_norm(z).sum(), muon.gate(z, 2, normalize=False).weights.sum(), muon.balance_loss(z, ids).loss):
+        (g,) = torch.autograd.grad(out, z, create_graph=True)
+        with pytest.raises(RuntimeError, match="differentiable once"):
+            g.square().sum().backward()
+    with torch.enable_grad():
+        assert not muon.gate(z, 2).ids.requires_grad and not muon.balance_loss(z, ids).counts.requires_grad
+        assert not muon.layer_norm(z.detach()).requires_grad
+
+
+def test_a_graph_is_walked_twice_and_from_another_thread(muon):
+    """retain_graph gives the same bits again; a backward pass on another thread and stream as well."""
+    import threading
+    x, w = normal((300, 200), BF16, 1).cuda().requires_grad_(), normal((200,), BF16, 2).cuda().requires_grad_()
+    dy = normal((300, 200), BF16, 3).cuda()
+    y = muon.layer_norm(x, w)
+    want = torch.autograd.grad(y, (x, w), dy, retain_graph=True)
+    got = []
+
+    def walk():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got.append(torch.autograd.grad(y, (x, w), dy))
+    t = threading.Thread(target=walk)
+    torch.cuda.synchronize()
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got[0]))
+
+
+def test_the_gradient_of_a_shared_input_is_summed(muon):
+    """One tensor as x and as residual, and a weight that two norms share."""
+    x, w = normal((20, 96), F32, 1).cuda().requires_grad_(), normal((96,), F32, 2).cuda().requires_grad_()
+    y, s = muon.layer_norm(x, w, residual=x)
+    z = muon.rms_norm(s, w)
+    dx, dw = torch.autograd.grad((y, z), (x, w), (torch.ones_like(y), torch.ones_like(z)))
+    xd, wd = x.detach().double().requires_grad_(), w.detach().double().requires_grad_()
+    sd = xd + xd
+    yd = torch.nn.functional.layer_norm(sd, (96,), wd, None, 1e-5)
+    zd = sd * torch.rsqrt(sd.square().mean(1, keepdim=True) + 1e-6) * wd
+    ex, ew = torch.autograd.grad((yd, zd), (xd, wd), (torch.ones_like(yd), torch.ones_like(zd)))
+    # chains of a few sums of 96 and 20 float32 terms
+    assert float((dx - ex).norm() / ex.norm()) < 100 * U32 and float((dw - ew).norm() / ew.norm()) < 100 * U32
