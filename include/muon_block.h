@@ -33,9 +33,10 @@ typedef struct {
   int32_t dtype;   /* of x, residual, w, b, y, s and their gradients */
   int32_t kind;    /* muon_norm_t                                     */
   int64_t rows, cols;
-  int64_t ldx;     /* row stride of x (forward), of s (backward)      */
-  int64_t ldr;     /* row stride of the residual (forward), of ds     */
+  int64_t ldx;     /* row stride of x                                 */
+  int64_t ldr;     /* row stride of the residual                      */
   int64_t ldg;     /* row stride of dy                                */
+  int64_t ldd;     /* row stride of ds                                */
   double eps;      /* at least 0                                      */
 } muon_norm_desc_t;
 
@@ -51,10 +52,11 @@ int muon_norm_workspace(const muon_norm_desc_t* desc, uint64_t* bytes);
 /* With g = dy w: dx = (g - mean(g) - xhat mean(g xhat)) / sqrt(var + eps) + ds
  * (no mean(g) for MUON_NORM_RMS; ds NULL: none), contiguous, the gradient of
  * x and of the residual alike; dw = sum over rows of dy xhat; db = sum of dy.
- * Each of dx, dw and db is NULL where not wanted. */
-int muon_norm_backward(const muon_norm_desc_t* desc, const void* dy, const void* s, const void* w, const float* stats,
-                       const void* ds, void* dx, void* dw, void* db, void* workspace, uint64_t workspace_bytes,
-                       void* stream);
+ * Each of dx, dw and db is NULL where not wanted.  x and residual as in the forward pass, or s for x and NULL:
+ * that reads and keeps one tensor less, and takes s as it was rounded. */
+int muon_norm_backward(const muon_norm_desc_t* desc, const void* dy, const void* x, const void* residual, const void* w,
+                       const float* stats, const void* ds, void* dx, void* dw, void* db, void* workspace,
+                       uint64_t workspace_bytes, void* stream);
 
 /* A router's logits [tokens, experts], rows ldz apart; experts up to 1024,
  * top <= experts.  mask: NULL, or one byte a token, 0 for a token that takes no part. */

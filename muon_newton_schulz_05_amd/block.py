@@ -34,7 +34,8 @@ EXPORTED_BLOCK = ("muon_norm_workspace", "muon_norm_forward", "muon_norm_backwar
 
 class NormDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
-                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldg", ctypes.c_int64), ("eps", ctypes.c_double)]
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldg", ctypes.c_int64), ("ldd", ctypes.c_int64),
+                ("eps", ctypes.c_double)]
 
 
 class GateDesc(ctypes.Structure):
@@ -62,7 +63,7 @@ def load_block():
     sig = {
         "muon_norm_workspace": [N, UP],
         "muon_norm_forward": [N] + [P] * 8,
-        "muon_norm_backward": [N] + [P] * 9 + [U64, P],
+        "muon_norm_backward": [N] + [P] * 10 + [U64, P],
         "muon_gate_forward": [G] + [P] * 5,
         "muon_gate_backward": [G] + [P] * 7,
         "muon_balance_workspace": [G, UP],
@@ -150,20 +151,22 @@ def norm_forward(x, weight=None, bias=None, *, eps=1e-5, residual=None, kind="la
     return y, x if s is None else s, stats
 
 
-def norm_backward(dy, s, weight, stats, *, kind="layer", ds=None, needs=(True, True, True)):
+def norm_backward(dy, x, weight, stats, *, residual=None, kind="layer", ds=None, needs=(True, True, True)):
     """(dx, dweight, dbias) of ``norm_forward`` for the gradients dy and ds; needs: which of them are computed.
 
-    dx is the gradient of x and of the residual alike."""
+    dx is the gradient of x and of the residual alike.  In their place s may be given as x: that keeps one tensor less
+    for the gradient, and takes s as it was rounded."""
     code = _norm_kind(kind)
-    _check_norm(s, weight, None, dy)
-    _same(s, ds=ds)
-    if ds is not None and ds.shape != s.shape:
-        raise ValueError(f"ds has shape {tuple(ds.shape)}, s {tuple(s.shape)}")
-    rows = math.prod(s.shape[:-1])
-    if stats.dtype is not torch.float32 or stats.shape != (rows, 2) or stats.device != s.device \
+    _check_norm(x, weight, None, residual)
+    for name, t in (("dy", dy), ("ds", ds)):
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, x {tuple(x.shape)}")
+    _same(x, dy=dy, ds=ds)
+    rows = math.prod(x.shape[:-1])
+    if stats.dtype is not torch.float32 or stats.shape != (rows, 2) or stats.device != x.device \
             or not stats.is_contiguous():
         raise ValueError("stats must be what norm_forward returned")
-    return tuple(_nodes("norm_backward").norm_backward(dy, s, weight, stats, ds, code, *needs))
+    return tuple(_nodes("norm_backward").norm_backward(dy, x, residual, weight, stats, ds, code, *needs))
 
 
 def _norm(x, weight, bias, residual, eps, kind):
@@ -180,8 +183,7 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, residual=None):
     the result is (y, s): the norm, and the sum that the residual stream goes on with.  Differentiable in
     every tensor (once), through both results.
 
-    bfloat16: y comes from the float32 sum and is rounded once.  The gradient takes the normalised value from
-    s as returned, so with a residual it is off by half a step of s over the row's standard deviation."""
+    bfloat16: y and the gradients come from the float32 sum and are rounded once."""
     return _norm(x, weight, bias, residual, eps, 0)
 
 

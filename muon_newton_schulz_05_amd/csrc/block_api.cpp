@@ -46,7 +46,7 @@ int check_norm(const muon_norm_desc_t* d) {
   if (d->kind != MUON_NORM_LAYER && d->kind != MUON_NORM_RMS) return bad("unknown norm");
   if (d->rows < 0 || d->rows > kMaxRows) return bad("rows outside [0, 2^31 - 1024]");
   if (d->cols < 0 || d->cols > kMaxCols) return bad("cols outside [0, 2^24]");
-  if (d->ldx < 0 || d->ldr < 0 || d->ldg < 0) return bad("a stride is negative");
+  if (d->ldx < 0 || d->ldr < 0 || d->ldg < 0 || d->ldd < 0) return bad("a stride is negative");
   if (!(d->eps >= 0.0 && d->eps < 1e30)) return bad("eps is negative or not finite");
   return MUON_OK;
 }
@@ -199,14 +199,16 @@ int muon_norm_forward(const muon_norm_desc_t* d, const void* x, const void* resi
   return hip_result(muon::launch_norm(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_norm_forward");
 }
 
-int muon_norm_backward(const muon_norm_desc_t* d, const void* dy, const void* s, const void* w, const float* stats,
-                       const void* ds, void* dx, void* dw, void* db, void* ws, uint64_t ws_bytes, void* stream) {
+int muon_norm_backward(const muon_norm_desc_t* d, const void* dy, const void* x, const void* residual, const void* w,
+                       const float* stats, const void* ds, void* dx, void* dw, void* db, void* ws, uint64_t ws_bytes,
+                       void* stream) {
   MUON_TRY(check_norm(d));
   if (!dx && !dw && !db) return set_error(MUON_OK, "%s", "");
   const int es = elem(d->dtype);
   const int64_t count = d->rows * d->cols;
   MUON_TRY(check_at(dy, count, es, "dy"));
-  MUON_TRY(check_at(s, count, es, "s"));
+  MUON_TRY(check_at(x, count, es, "x"));
+  MUON_TRY(check_at(residual, 0, es, "residual"));
   MUON_TRY(check_at(w, 0, es, "w"));
   MUON_TRY(check_at(stats, count, 4, "stats"));
   MUON_TRY(check_at(ds, 0, es, "ds"));
@@ -214,8 +216,8 @@ int muon_norm_backward(const muon_norm_desc_t* d, const void* dy, const void* s,
   MUON_TRY(check_at(dw, 0, es, "dw"));
   MUON_TRY(check_at(db, 0, es, "db"));
   if (dw || db) MUON_TRY(check_space(norm_bytes(d), ws, ws_bytes));
-  const muon::NormGradArgs a{dy, s, w, ds, stats, dx, dw, db, dw || db ? static_cast<float*>(ws) : nullptr,
-                             d->rows, d->cols, d->ldg, d->ldx, d->ldr, d->kind == MUON_NORM_LAYER};
+  const muon::NormGradArgs a{dy, x, residual, w, ds, stats, dx, dw, db, dw || db ? static_cast<float*>(ws) : nullptr,
+                             d->rows, d->cols, d->ldg, d->ldx, d->ldr, d->ldd, d->kind == MUON_NORM_LAYER};
   return hip_result(muon::launch_norm_grad(a, d->dtype, static_cast<hipStream_t>(stream)), "muon_norm_backward");
 }
 

@@ -65,7 +65,7 @@ variable_list once(variable_list grads) {
 
 struct Normed {
   Tensor y, s, stats, w;
-  Tensor kept;  // what the gradient reads: s, or x (or its copy, where x has no contiguous rows)
+  Tensor x, r;  // what the gradient reads: as given, or the copies, where their rows are not contiguous
 };
 Normed norm_run(const Tensor& x, const OptTensor& weight, const OptTensor& bias, const OptTensor& residual, double eps,
                 int64_t kind, bool keep) {
@@ -78,28 +78,31 @@ Normed norm_run(const Tensor& x, const OptTensor& weight, const OptTensor& bias,
   o.y = at::empty(x.sizes(), x.options());
   if (residual) o.s = at::empty(x.sizes(), x.options());
   if (keep) o.stats = at::empty({x2.size(0), 2}, x.options().dtype(at::kFloat));
-  const muon_norm_desc_t d{dtype_of(x), (int32_t)kind, x2.size(0), cols, ld(x2), residual ? ld(r2) : 0, 0, eps};
+  const muon_norm_desc_t d{dtype_of(x), (int32_t)kind, x2.size(0), cols, ld(x2), residual ? ld(r2) : 0, 0, 0, eps};
   check(muon_norm_forward(&d, at_of(x2), at_of(r2), at_of(o.w), at_of(b), out_of(o.y), out_of(o.s),
                           static_cast<float*>(out_of(o.stats)), stream_of(x)),
         "muon_norm_forward");
-  o.kept = residual ? o.s : x2.is_alias_of(x) ? x : x2;
+  o.x = x2.is_alias_of(x) ? x : x2;
+  if (residual) o.r = r2.is_alias_of(*residual) ? *residual : r2;
   return o;
 }
-// dx like s, dw, db; undefined where not needed.
-variable_list norm_grad(const Tensor& dy, const Tensor& s, const Tensor& w, const Tensor& stats, const Tensor& ds,
+// dx like x, dw, db; undefined where not needed.
+variable_list norm_grad(const Tensor& dy, const Tensor& x, const Tensor& residual, const Tensor& w, const Tensor& stats, const Tensor& ds,
                         int64_t kind, bool need_x, bool need_w, bool need_b) {
-  const c10::DeviceGuard guard(s.device());
-  const int64_t cols = s.size(-1);
-  const Tensor rows = flat(s, cols), g = flat(dy, cols), d2 = ds.defined() ? flat(ds, cols) : Tensor();
+  const c10::DeviceGuard guard(x.device());
+  const int64_t cols = x.size(-1);
+  const Tensor rows = flat(x, cols), g = flat(dy, cols), d2 = ds.defined() ? flat(ds, cols) : Tensor();
+  const Tensor r2 = residual.defined() ? flat(residual, cols) : Tensor();
   Tensor dx, dw, db;
-  if (need_x) dx = at::empty(s.sizes(), rows.options());
+  if (need_x) dx = at::empty(x.sizes(), rows.options());
   if (need_w) dw = at::empty({cols}, rows.options());
   if (need_b) db = at::empty({cols}, rows.options());
-  const muon_norm_desc_t d{dtype_of(rows), (int32_t)kind, rows.size(0), cols, ld(rows), ds.defined() ? ld(d2) : 0, ld(g), 0.0};
+  const muon_norm_desc_t d{dtype_of(rows), (int32_t)kind, rows.size(0), cols, ld(rows), residual.defined() ? ld(r2) : 0, ld(g),
+                           ds.defined() ? ld(d2) : 0, 0.0};
   uint64_t bytes = 0;
   if (need_w || need_b) check(muon_norm_workspace(&d, &bytes), "muon_norm_workspace");
   const Tensor ws = space(bytes, rows);
-  check(muon_norm_backward(&d, at_of(g), at_of(rows), at_of(w), static_cast<const float*>(at_of(stats)), at_of(d2),
+  check(muon_norm_backward(&d, at_of(g), at_of(rows), at_of(r2), at_of(w), static_cast<const float*>(at_of(stats)), at_of(d2),
                            out_of(dx), out_of(dw), out_of(db), out_of(ws), bytes, stream_of(rows)),
         "muon_norm_backward");
   return {dx, dw, db};
@@ -109,8 +112,8 @@ struct NormNode : public Function<NormNode> {
   static variable_list forward(AutogradContext* ctx, const Tensor& x, const OptTensor& weight, const OptTensor& bias,
                                const OptTensor& residual, double eps, int64_t kind) {
     const Normed o = norm_run(x, weight, bias, residual, eps, kind, true);
-    ctx->save_for_backward({o.kept, o.w, o.stats});
-    const bool reshaped = o.kept.dim() != x.dim();
+    ctx->save_for_backward({o.x, o.r, o.w, o.stats});
+    const bool reshaped = o.x.dim() != x.dim();
     if (reshaped) ctx->saved_data["shape"] = x.sizes().vec();
     ctx->saved_data["given"] = int64_t((weight ? 1 : 0) | (bias ? 2 : 0) | (residual ? 4 : 0) | (reshaped ? 8 : 0)) | kind << 8;
     ctx->set_materialize_grads(false);
@@ -132,7 +135,7 @@ struct NormNode : public Function<NormNode> {
       dx = ds;
     } else {
       const variable_list saved = ctx->get_saved_variables();
-      const variable_list g = norm_grad(dy, saved[0], saved[1], saved[2], ds, given >> 8, need_x || need_r, need_w, need_b);
+      const variable_list g = norm_grad(dy, saved[0], saved[1], saved[2], saved[3], ds, given >> 8, need_x || need_r, need_w, need_b);
       dx = g[0];
       if (dx.defined() && (given & 8)) dx = dx.view(ctx->saved_data["shape"].toIntVector());
       dw = g[1];
@@ -156,10 +159,11 @@ std::tuple<Tensor, OptTensor, Tensor> norm_forward(const Tensor& x, const OptTen
   const Normed o = norm_run(x, weight, bias, residual, eps, kind, true);
   return {o.y, residual ? OptTensor(o.s) : OptTensor(), o.stats};
 }
-std::vector<OptTensor> norm_backward(const Tensor& dy, const Tensor& s, const OptTensor& weight, const Tensor& stats,
-                                     const OptTensor& ds, int64_t kind, bool need_x, bool need_w, bool need_b) {
+std::vector<OptTensor> norm_backward(const Tensor& dy, const Tensor& x, const OptTensor& residual, const OptTensor& weight,
+                                     const Tensor& stats, const OptTensor& ds, int64_t kind, bool need_x, bool need_w, bool need_b) {
   const at::NoGradGuard no_grad;
-  const variable_list g = norm_grad(dy, s, whole(weight), stats, ds ? *ds : Tensor(), kind, need_x, need_w, need_b);
+  const variable_list g = norm_grad(dy, x, residual ? *residual : Tensor(), whole(weight), stats, ds ? *ds : Tensor(), kind,
+                                    need_x, need_w, need_b);
   std::vector<OptTensor> out;
   for (const Tensor& t : g) out.push_back(t.defined() ? OptTensor(t) : OptTensor());
   return out;

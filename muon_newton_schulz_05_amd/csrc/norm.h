@@ -19,7 +19,8 @@ struct NormArgs {
 };
 struct NormGradArgs {
   const void* dy;
-  const void* s;
+  const void* x;
+  const void* res;   // null: s is x
   const void* w;
   const void* ds;    // null, or what reaches s by other ways
   const float* stats;
@@ -27,7 +28,7 @@ struct NormGradArgs {
   void* dw;
   void* db;
   float* part;       // [norm_parts][2][cols], where dw or db is wanted
-  int64_t rows, cols, ldg, lds, ldd;
+  int64_t rows, cols, ldg, ldx, ldr, ldd;
   int32_t layer;
 };
 int64_t norm_parts(int64_t rows, int64_t cols);  // rows of partial sums

@@ -7,8 +7,8 @@
 // (The root-mean-square norm takes mean = 0 and has no mean(g).)  A row stays in the registers of TPR threads, CH
 // pieces of eight columns each, so that it is read once; the variance is taken of the
 // differences from the mean, in a second reduction, and loses nothing to a large mean.  y comes from the
-// float32 sum s; what is kept of s for the gradient (and for the residual stream) has
-// the tensors' type, so in bf16 xhat is there off by at most half a step of s times rstd.
+// float32 sum s, and the gradient adds x and r again: from s as it is stored, in bf16, dw would be 1.4 times as
+// far off as its own rounding makes it (reading one tensor less, 105 us for 110 at 16384 x 4096).
 //
 // The gradient of w and b is a sum over rows: each thread adds up its columns over the rows that its
 // workgroup walks, workgroups leave one row of partial sums each, and a second
@@ -127,12 +127,13 @@ __global__ __launch_bounds__(kThreads(TPR)) void k_norm_grad(NormGradArgs a) {
   const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - col));
   float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, dw[8] = {}, db[8] = {};
   if (a.w) load8(static_cast<const T*>(a.w) + col, n, w);
-  Raw<T> rx, rg, rd;
+  Raw<T> rx, rr, rg, rd;
   float mean = 0.f, rstd = 0.f;
   auto fetch = [&](int64_t row) __attribute__((always_inline)) {
     const bool in = row < a.rows;
     const int m = in ? n : 0;
-    rx.load(static_cast<const T*>(a.s) + row * a.lds + col, m);
+    rx.load(static_cast<const T*>(a.x) + row * a.ldx + col, m);
+    if (a.res) rr.load(static_cast<const T*>(a.res) + row * a.ldr + col, m);
     rg.load(static_cast<const T*>(a.dy) + row * a.ldg + col, m);
     if (a.ds) rd.load(static_cast<const T*>(a.ds) + row * a.ldd + col, m);
     mean = in && a.layer ? a.stats[2 * row] : 0.f;
@@ -144,13 +145,13 @@ __global__ __launch_bounds__(kThreads(TPR)) void k_norm_grad(NormGradArgs a) {
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += step, turn ^= 1) {
     const int64_t row = r0 + sub;
     const bool in = row < a.rows;
-    const Raw<T> cx = rx, cg = rg, cd = rd;
+    const Raw<T> cx = rx, cr = rr, cg = rg, cd = rd;
     const float mu = mean, rs = rstd;
     fetch(row + step);
     float x[8], g[8], t[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      x[i] = in && i < n ? (cx.at(i) - mu) * rs : 0.f;
+      x[i] = in && i < n ? ((a.res ? cx.at(i) + cr.at(i) : cx.at(i)) - mu) * rs : 0.f;
       g[i] = cg.at(i);
       dw[i] += g[i] * x[i];
       db[i] += g[i];
@@ -191,6 +192,17 @@ __global__ __launch_bounds__(kThreads(TPR)) void k_norm_grad(NormGradArgs a) {
   if (a.db) leave(db, 1);
 }
 
+// Eight elements of s = x + r.
+template <typename T, typename A>
+__device__ __forceinline__ void load_sum(const A& a, int64_t row, int64_t col, int n, float (&v)[8]) {
+  load8(static_cast<const T*>(a.x) + row * a.ldx + col, n, v);
+  if (!a.res) return;
+  float r[8];
+  load8(static_cast<const T*>(a.res) + row * a.ldr + col, n, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += r[i];
+}
+
 // Rows longer than the registers of a workgroup hold: read three times.
 constexpr int kWide = 1024, kWideCols = 16384, kWideGradCols = 8192;
 constexpr int64_t kWideGrid = 1 << 20;  // a launch holds fewer than 2^32 threads
@@ -202,13 +214,7 @@ __global__ __launch_bounds__(kWide) void k_norm_wide(NormArgs a) {
   int64_t row = blockIdx.x;
   auto get = [&](int64_t col, float (&v)[8]) {
     const int n = (int)min((int64_t)8, a.cols - col);
-    load8(static_cast<const T*>(a.x) + row * a.ldx + col, n, v);
-    if (a.res) {
-      float r[8];
-      load8(static_cast<const T*>(a.res) + row * a.ldr + col, n, r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[i];
-    }
+    load_sum<T>(a, row, col, n, v);
     return n;
   };
   for (; row < a.rows; row += gridDim.x) {
@@ -261,7 +267,7 @@ __global__ __launch_bounds__(kWide) void k_norm_grad_wide(NormGradArgs a) {
   float mean = 0.f, rstd = 0.f, x[8], g[8];
   auto get = [&](int64_t col) {
     const int n = (int)min((int64_t)8, a.cols - col);
-    load8(static_cast<const T*>(a.s) + row * a.lds + col, n, x);
+    load_sum<T>(a, row, col, n, x);
     load8(static_cast<const T*>(a.dy) + row * a.ldg + col, n, g);
     float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
     if (a.w) load8(static_cast<const T*>(a.w) + col, n, w);
@@ -312,7 +318,7 @@ __global__ __launch_bounds__(256) void k_norm_cols(NormGradArgs a, int64_t stret
   for (int64_t row = r0; row < r1; ++row) {
     const float mean = a.layer ? a.stats[2 * row] : 0.f, rstd = a.stats[2 * row + 1];
     float x[8], g[8];
-    load8(static_cast<const T*>(a.s) + row * a.lds + col, n, x);
+    load_sum<T>(a, row, col, n, x);
     load8(static_cast<const T*>(a.dy) + row * a.ldg + col, n, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -46,8 +46,6 @@ def norm64(x, r, w, b, dy, ds, eps, layer):
     if dy is None:
         return out
     dy = dy.double()
-    if r is not None:
-        ex = ex + u * h.abs() * rstd                          # s as it is kept
     g = dy * w
     mg = g.mean(1, keepdim=True) if layer else torch.zeros(rows, 1, dtype=torch.float64)
     mx = (g * xhat).mean(1, keepdim=True)

@@ -75,7 +75,7 @@ def _desc(cls, defaults, kw):
 
 
 def norm_desc(block, **kw):
-    return _desc(block.NormDesc, dict(dtype=1, kind=0, rows=4, cols=8, ldx=8, ldr=8, ldg=8, eps=1e-5), kw)
+    return _desc(block.NormDesc, dict(dtype=1, kind=0, rows=4, cols=8, ldx=8, ldr=8, ldg=8, ldd=8, eps=1e-5), kw)
 
 
 def gate_desc(block, **kw):
@@ -92,7 +92,7 @@ def norm_calls(lib, d):
     need = ctypes.c_uint64(0)
     return [lambda: lib.muon_norm_workspace(p, ctypes.byref(need)),
             lambda: lib.muon_norm_forward(p, A, None, None, None, A, None, None, None),
-            lambda: lib.muon_norm_backward(p, A, A, None, A, None, A, None, None, None, 0, None)]
+            lambda: lib.muon_norm_backward(p, A, A, None, None, A, None, A, None, None, None, 0, None)]
 
 
 def gate_calls(lib, d):
@@ -120,7 +120,7 @@ BIG = 1 << 31
 
 
 @pytest.mark.parametrize("kw", [dict(dtype=7), dict(kind=2), dict(kind=-1), dict(rows=-1), dict(rows=BIG - 1023),
-                                dict(cols=-1), dict(cols=(1 << 24) + 1), dict(ldx=-8), dict(ldr=-1), dict(ldg=-1),
+                                dict(cols=-1), dict(cols=(1 << 24) + 1), dict(ldx=-8), dict(ldr=-1), dict(ldg=-1), dict(ldd=-1),
                                 dict(eps=-1e-9), dict(eps=float("nan")), dict(eps=float("inf"))], ids=str)
 def test_norm_refuses_bad_descriptors(block, kw):
     for call in norm_calls(block.load_block(), norm_desc(block, **kw)):
@@ -176,11 +176,11 @@ def test_norm_checks_every_pointer(block):
     need = ctypes.c_uint64(0)
     assert lib.muon_norm_workspace(ctypes.byref(d), ctypes.byref(need)) == 0 and need.value
 
-    def backward(dy, s, w, stats, ds, dx, dw, db, ws, size):
-        return lib.muon_norm_backward(ctypes.byref(d), dy, s, w, stats, ds, dx, dw, db, ws, size, None)
-    good = dict(dy=A, s=A, w=A, stats=A, ds=A, dx=A, dw=A, db=A, ws=A, size=need.value)
-    _refused(backward, good, [dict(dy=None), dict(s=None), dict(stats=None), dict(ws=None), dict(size=need.value - 1),
-                              dict(ws=A + 8), dict(stats=A + 2)] + [{n: A + 1} for n in ("dy", "s", "w", "ds", "dx", "dw", "db")])
+    def backward(dy, x, r, w, stats, ds, dx, dw, db, ws, size):
+        return lib.muon_norm_backward(ctypes.byref(d), dy, x, r, w, stats, ds, dx, dw, db, ws, size, None)
+    good = dict(dy=A, x=A, r=A, w=A, stats=A, ds=A, dx=A, dw=A, db=A, ws=A, size=need.value)
+    _refused(backward, good, [dict(dy=None), dict(x=None), dict(stats=None), dict(ws=None), dict(size=need.value - 1),
+                              dict(ws=A + 8), dict(stats=A + 2)] + [{n: A + 1} for n in ("dy", "x", "r", "w", "ds", "dx", "dw", "db")])
     assert backward(**{**good, "dw": None, "db": None, "ws": None, "size": 0}) == LAUNCHED   # dx alone needs none
     assert backward(**{**good, "dx": None, "dw": None, "db": None, "dy": None}) == 0         # nothing is asked for
 
@@ -347,7 +347,8 @@ def test_the_binding_refuses_what_does_not_fit(block):
         lambda: muon.layer_norm(G()), lambda: muon.norm_forward(x, kind="batch"),
         lambda: muon.norm_backward(x, x, None, G(3, 2), kind="x"), lambda: muon.norm_backward(x, x, None, G(2, 2)),
         lambda: muon.norm_backward(x, x, None, G(3, 2, dtype=BF)), lambda: muon.norm_backward(G(2, 8), x, None, G(3, 2)),
-        lambda: muon.norm_backward(x, x, None, G(3, 2), ds=G(3, 9)), lambda: muon.norm_backward(x, x, G(9), G(3, 2)),
+        lambda: muon.norm_backward(x, x, None, G(3, 2), ds=G(3, 9)),
+        lambda: muon.norm_backward(x, x, None, G(3, 2), residual=G(3, 9)), lambda: muon.norm_backward(x, x, None, G(3, 2), ds=host), lambda: muon.norm_backward(x, x, G(9), G(3, 2)),
         lambda: muon.gate(host, 2), lambda: muon.gate(z, 0), lambda: muon.gate(z, 9), lambda: muon.gate(G(8), 2),
         lambda: muon.gate(G(3, 1025), 2), lambda: muon.gate(G(3, 0), 1), lambda: muon.gate(G(3, 8, dtype=torch.float64), 2),
         lambda: muon.gate(z, 2, mask=G(3, dtype=torch.uint8)), lambda: muon.gate(z, 2, mask=G(4, dtype=torch.bool)),

@@ -147,16 +147,23 @@ def test_norm_partial_gradients(muon):
     x, w, b = (normal(s, BF16, i).cuda() for i, s in enumerate(((50, 200), (200,), (200,))))
     dy = normal((50, 200), BF16, 9).cuda()
     y, s, stats = muon.norm_forward(x, w, b, residual=dy)
-    whole = muon.norm_backward(dy, s, w, stats, ds=x)
+    whole = muon.norm_backward(dy, x, w, stats, residual=dy, ds=x)
     for i in range(3):
-        part = muon.norm_backward(dy, s, w, stats, ds=x, needs=tuple(j == i for j in range(3)))
+        part = muon.norm_backward(dy, x, w, stats, residual=dy, ds=x, needs=tuple(j == i for j in range(3)))
         assert torch.equal(part[i], whole[i]) and [p is None for p in part] == [j != i for j in range(3)]
+    # From the stored sum in their place: xhat is off by half a step of s more, over the standard deviation.
+    h = x.double() + dy.double()
+    xhat = (h - h.mean(1, keepdim=True)) / h.var(1, correction=0, keepdim=True).sqrt()
+    dw, tol = (dy.double() * xhat).sum(0), (dy.double().abs() * h.abs() / h.std(1, keepdim=True)).sum(0) * 2.0 ** -8
+    stored = muon.norm_backward(dy, s, w, stats, ds=x)
+    assert ((stored[1].double() - dw).abs() <= tol + 2.0 ** -8 * dw.abs() + 1e-3).all()
+    assert torch.equal(stored[2], whole[2])
     leaf, res = x.clone().requires_grad_(), dy.clone().requires_grad_()
     y, s = muon.layer_norm(leaf, residual=res)
     g1, g2 = torch.autograd.grad(s, (leaf, res), dy, retain_graph=True)      # y is not used
     assert torch.equal(g1, dy) and torch.equal(g2, dy)
     (only,) = torch.autograd.grad(y, leaf, dy, retain_graph=True)            # s is not used
-    want = muon.norm_backward(dy, s.detach(), None, muon.norm_forward(x, residual=dy)[2])[0]
+    want = muon.norm_backward(dy, x, None, muon.norm_forward(x, residual=dy)[2], residual=dy)[0]
     assert torch.equal(only, want)
     (none,) = torch.autograd.grad(muon.layer_norm(x, w.requires_grad_()), w, dy)
     assert none.shape == w.shape
@@ -475,7 +482,7 @@ def test_capture_of_forward_and_backward(muon):
         u = muon.mx_expert_linear(muon.dispatch_forward(y, r), up, r.offsets, activation="gelu")
         dz = muon.gate_backward(dw, z, gating, normalize=False, mask=mask)
         dz = dz + muon.balance_backward(dloss, z, gating.ids, shares, mask=mask)
-        return (y, s, loss, counts, u, dz, *muon.norm_backward(dy, s, g, stats, ds=x), gating.weights, gating.ids)
+        return (y, s, loss, counts, u, dz, *muon.norm_backward(dy, x, g, stats, residual=dy, ds=x), gating.weights, gating.ids)
 
     step()
     side = torch.cuda.Stream()
@@ -528,11 +535,15 @@ def test_captured_autograd(muon):
 def test_what_a_gradient_needs_must_not_change(muon):
     """A tensor kept for the gradient and written to since is refused, as torch's own operators refuse it."""
     x, w = normal((8, 64), F32, 1).cuda().requires_grad_(), torch.ones(64, device="cuda", requires_grad=True)
-    y, s = muon.layer_norm(x, w, residual=normal((8, 64), F32, 2).cuda())
+    r = normal((8, 64), F32, 2).cuda()
+    y, s = muon.layer_norm(x, w, residual=r)
     with torch.no_grad():
-        s.add_(1)
+        r.add_(1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+    y, s = muon.layer_norm(x, w, residual=r)
+    s.add_(1)                                                   # the sum is the caller's
+    (y.sum() + s.sum()).backward()
     z = normal((8, 64), F32, 3).cuda().requires_grad_()
     weights, _ = muon.gate(z, 3, normalize=False)
     loss = muon.balance_loss(z, torch.zeros(8, 2, dtype=torch.int32, device="cuda")).loss
