@@ -43,6 +43,52 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   if (v == -kInf) return 0u;
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float key_value(uint32_t k) {  // any NaN for NaN
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// The next choice of a token: the largest of its keys, the lowest expert among equals, which leaves the keys.  A bfloat16
+// value's key has 16 bits, which leaves room for the expert: one maximum then finds both.  A
+// float32 value takes a second reduction, of the experts that have it.
+template <typename T> struct Choice;
+template <> struct Choice<uint16_t> {
+  static __device__ __forceinline__ uint32_t key(float v, int e) {
+    const uint32_t k = order_key(v);
+    return k ? (k & 0xffff0000u) | (uint32_t)(kGateMaxExperts - 1 - e) : 0u;
+  }
+  template <int L, int V>
+  static __device__ __forceinline__ bool next(uint32_t (&key)[V], int, float& v, int& e) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    best = group_max<L>(best);
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = key[i] == best ? 0u : key[i];
+    e = kGateMaxExperts - 1 - (int)(best & (kGateMaxExperts - 1));
+    // The low bits that a negative value's key would have are ones.
+    v = key_value(best & 0x80000000u ? best & 0xffff0000u : best | 0xffffu);
+    if (best >= 0xffff0000u) v = __builtin_nanf("");
+    return best != 0u;
+  }
+};
+template <> struct Choice<float> {
+  static __device__ __forceinline__ uint32_t key(float v, int) { return order_key(v); }
+  template <int L, int V>
+  static __device__ __forceinline__ bool next(uint32_t (&key)[V], int first, float& v, int& e) {
+    uint32_t best = key[0], at = ~0u;
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    best = group_max<L>(best);
+#pragma unroll
+    for (int i = 0; i < V; ++i) at = min(at, key[i] == best ? (uint32_t)(first + i) : ~0u);
+    at = group_min<L>(at);
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = (uint32_t)(first + i) == at ? 0u : key[i];
+    e = (int)at;
+    v = key_value(best);
+    return best != 0u;
+  }
+};
 
 // The tokens of a wave: lane l of L holds experts l V .. l V + V - 1.
 template <typename T, int L, int V>
@@ -95,18 +141,6 @@ struct Row {
   }
 };
 
-template <int L, int S = 0>
-__device__ __forceinline__ void group_best(uint32_t& key, int& at) {
-  if constexpr ((1 << S) < L) {
-    const uint32_t k = partner<S>(key);
-    const int i = (int)partner<S>((uint32_t)at);
-    const bool take = k > key || (k == key && i < at);
-    key = take ? k : key;
-    at = take ? i : at;
-    group_best<L, S + 1>(key, at);
-  }
-}
-
 // The tokens of one workgroup, from `first` on.
 template <typename T, int L, int V>
 __device__ __forceinline__ void gate_tokens(const GateArgs& a, int64_t first) {
@@ -117,7 +151,7 @@ __device__ __forceinline__ void gate_tokens(const GateArgs& a, int64_t first) {
   r.load(static_cast<const T*>(a.logits) + t * a.ldz, on, z);
   uint32_t key[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = order_key(z[i]);
+  for (int i = 0; i < V; ++i) key[i] = Choice<T>::key(z[i], r.l * V + i);
   // Rank j's choice stays in lane j mod L, slot j / L.
   float val[V], peak = 0.f;
   int id[V];
@@ -127,22 +161,11 @@ __device__ __forceinline__ void gate_tokens(const GateArgs& a, int64_t first) {
     id[s] = -1;
     for (int q = 0; q < L; ++q) {
       if (s * L + q >= a.top) break;  // uniform
-      uint32_t best = 0u;
-      int at = r.l * V;
-      float v = 0.f;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i) {
-        const bool take = key[i] >= best;
-        best = take ? key[i] : best;
-        at = take ? r.l * V + i : at;
-      }
-      group_best<L>(best, at);
-      // What the key stands for (any NaN for NaN).
-      v = best == 0xffffffffu ? __builtin_nanf("") : __uint_as_float(best & 0x80000000u ? best & 0x7fffffffu : ~best);
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = at == r.l * V + i ? 0u : key[i];
+      float v;
+      int at;
+      const bool found = Choice<T>::template next<L, V>(key, r.l * V, v, at);
       if (s == 0 && q == 0) peak = v;
-      if (q == r.l && best != 0u) {
+      if (q == r.l && found) {
         val[s] = v;
         id[s] = at;
       }

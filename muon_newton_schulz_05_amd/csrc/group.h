@@ -41,4 +41,15 @@ __device__ __forceinline__ float group_max(float v) {
   else return v;
 }
 
+template <int L, int S = 0>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr ((1 << S) < L) return group_max<L, S + 1>(max(v, partner<S>(v)));
+  else return v;
+}
+template <int L, int S = 0>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  if constexpr ((1 << S) < L) return group_min<L, S + 1>(min(v, partner<S>(v)));
+  else return v;
+}
+
 }  // namespace muon
