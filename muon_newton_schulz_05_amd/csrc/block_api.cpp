@@ -124,12 +124,13 @@ muon::MxArgs mx_args(const muon_mx_desc_t* d) {
   a.t = d->w_layout == 0;
   return a;
 }
+constexpr int64_t kMxOwnRows = 4;
 // A layer's product: its tile and split, and what it takes of the workspace.
 struct MxPlan {
   muon::MxProduct p{};
   int tile = 0, cols = 0;
   uint64_t x_values = 0, x_scales = 0, partials = 0;  // bytes
-  bool few() const { return tile >= muon::kMxRows32; }
+  bool own() const { return tile == muon::kMxRowsOwn; }
   uint64_t bytes() const { return x_values + x_scales + partials; }
 };
 
@@ -147,18 +148,18 @@ MxPlan mx_plan(const muon_mx_desc_t* d) {
   auto blocks_m = [&](int tile) { return muon::group_blocks(d->rows, d->groups, grouped, muon::mx_tile_m(tile)); };
   auto tiles = [&](int tile) { return blocks_m(tile) * ((d->n + muon::mx_tile_n(tile, 0, 0) - 1) / muon::mx_tile_n(tile, 0, 0)); };
   const int64_t m_each = grouped ? d->rows / d->groups : d->rows;
-  if (m_each <= 32) q.tile = m_each <= 16 ? muon::kMxRows16 : muon::kMxRows32;
+  if (m_each <= 32) q.tile = m_each <= kMxOwnRows ? muon::kMxRowsOwn : m_each <= 16 ? muon::kMxRows16 : muon::kMxRows32;
   else if (m_each >= 256 && tiles(muon::kMx256x128) >= kCus) q.tile = muon::kMx256x128;
   else if (tiles(muon::kMx128) >= kCus) q.tile = muon::kMx128;
   else q.tile = muon::kMx64;
   q.cols = muon::mx_tile_n(q.tile, blocks_m(q.tile), d->n);
   g.tiles_m = (int32_t)blocks_m(q.tile);
   g.tiles_n = (int32_t)((d->n + q.cols - 1) / q.cols);
-  if (q.few()) return q;
+  if (q.own()) return q;
   q.x_values = (uint64_t)muon::mx_value_bytes(d->rows, d->k);
   q.x_scales = (uint64_t)muon::mx_scale_bytes(d->rows, d->k);
   const int64_t t = (int64_t)g.tiles_m * g.tiles_n, chunks = muon::mx_chunks(d->k);
-  if (!grouped && t > 0 && t < kCus && chunks >= 4) {
+  if (q.tile <= muon::kMx64 && !grouped && t > 0 && t < kCus && chunks >= 4) {
     const int64_t s = std::min<int64_t>((2 * kCus + t - 1) / t, chunks / 2), per = (chunks + s - 1) / s;
     if (per < chunks) {
       g.k_per = 4 * per;
@@ -356,7 +357,7 @@ int muon_mx_linear(const muon_mx_desc_t* d, const int32_t* offsets, const void* 
   MUON_TRY(check_space(p.bytes(), ws, ws_bytes));
   hipStream_t s = static_cast<hipStream_t>(stream);
   muon::GemmArgs& g = p.p.g;
-  if (!p.few()) {
+  if (!p.own()) {
     muon::MxArgs q{};
     q.src = x;
     q.values = static_cast<uint8_t*>(ws);

@@ -339,16 +339,16 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void k_mx_tile(MxProduct a) {
   else strips(std::true_type{}, std::false_type{});
 }
 
-// Up to 16 FM rows of a group by 16 FN columns, in rounds of kFewWaves chunks: the workgroup takes its rows of x to four
-// bits in LDS while the weight's values of the round are on their way to registers.
-constexpr int kFewWaves = 8;
-template <typename O, int FM, int FN>
-__global__ __launch_bounds__(64 * kFewWaves) void k_mx_rows(MxProduct a) {
-  constexpr int BM = 16 * FM, BN = 16 * FN, STRIDE = BN + 4, NT = 64 * kFewWaves;
-  constexpr int XB = kFewWaves * 4 * BM * kMxSliceBytes, XS = kFewWaves * BM * kMxChunkBytes, SUMS = kFewWaves * BM * STRIDE * 4;
+// Up to 16 FM rows of a group by 16 FN columns, in rounds of WK chunks, one a wave.  A wave's part of the weight goes
+// to its registers at once; further rounds are hidden by other workgroups.  OWN: the workgroup takes its rows of x to four
+// bits itself, in LDS, while the weight is on its way; otherwise they come in four bits, like the weight.
+template <typename O, int FM, int FN, int WK, bool OWN>
+__global__ __launch_bounds__(64 * WK) void k_mx_rows(MxProduct a) {
+  constexpr int BM = 16 * FM, BN = 16 * FN, STRIDE = BN + 4, NT = 64 * WK;
+  constexpr int XB = OWN ? WK * 4 * BM * kMxSliceBytes : 0, XS = OWN ? WK * BM * kMxChunkBytes : 0, SUMS = WK * BM * STRIDE * 4;
   __shared__ __attribute__((aligned(16))) char lds[XB + XS > SUMS ? XB + XS : SUMS];
   const GemmArgs& g = a.g;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int i16 = lane & 15, g4 = lane >> 4;
   Place at;
   if (!at.find(g, BM)) return;
@@ -363,68 +363,72 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_rows(MxProduct a) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{};
-  u32x4_t next[4][FN];
-  uint32_t next_sb[FN];
-  auto fetch = [&](int c) __attribute__((always_inline)) {  // zeros past the last chunk
+  const int value_at = (i16 << 6) + (g4 << 4), scale_at = (i16 << 4) + (g4 << 2);  // of a lane, in 16 rows
+  for (int c0 = 0; c0 < chunks; c0 += WK) {
+    const int c = c0 + wave;  // zeros past the last chunk
+    u32x4_t bf[4][FN], af[OWN ? 1 : 4][FM];
+    uint32_t sb[FN], sa[FM];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int h = 4 * c + s;
       const __amdgpu_buffer_rsrc_t rb = descriptor(B + (int64_t)h * g.n * kMxSliceBytes, h < steps ? rows_b * kMxSliceBytes : 0);
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        next[s][j] = __builtin_amdgcn_raw_buffer_load_b128(rb, ((16 * j + i16) << 6) + (g4 << 4), 0, 0);
+      for (int j = 0; j < FN; ++j) bf[s][j] = __builtin_amdgcn_raw_buffer_load_b128(rb, value_at + j * 1024, 0, 0);
+      if constexpr (!OWN) {
+        const __amdgpu_buffer_rsrc_t ra = descriptor(static_cast<const uint8_t*>(g.a) + ((int64_t)h * g.m + at.row0) * kMxSliceBytes,
+                                                     h < steps ? rows_a * kMxSliceBytes : 0);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) af[s][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, value_at + i * 1024, 0, 0);
+      }
     }
     const __amdgpu_buffer_rsrc_t rs = descriptor(SC + (int64_t)c * g.n * kMxChunkBytes, c < chunks ? rows_b * kMxChunkBytes : 0);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) next_sb[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, ((16 * j + i16) << 4) + (g4 << 2), 0, 0);
-  };
-  fetch(wave);
-  for (int c0 = 0; c0 < chunks; c0 += kFewWaves) {
-    // x: a thread takes eight values of a row at a time, four lanes a block; rows past the last one are never read back
-    // into a row of C.
-    const int pieces = min(kFewWaves, chunks - c0) * 64;
-    for (int u = tid; u < rows_a * pieces; u += NT) {
-      const int r = u / pieces, p = u - r * pieces;
-      const int64_t k = (int64_t)c0 * kMxChunk + p * 8;
-      float v[8];
-      load8(static_cast<const O*>(a.x) + (at.row0 + r) * a.ldx + k, (int)max((int64_t)0, min((int64_t)8, a.kx - k)), v);
-      uint32_t m = 0;
+    for (int j = 0; j < FN; ++j) sb[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, scale_at + j * 256, 0, 0);
+    if constexpr (!OWN) {
+      const __amdgpu_buffer_rsrc_t ra = descriptor(a.sca + ((int64_t)c * g.m + at.row0) * kMxChunkBytes,
+                                                   c < chunks ? rows_a * kMxChunkBytes : 0);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m = max(m, magnitude(v[q]));
-      m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));
-      m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));
-      const int scale = scale_of(m);
-      *reinterpret_cast<uint32_t*>(lds + ((p >> 4) * BM + r) * kMxSliceBytes + (p & 15) * 4) = pack8(v, scale);
-      if ((p & 3) == 0)
-        lds[XB + ((p >> 6) * BM + r) * kMxChunkBytes + 4 * ((p >> 2) & 3) + ((p >> 4) & 3)] = (char)scale;
+      for (int i = 0; i < FM; ++i) sa[i] = __builtin_amdgcn_raw_buffer_load_b32(ra, scale_at + i * 256, 0, 0);
     }
-    __syncthreads();
-    u32x4_t bf[4][FN];
-    uint32_t sb[FN];
+    __builtin_amdgcn_sched_barrier(0);  // all of them are on their way before the first is waited for
+    if constexpr (OWN) {
+      // A thread takes eight values of a row at a time, four lanes a block; what LDS holds past the last row never gets
+      // into a row of C.
+      const int pieces = min(WK, chunks - c0) * 64;
+      for (int u = tid; u < rows_a * pieces; u += NT) {
+        const int r = u / pieces, p = u - r * pieces;
+        const int64_t k = (int64_t)c0 * kMxChunk + p * 8;
+        float v[8];
+        load8(static_cast<const O*>(a.x) + (at.row0 + r) * a.ldx + k, (int)max((int64_t)0, min((int64_t)8, a.kx - k)), v);
+        uint32_t m = 0;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) bf[s][j] = next[s][j];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) sb[j] = next_sb[j];
-    if (c0 + kFewWaves < chunks) fetch(c0 + kFewWaves + wave);
-    if (c0 + wave < chunks) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const uint32_t sa = *reinterpret_cast<const uint32_t*>(lds + XB + (wave * BM + 16 * i + i16) * kMxChunkBytes + 4 * g4);
-        auto slice = [&](auto tag) __attribute__((always_inline)) {
-          constexpr int S = decltype(tag)::value;
-          const u32x4_t af = *reinterpret_cast<const u32x4_t*>(lds + ((4 * wave + S) * BM + 16 * i + i16) * kMxSliceBytes + 16 * g4);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = multiply4<S>(bf[S][j], af, acc[i][j], sb[j], sa);
-        };
-        slice(std::integral_constant<int, 0>{});
-        slice(std::integral_constant<int, 1>{});
-        slice(std::integral_constant<int, 2>{});
-        slice(std::integral_constant<int, 3>{});
+        for (int q = 0; q < 8; ++q) m = max(m, magnitude(v[q]));
+        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));
+        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));
+        const int scale = scale_of(m);
+        *reinterpret_cast<uint32_t*>(lds + ((p >> 4) * BM + r) * kMxSliceBytes + (p & 15) * 4) = pack8(v, scale);
+        if ((p & 3) == 0)
+          lds[XB + ((p >> 6) * BM + r) * kMxChunkBytes + 4 * ((p >> 2) & 3) + ((p >> 4) & 3)] = (char)scale;
       }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        sa[i] = *reinterpret_cast<const uint32_t*>(lds + XB + (wave * BM + 16 * i) * kMxChunkBytes + scale_at);
     }
-    __syncthreads();
+    if (c < chunks) {
+      counted<4>([&](auto tag) __attribute__((always_inline)) {
+        constexpr int S = decltype(tag)::value;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          u32x4_t av;
+          if constexpr (OWN) av = *reinterpret_cast<const u32x4_t*>(lds + ((4 * wave + S) * BM + 16 * i) * kMxSliceBytes + value_at);
+          else av = af[S][i];
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = multiply4<S>(bf[S][j], av, acc[i][j], sb[j], sa[i]);
+        }
+      });
+    }
+    if constexpr (OWN) __syncthreads();
   }
   float* const sums = reinterpret_cast<float*>(lds);
 #pragma unroll
@@ -433,38 +437,45 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_rows(MxProduct a) {
     for (int j = 0; j < FN; ++j)
       *reinterpret_cast<f32x4_t*>(sums + (wave * BM + 16 * i + i16) * STRIDE + 16 * j + 4 * g4) = acc[i][j];
   __syncthreads();
-  if (tid >= BM * BN / 8) return;
-  const int lr = tid / (BN / 8), c8 = tid % (BN / 8) * 8, col = (int)col0 + c8;
-  const int n = (int)min((int64_t)8, g.n - col);
-  if (lr >= rows_a || n <= 0) return;
-  float v[8] = {}, bias[8] = {};
+  for (int u = tid; u < BM * BN / 8; u += NT) {
+    const int lr = u / (BN / 8), c8 = u % (BN / 8) * 8, col = (int)col0 + c8;
+    const int n = (int)min((int64_t)8, g.n - col);
+    if (lr >= rows_a || n <= 0) continue;
+    float v[8] = {}, bias[8] = {};
 #pragma unroll
-  for (int w = 0; w < kFewWaves; ++w)
+    for (int w = 0; w < WK; ++w)
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] += sums[(w * BM + lr) * STRIDE + c8 + u];
-  bias8<O>(g, at, col, n, bias);
-  finish8<O>(g, v, bias, 0, at.row0 + lr, col, n);
+      for (int q = 0; q < 8; ++q) v[q] += sums[(w * BM + lr) * STRIDE + c8 + q];
+    bias8<O>(g, at, col, n, bias);
+    finish8<O>(g, v, bias, 0, at.row0 + lr, col, n);
+  }
+}
+
+// Eight waves where the contraction has a chunk for each, else four.
+template <typename O, int FM, int FN, bool OWN>
+void launch_waves(const MxProduct& a, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.g.tiles_m * a.g.tiles_n));
+  if (a.g.k > 16) hipLaunchKernelGGL((k_mx_rows<O, FM, FN, 8, OWN>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((k_mx_rows<O, FM, FN, 4, OWN>), grid, dim3(256), 0, s, a);
+}
+template <typename O, int FM, bool OWN>
+void launch_rows(const MxProduct& a, int cols, hipStream_t s) {
+  if (cols == 64) launch_waves<O, FM, 4, OWN>(a, s);
+  else if (cols == 32) launch_waves<O, FM, 2, OWN>(a, s);
+  else launch_waves<O, FM, 1, OWN>(a, s);
 }
 
 template <typename O>
 hipError_t launch(const MxProduct& a, int tile, int cols, hipStream_t s) {
   const int64_t blocks = (int64_t)a.g.tiles_m * a.g.tiles_n * a.g.splits;
   if (blocks <= 0) return hipSuccess;
-  const dim3 grid((unsigned)blocks), few(64 * kFewWaves);
-  switch (tile) {
-    case kMx256x128: hipLaunchKernelGGL((k_mx_tile<O, 256, 128, 2, 2, 3>), grid, dim3(256), 0, s, a); break;
-    case kMx128: hipLaunchKernelGGL((k_mx_tile<O, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, a); break;
-    case kMx64: hipLaunchKernelGGL((k_mx_tile<O, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, a); break;
-    case kMxRows32:
-      if (cols == 64) hipLaunchKernelGGL((k_mx_rows<O, 2, 4>), grid, few, 0, s, a);
-      else if (cols == 32) hipLaunchKernelGGL((k_mx_rows<O, 2, 2>), grid, few, 0, s, a);
-      else hipLaunchKernelGGL((k_mx_rows<O, 2, 1>), grid, few, 0, s, a);
-      break;
-    default:
-      if (cols == 64) hipLaunchKernelGGL((k_mx_rows<O, 1, 4>), grid, few, 0, s, a);
-      else if (cols == 32) hipLaunchKernelGGL((k_mx_rows<O, 1, 2>), grid, few, 0, s, a);
-      else hipLaunchKernelGGL((k_mx_rows<O, 1, 1>), grid, few, 0, s, a);
-  }
+  const dim3 grid((unsigned)blocks);
+  if (tile == kMx256x128) hipLaunchKernelGGL((k_mx_tile<O, 256, 128, 2, 2, 3>), grid, dim3(256), 0, s, a);
+  else if (tile == kMx128) hipLaunchKernelGGL((k_mx_tile<O, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, a);
+  else if (tile == kMx64) hipLaunchKernelGGL((k_mx_tile<O, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, a);
+  else if (tile == kMxRows32) launch_rows<O, 2, false>(a, cols, s);
+  else if (tile == kMxRows16) launch_rows<O, 1, false>(a, cols, s);
+  else launch_rows<O, 1, true>(a, cols, s);
   return hipGetLastError();
 }
 

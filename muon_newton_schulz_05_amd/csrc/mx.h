@@ -35,12 +35,12 @@ struct MxProduct {
   GemmArgs g;
   const uint8_t* sca;    // scales of A
   const uint8_t* scb;
-  const void* x;         // kMxRows16 and kMxRows32: A itself, taken to four bits on the way
+  const void* x;         // kMxRowsOwn: A itself, taken to four bits on the way
   int64_t ldx, kx;
 };
-enum MxTile { kMx256x128 = 0, kMx128, kMx64, kMxRows32, kMxRows16 };
+enum MxTile { kMx256x128 = 0, kMx128, kMx64, kMxRows32, kMxRows16, kMxRowsOwn };
 inline int mx_tile_m(int tile) {
-  constexpr int rows[] = {256, 128, 64, 32, 16};
+  constexpr int rows[] = {256, 128, 64, 32, 16, 16};
   return rows[tile];
 }
 // Columns of a workgroup: fixed for the tiles in LDS; for few rows, as few as it takes to occupy every compute unit.
