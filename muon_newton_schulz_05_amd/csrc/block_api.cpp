@@ -124,8 +124,20 @@ muon::MxArgs mx_args(const muon_mx_desc_t* d) {
   a.t = d->w_layout == 0;
   return a;
 }
+// A layer's product: its tile and split, and what it takes of the workspace.  Times in us, bf16, of a whole call:
+//  - Up to 4 rows (on average, of experts) the product takes x to four bits itself, where a launch ahead of it costs
+//    more than doing so in every workgroup.  x [4096, 16384]: 1 row 9.6 and 13.1, 4 rows 10.9 and 13.2, 8 rows 13.1 and
+//    13.5, 16 rows 17.0 and 13.4.
+//  - Up to 32 rows, or 16 an expert, the weight goes straight to registers (16 x 4096 x 16384: 14); from 64 on
+//    64 x 64 tiles are faster (64 x 4096 x 16384: 13.5 and 17.6; 64 experts [2048, 1408] with 32 rows each: 32 and 40).
+//  - 64 x 64 below 256 tiles of 128 x 128 (128 x 4096 x 16384: 16.5 and 32), and for up to 32 rows an expert.
+//  - 128 x 128 below 256 rows (64 experts with 128 each: 48 and 53) or 256 tiles of 256 x 128 (256 x 4096 x 16384: 18.7 and 45;
+//    1024 x 4096 x 4096: 19 and 38).
+//  - 256 x 128 above (8192 x 4096 x 16384: 325, with 128 x 128 373, with 64 x 64 461; 2048 x 4096 x 4096: 30 and 29).
+//    256 x 256 with one workgroup a unit was 4 - 7% faster without an activation or a residual and 4 - 8% slower with
+//    both, whose work nothing hides then.
+// Tiles that do not fill the card are split along the contraction, two chunks of 512 each at least.
 constexpr int64_t kMxOwnRows = 4;
-// A layer's product: its tile and split, and what it takes of the workspace.
 struct MxPlan {
   muon::MxProduct p{};
   int tile = 0, cols = 0;
@@ -148,9 +160,10 @@ MxPlan mx_plan(const muon_mx_desc_t* d) {
   auto blocks_m = [&](int tile) { return muon::group_blocks(d->rows, d->groups, grouped, muon::mx_tile_m(tile)); };
   auto tiles = [&](int tile) { return blocks_m(tile) * ((d->n + muon::mx_tile_n(tile, 0, 0) - 1) / muon::mx_tile_n(tile, 0, 0)); };
   const int64_t m_each = grouped ? d->rows / d->groups : d->rows;
-  if (m_each <= 32) q.tile = m_each <= kMxOwnRows ? muon::kMxRowsOwn : m_each <= 16 ? muon::kMxRows16 : muon::kMxRows32;
+  if (m_each <= (grouped ? 16 : 32))
+    q.tile = m_each <= kMxOwnRows ? muon::kMxRowsOwn : m_each <= 16 ? muon::kMxRows16 : muon::kMxRows32;
   else if (m_each >= 256 && tiles(muon::kMx256x128) >= kCus) q.tile = muon::kMx256x128;
-  else if (tiles(muon::kMx128) >= kCus) q.tile = muon::kMx128;
+  else if (m_each > 32 && tiles(muon::kMx128) >= kCus) q.tile = muon::kMx128;
   else q.tile = muon::kMx64;
   q.cols = muon::mx_tile_n(q.tile, blocks_m(q.tile), d->n);
   g.tiles_m = (int32_t)blocks_m(q.tile);

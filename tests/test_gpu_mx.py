@@ -266,3 +266,40 @@ def test_past_32_bit_offsets(muon):
     at = torch.tensor([0, 65535, 65536, rows - 1], device="cuda")
     want = (muon.mx_dequantize(muon.mx_quantize(x[at].t())).t().double() @ muon.mx_dequantize(q).double())
     assert ((y[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-4).all()
+
+
+@both
+@pytest.mark.parametrize("k", [70, 2600])
+@pytest.mark.parametrize("counts", [[3, 0, 9, 1], [10, 3, 20, 0, 17], [40, 9, 16]], ids=str)
+def test_experts_of_few_rows(muon, counts, k, dtype):
+    """Rows that are taken to four bits by the product or ahead of it, short and long contractions, columns of each width."""
+    e = len(counts)
+    offsets = torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    for n in (24, 1030):
+        x, w = normal((int(offsets[-1]) + 2, k), dtype, 1), normal((e, k, n), dtype, 2, k ** -0.5)
+        y = muon.mx_expert_linear(x.cuda(), muon.mx_quantize(w.cuda()), offsets.cuda())
+        for i in range(e):
+            lo, hi = offsets[i], offsets[i + 1]
+            xq, wq = ref.fast_blocks64(x[lo:hi]).to(dtype), ref.fast_blocks64(w[i].t()).t().to(dtype)
+            ops_reference.check(i, y[lo:hi], ops_reference.linear64(xq, wq, None, None, None, "none")["y"])
+        assert torch.equal(y[-2:].cpu(), torch.zeros(2, n, dtype=dtype))
+
+
+@both
+@pytest.mark.parametrize("m", [4, 5, 16, 17, 32, 33])
+def test_rows_at_the_borders_of_the_rules(muon, m, dtype):
+    """Neighbouring row counts take different kernels: each row's result is the same sum in another order."""
+    x, w = normal((40, 1100), dtype, 1), normal((1100, 96), dtype, 2, 0.03)
+    q = muon.mx_quantize(w.cuda())
+    xq, wq = ref.fast_blocks64(x[:m]).to(dtype), ref.fast_blocks64(w.t()).t().to(dtype)
+    ops_reference.check("y", muon.mx_linear(x[:m].cuda(), q), ops_reference.linear64(xq, wq, None, None, None, "none")["y"])
+
+
+def test_offsets_that_do_not_ascend_stay_in_bounds(muon):
+    """Offsets against the rules give unspecified values, and read and write nothing outside the tensors."""
+    x, q = normal((700, 200), BF16, 1).cuda(), muon.mx_quantize(normal((3, 200, 72), BF16, 2).cuda())
+    for rows in (8, 40, 700):
+        for off in ([0, 600, 100, 700], [5, 5, 5, 5], [0, -9, 1 << 30, 4], [0, 700, 700, 0]):
+            y = muon.mx_expert_linear(x[:rows], q, torch.tensor(off, dtype=torch.int32).cuda())
+            torch.cuda.synchronize()
+            assert y.shape == (rows, 72)
