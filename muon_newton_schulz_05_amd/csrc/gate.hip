@@ -12,6 +12,11 @@
 //    probabilities in registers, workgroups leave partial sums, the join adds them in order.  c_e are integer
 //    counts, exact in any order, so LDS atomics may make them.  dz_te = dloss E / T p_te (f_e - sum_i p_ti f_i).
 //
+// The logits are a few megabytes, and what bounds the kernels is the work between loads: per choice a maximum in the lane, log2 L
+// steps between lanes and the taking out of the key, per logit one exponential.  In us: gate 16384 x 64, top 8, bf16 5.9,
+// its gradient 4.8; 65536 x 256 35 and 21; balance loss of 65536 x 256, bf16, 17 and 6 - 9 for the join (one workgroup,
+// 512 KiB of sums), its gradient 23 (2.9 TB/s); 64 x 64 4 each.
+//
 // A masked token takes no part in anything, whatever its logits hold.  Logits of -inf are experts that cannot be
 // chosen: their probability is zero, and a row of nothing else has no choice and no probabilities.
 #include <algorithm>

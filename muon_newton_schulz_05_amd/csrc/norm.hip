@@ -13,6 +13,10 @@
 // The gradient of w and b is a sum over rows: each thread adds up its columns over the rows that its
 // workgroup walks, workgroups leave one row of partial sums each, and a second
 // kernel adds those in order.
+//
+// Bound by memory.  16384 x 4096 bf16 with a residual: forward 93 - 105 us (5.1 - 5.8 TB/s over its four tensors),
+// gradient 134 - 139 and 5 for the join (4.9 TB/s over five); a row of 4096 alone 3.6 us.  The gradient
+// without the next row's loads in flight took 172 us.
 #include "act.h"
 #include "group.h"
 #include "norm.h"
@@ -203,7 +207,8 @@ __device__ __forceinline__ void load_sum(const A& a, int64_t row, int64_t col, i
   for (int i = 0; i < 8; ++i) v[i] += r[i];
 }
 
-// Rows longer than the registers of a workgroup hold: read three times.
+// Rows longer than the registers of a workgroup hold: read three times (4096 x 16384 bf16, gradient: 233 us, 2.3 TB/s
+// over what it has to read once).
 constexpr int kWide = 1024, kWideCols = 16384, kWideGradCols = 8192;
 constexpr int64_t kWideGrid = 1 << 20;  // a launch holds fewer than 2^32 threads
 
