@@ -31,8 +31,14 @@ void* stream_of(const Tensor& t) {
 }
 int32_t dtype_of(const Tensor& t) { return t.scalar_type() == at::kBFloat16 ? MUON_BF16 : MUON_F32; }
 
+// A transform's wrapper (functionalization's, a fake tensor) has no memory: a view's place in it would be an address.
+void check_memory(const Tensor& t) {
+  TORCH_CHECK(t.numel() == 0 || t.storage().data(),
+              "a tensor has no memory: these operators cannot run under tracers and transforms");
+}
 // t as [rows, cols] with contiguous rows.
 Tensor flat(const Tensor& t, int64_t cols) {
+  check_memory(t);
   Tensor r = t;
   if (t.dim() != 2) {
     int64_t rows = 1;
@@ -43,8 +49,16 @@ Tensor flat(const Tensor& t, int64_t cols) {
 }
 int64_t ld(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : std::max<int64_t>(t.size(1), 1); }
 Tensor whole(const OptTensor& t) { return t && t->defined() ? t->contiguous() : Tensor(); }
-const void* at_of(const Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
-void* out_of(const Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; }
+const void* at_of(const Tensor& t) {
+  if (!t.defined()) return nullptr;
+  check_memory(t);
+  return t.const_data_ptr();
+}
+void* out_of(const Tensor& t) {
+  if (!t.defined()) return nullptr;
+  check_memory(t);
+  return t.mutable_data_ptr();
+}
 Tensor space(uint64_t bytes, const Tensor& like) {
   return bytes ? at::empty({(int64_t)bytes}, like.options().dtype(at::kByte)) : Tensor();
 }

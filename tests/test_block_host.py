@@ -312,6 +312,15 @@ def test_tracing_is_refused(on_cpu, name, how):
             lambda x: calls(x)[name](), (x,)))(x)
 
 
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("transform", [torch.func.functionalize, torch.func.vmap])
+def test_tensors_without_memory_are_refused(on_cpu, name, transform):
+    """A view inside functionalization reports its place in a storage of nothing as an address."""
+    x = torch.randn(*(() if transform is torch.func.functionalize else (2,)), 4, 8)
+    with torch.no_grad(), pytest.raises(RuntimeError, match="no memory|torage"):
+        transform(lambda t: calls(t[1:])[name]())(x)
+
+
 def test_four_bits_refuse_a_gradient(on_cpu, mx, monkeypatch):
     stand_in(on_cpu, mx, monkeypatch)
     x = torch.randn(3, 8, requires_grad=True)
