@@ -96,7 +96,8 @@ int muon_balance_backward(const muon_gate_desc_t* desc, const void* logits, cons
                           const float* dloss, void* dlogits, void* stream);
 
 /* A weight [k, n], or `groups` of them w_stride elements apart, held in four
- * bits along k.  k and n up to 2^23. */
+ * bits along k.  k and n up to 2^23; groups n k and rows k, with k in steps of 512, n at least 4 and rows in steps of 4,
+ * below 2^35. */
 typedef struct {
   int32_t dtype;     /* of the weight; of x, bias, residual and y */
   int32_t act;       /* muon_act_t                                */

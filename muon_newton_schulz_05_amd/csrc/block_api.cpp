@@ -320,7 +320,7 @@ int muon_mx_quantize(const muon_mx_desc_t* d, const void* w, uint8_t* values, ui
   MUON_TRY(check_mx(d));
   MUON_TRY(check_at(w, d->k * d->n, elem(d->dtype), "w"));
   MUON_TRY(check_mx_weight(d, values, scales));
-  if (!muon::mx_rows_fit(mx_weights(d) * d->n, d->k)) return bad("groups * n * k (k in steps of 512) is over 2^35");
+  if (!muon::mx_weight_fits(mx_weights(d), d->n, d->k)) return bad("groups * n * k (n at least 4, k in steps of 512) is 2^35 or more");
   muon::MxArgs a = mx_args(d);
   a.src = w;
   a.values = values;
@@ -332,7 +332,7 @@ int muon_mx_dequantize(const muon_mx_desc_t* d, const uint8_t* values, const uin
   MUON_TRY(check_mx(d));
   MUON_TRY(check_mx_weight(d, values, scales));
   MUON_TRY(check_at(w, d->k * d->n, elem(d->dtype), "w"));
-  if (!muon::mx_rows_fit(mx_weights(d) * d->n, d->k)) return bad("groups * n * k (k in steps of 512) is over 2^35");
+  if (!muon::mx_weight_fits(mx_weights(d), d->n, d->k)) return bad("groups * n * k (n at least 4, k in steps of 512) is 2^35 or more");
   muon::MxArgs a = mx_args(d);
   a.values = const_cast<uint8_t*>(values);
   a.scales = const_cast<uint8_t*>(scales);
@@ -364,7 +364,7 @@ int muon_mx_linear(const muon_mx_desc_t* d, const int32_t* offsets, const void* 
   MUON_TRY(check_at(y, d->rows * d->n, es, "y"));
   if (d->groups > 0 && residual) return bad("a grouped layer takes no residual");
   if (d->rows == 0 || d->n == 0) return set_error(MUON_OK, "%s", "");
-  if (!muon::mx_rows_fit(d->rows, d->k)) return bad("rows * k (k in steps of 512) is over 2^35");
+  if (!muon::mx_rows_fit(d->rows, d->k)) return bad("rows * k (k in steps of 512) is 2^35 or more");
   MxPlan p = mx_plan(d);
   if ((int64_t)p.p.g.tiles_m * p.p.g.tiles_n * p.p.g.splits > 0x7fffff) return bad("rows * n has too many tiles for a launch");
   MUON_TRY(check_space(p.bytes(), ws, ws_bytes));

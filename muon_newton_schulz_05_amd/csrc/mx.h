@@ -26,6 +26,8 @@ struct MxArgs {
 // Workgroups of the kernels over rows, and whether one launch holds them (2^32 threads).
 inline int64_t mx_row_blocks(int64_t rows, int64_t k) { return (rows + 3) / 4 * mx_chunks(k); }
 inline bool mx_rows_fit(int64_t rows, int64_t k) { return mx_row_blocks(rows, k) < (int64_t(1) << 24); }
+// A weight's: with at least four rows a group, since the kernel across memory takes one group a workgroup.
+inline bool mx_weight_fits(int64_t groups, int64_t n, int64_t k) { return mx_rows_fit(groups * (n > 4 ? n : 4), k); }
 hipError_t launch_mx_quantize(const MxArgs& a, int dtype, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxArgs& a, int dtype, hipStream_t s);
 

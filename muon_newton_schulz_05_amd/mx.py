@@ -52,7 +52,7 @@ def mx_quantize(weight):
 
     A block's scale is 2^(floor(log2 of its largest magnitude) - 2), at least 2^-127; values are rounded
     to nearest, ties to even, and saturate at 6 scales.  A block with an infinity or NaN becomes NaN.  Takes the weight's
-    value: a parameter that requires a gradient may be given."""
+    value: a parameter that requires a gradient may be given.  K and N up to 2^23, fewer than 2^35 values in all."""
     _gpu(weight, "weight")
     _dtype(weight, "weight")
     if weight.dim() not in (2, 3):

@@ -248,6 +248,16 @@ def test_sizes_without_anything_to_do_launch_nothing(block):
     assert lib.muon_mx_linear(ctypes.byref(mx_desc(block, rows=0)), None, None, A, A, None, None, None, None, 0, None) == 0
 
 
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("groups, k, n", [(65535, 1000 * 512, 1), (1, 1 << 23, 4096), (4096, 1 << 13, 1 << 10)])
+def test_weights_that_no_launch_holds_are_refused(block, groups, k, n, layout):
+    """A launch holds fewer than 2^32 threads; one column of many weights takes a workgroup of 256 for 512 values each."""
+    lib = block.load_block()
+    d = mx_desc(block, groups=groups, k=k, n=n, w_layout=layout)
+    assert lib.muon_mx_quantize(ctypes.byref(d), A, A, A, None) == INVALID
+    assert lib.muon_mx_dequantize(ctypes.byref(d), A, A, A, None) == INVALID
+
+
 def test_mx_sizes(block):
     lib, v, s = block.load_block(), ctypes.c_uint64(0), ctypes.c_uint64(0)
     for groups, k, n in ((0, 1, 1), (0, 32, 5), (0, 33, 5), (2, 257, 3), (0, 0, 4), (7, 4096, 16384)):
