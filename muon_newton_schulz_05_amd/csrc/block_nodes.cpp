@@ -332,6 +332,8 @@ std::tuple<Tensor, Tensor> mx_quantize(const Tensor& weight) {
   const c10::DeviceGuard guard(weight.device());
   const int64_t k = weight.size(-2), n = weight.size(-1), groups = weight.dim() == 3 ? weight.size(0) : 0;
   auto layout = [&](const Tensor& w) {
+    // Strides that reach nothing: torch calls such a view contiguous, and a copy would keep them.
+    if (w.numel() == 0 || (k == 1 && n == 1)) return 0;
     if (w.stride(-1) == 1 && (k <= 1 || w.stride(-2) >= n)) return 0;
     return w.stride(-2) == 1 && (n <= 1 || w.stride(-1) >= k) ? 1 : -1;
   };
