@@ -410,7 +410,8 @@ hipError_t backward(const NormGradArgs& a, hipStream_t s) {
   const int64_t parts = norm_parts(a.rows, a.cols);
   hipError_t e = hipSuccess;
   if (a.cols > kWideGradCols) {
-    if (a.dx) hipLaunchKernelGGL((k_norm_grad_wide<T>), dim3((unsigned)std::min<int64_t>(a.rows, kWideGrid)), dim3(kWide), 0, s, a);
+    if (a.dx && a.rows > 0)
+      hipLaunchKernelGGL((k_norm_grad_wide<T>), dim3((unsigned)std::min<int64_t>(a.rows, kWideGrid)), dim3(kWide), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.part && parts > 0)
       hipLaunchKernelGGL((k_norm_cols<T>), dim3((unsigned)((a.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s, a,
@@ -441,7 +442,7 @@ hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s) {
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, int dtype, hipStream_t s) {
-  if (a.cols == 0) return hipSuccess;
+  if (a.cols == 0 || (a.rows == 0 && !a.dw && !a.db)) return hipSuccess;  // of no rows dw and db are zero
   return dtype == MUON_BF16 ? backward<uint16_t>(a, s) : backward<float>(a, s);
 }
 

@@ -2,10 +2,12 @@
 
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 import torch
 
-from test_gpu_mx import both, muon, normal  # noqa: F401 (muon is a fixture)
+from test_gpu_mx import BF16, NAN, both, muon, normal  # noqa: F401 (muon is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +27,23 @@ def test_quantize_views_whose_strides_do_not_count(muon, dtype):  # noqa: F811
         assert q.shape == v.shape and q.k == want.k
         assert torch.equal(q.values, want.values) and torch.equal(q.scales, want.scales)
         assert muon.mx_dequantize(q).shape == v.shape
+
+
+# ------------------------------------------------------------------ norms
+
+
+@both
+@pytest.mark.parametrize("cols", [8, 8192, 9000])
+def test_a_norm_gradient_of_no_rows_by_the_c_abi(muon, cols, dtype):  # noqa: F811
+    """dw and db are sums of nothing, and dx, which has an address and no elements, is left alone."""
+    from muon_newton_schulz_05_amd import block
+    lib = block.load_block()
+    d = block.NormDesc(muon.MUON_BF16 if dtype is BF16 else muon.MUON_F32, 0, 0, cols, cols, cols, cols, cols, 1e-5)
+    need = ctypes.c_uint64(0)
+    assert lib.muon_norm_workspace(ctypes.byref(d), ctypes.byref(need)) == 0
+    dx, dw, db = (torch.full((cols,), NAN, dtype=dtype, device="cuda") for _ in range(3))
+    ws = torch.empty(need.value + 16, dtype=torch.uint8, device="cuda")
+    rc = lib.muon_norm_backward(ctypes.byref(d), None, None, None, None, None, None, dx.data_ptr(), dw.data_ptr(),
+                                db.data_ptr(), ws.data_ptr(), need.value, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and dx.isnan().all() and not dw.any() and not db.any()
