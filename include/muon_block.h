@@ -86,7 +86,7 @@ int muon_balance_workspace(const muon_gate_desc_t* desc, uint64_t* bytes);
  * tokens of softmax(logits)_e, T the number of tokens that the mask leaves.  Ids
  * outside [0, experts) are not counted; a row of -inf alone has no probabilities.  T = 0 gives 0.
  * counts [experts]: c_e.  shares [experts + 1] float32: what the gradient needs.
- * tokens top < 2^31. */
+ * tokens top up to 2^31 - 1024. */
 int muon_balance_forward(const muon_gate_desc_t* desc, const void* logits, const void* ids, int32_t ids_bytes,
                          const uint8_t* mask, float* loss, int32_t* counts, float* shares, void* workspace,
                          uint64_t workspace_bytes, void* stream);

@@ -25,6 +25,7 @@ from torch.autograd import forward_ad
 from .ops import _dtype, _gpu, _same, _traced, _tracked, load_ops
 
 GATE_MAX_EXPERTS = 1024
+BALANCE_MAX_ENTRIES = (1 << 31) - 1024  # counts are held in 32 bits
 NORMS = {"layer": 0, "rms": 1}
 EXPORTED_BLOCK = ("muon_norm_workspace", "muon_norm_forward", "muon_norm_backward", "muon_gate_forward",
                   "muon_gate_backward", "muon_balance_workspace", "muon_balance_forward", "muon_balance_backward",
@@ -269,6 +270,8 @@ def _check_balance(logits, ids, mask):
     _check_logits(logits, mask)
     if ids.dim() != 2 or ids.shape[0] != logits.shape[0] or ids.shape[1] < 1:
         raise ValueError(f"expert_ids has shape {tuple(ids.shape)}, expected ({logits.shape[0]}, top)")
+    if max(ids.shape[0], 1) * ids.shape[1] > BALANCE_MAX_ENTRIES:
+        raise ValueError(f"expert_ids has shape {tuple(ids.shape)}: up to 2^31 - 1024 entries are supported")
     if ids.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"expert_ids is {ids.dtype}: int64 or int32 is supported")
     if ids.device != logits.device:
@@ -298,7 +301,7 @@ def balance_loss(logits, expert_ids, *, mask: Optional[torch.Tensor] = None):
     f_e is the part of all entries of expert_ids [tokens, top] (int64 or int32, as ``gate`` gives them) that
     goes to expert e, P_e the mean over tokens of softmax(logits)_e.  Tokens that mask (bool [tokens]) leaves
     out count nowhere.  An id outside [0, E) (a dropped entry's -1) is not counted, but its place is: f_e is c_e / (T
-    top).  Differentiable in logits, through P."""
+    top).  Up to 2^31 - 1024 entries.  Differentiable in logits, through P."""
     _check_balance(logits, expert_ids, mask)
     _refuse_tangents("balance_loss", logits=logits)
     return Balance(*_nodes("balance_loss").balance(logits, expert_ids, mask, _tracked(logits)))
