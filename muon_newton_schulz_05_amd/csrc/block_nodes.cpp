@@ -204,14 +204,16 @@ Gated gate_run(const Tensor& logits, int64_t top, int64_t normalize, const OptTe
         "muon_gate_forward");
   return o;
 }
-Tensor gate_grad(const Tensor& dweights, const Tensor& z, const Tensor& weights, const Tensor& ids, int64_t normalize,
-                 const Tensor& mask) {
-  const c10::DeviceGuard guard(z.device());
-  const Tensor dw = dweights.contiguous(), dz = at::empty(z.sizes(), z.options());
-  const muon_gate_desc_t d = gate_desc(z, ids.size(1), normalize);
+// z: the logits, or (normalised weights need no more of them) nothing.
+Tensor gate_grad(const Tensor& dweights, const Tensor& z, at::ScalarType dtype, int64_t experts, const Tensor& weights,
+                 const Tensor& ids, int64_t normalize, const Tensor& mask) {
+  const c10::DeviceGuard guard(weights.device());
+  const Tensor dw = dweights.contiguous(), dz = at::empty({ids.size(0), experts}, weights.options().dtype(dtype));
+  muon_gate_desc_t d = gate_desc(dz, ids.size(1), normalize);
+  if (z.defined()) d.ldz = ld(z);
   check(muon_gate_backward(&d, at_of(z), static_cast<const uint8_t*>(at_of(mask)), static_cast<const float*>(at_of(weights)),
                            static_cast<const int32_t*>(at_of(ids)), static_cast<const float*>(at_of(dw)), out_of(dz),
-                           stream_of(z)),
+                           stream_of(weights)),
         "muon_gate_backward");
   return dz;
 }
@@ -220,8 +222,8 @@ struct GateNode : public Function<GateNode> {
   static variable_list forward(AutogradContext* ctx, const Tensor& logits, int64_t top, int64_t normalize,
                                const OptTensor& mask) {
     const Gated o = gate_run(logits, top, normalize, mask);
-    ctx->save_for_backward({o.z, o.weights, o.ids, o.mask});
-    ctx->saved_data["normalize"] = normalize;
+    ctx->save_for_backward({normalize ? Tensor() : o.z, o.weights, o.ids, o.mask});
+    ctx->saved_data["kind"] = normalize | (int64_t)logits.scalar_type() << 1 | logits.size(1) << 16;
     ctx->mark_non_differentiable({o.ids});
     ctx->set_materialize_grads(false);
     return {o.weights, o.ids};
@@ -230,7 +232,8 @@ struct GateNode : public Function<GateNode> {
     variable_list out(4);
     if (grads[0].defined()) {
       const variable_list s = ctx->get_saved_variables();
-      out[0] = gate_grad(grads[0], s[0], s[1], s[2], ctx->saved_data["normalize"].toInt(), s[3]);
+      const int64_t kind = ctx->saved_data["kind"].toInt();
+      out[0] = gate_grad(grads[0], s[0], static_cast<at::ScalarType>(kind >> 1 & 0x7fff), kind >> 16, s[1], s[2], kind & 1, s[3]);
     }
     return once(std::move(out));
   }
@@ -248,7 +251,8 @@ std::tuple<Tensor, Tensor> gate(const Tensor& logits, int64_t top, int64_t norma
 Tensor gate_backward(const Tensor& dweights, const Tensor& logits, const Tensor& weights, const Tensor& ids,
                      int64_t normalize, const OptTensor& mask) {
   const at::NoGradGuard no_grad;
-  return gate_grad(dweights, flat(logits, logits.size(1)), weights, ids, normalize, whole(mask));
+  return gate_grad(dweights, normalize ? Tensor() : flat(logits, logits.size(1)), logits.scalar_type(), logits.size(1), weights,
+                   ids, normalize, whole(mask));
 }
 
 // ------------------------------------------------------------------ balance loss

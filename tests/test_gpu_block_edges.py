@@ -7,7 +7,7 @@ import ctypes
 import pytest
 import torch
 
-from test_gpu_mx import BF16, NAN, both, muon, normal  # noqa: F401 (muon is a fixture)
+from test_gpu_mx import BF16, F32, NAN, both, muon, normal  # noqa: F401 (muon is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,32 @@ def test_a_norm_gradient_of_no_rows_by_the_c_abi(muon, cols, dtype):  # noqa: F8
                                 db.data_ptr(), ws.data_ptr(), need.value, torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert rc == 0 and dx.isnan().all() and not dw.any() and not db.any()
+
+
+# ------------------------------------------------------------------ gate
+
+
+def test_a_normalised_gate_does_not_keep_the_logits(muon):  # noqa: F811
+    """Its gradient does not read them: they may be written to, and their memory comes back, ahead of the backward pass."""
+    for dtype, e, top, normalised in ((F32, 24, 3, True), (BF16, 200, 8, True), (BF16, 24, 5, False)):
+        leaf = normal((500, e), dtype, 1).cuda().requires_grad_()
+        dw = normal((500, top), F32, 2).cuda()
+        mask = (torch.arange(500) % 7 > 0).cuda()
+        want, = torch.autograd.grad(muon.gate(leaf, top, normalize=normalised, mask=mask).weights, leaf, dw)
+        logits = leaf * 1
+        weights = muon.gate(logits, top, normalize=normalised, mask=mask).weights
+        if normalised:
+            with torch.no_grad():
+                logits.zero_()
+        got, = torch.autograd.grad(weights, leaf, dw)
+        assert got.dtype is dtype and torch.equal(got, want)
+        strided = torch.cat([leaf, leaf], 1)[:, :e]              # and rows that are not dense
+        got, = torch.autograd.grad(muon.gate(strided, top, normalize=normalised, mask=mask).weights, leaf, dw)
+        assert torch.equal(got, want)
+    leaf = normal((1 << 14, 512), F32, 3).cuda().requires_grad_()
+    logits = leaf * 1
+    weights = muon.gate(logits, 2).weights
+    before = torch.cuda.memory_allocated()
+    del logits
+    assert before - torch.cuda.memory_allocated() >= leaf.numel() * 4
+    weights.sum().backward()
