@@ -54,23 +54,53 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    if not os.path.exists(HIPCC) and shutil.which("hipcc") is None:
-        raise RuntimeError("hipcc not found")
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
-        nodes, *objs = ex.map(_compile, [NODES_SOURCE, *SOURCES])
-    tmp = LIB + ".tmp"
-    _run("link", [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
+def _no_nodes() -> str | None:
+    """Why _nodes.so cannot be built here, or None.  libmuon.so takes neither torch nor a second compiler."""
+    try:
+        import torch
+        from torch.utils import cpp_extension  # noqa: F401
+    except (ImportError, OSError) as e:
+        return f"torch is not importable ({e})"
+    if torch.version.hip is None:
+        return "torch is not built for ROCm"
+    return None if shutil.which(CXX) else f"{CXX} is not found"
+
+
+def _link_nodes(obj: str) -> None:
     from torch.utils import cpp_extension
     libs = [f"-L{d}" for d in cpp_extension.library_paths()]
     tmp = NODES + ".tmp"
-    _run("link", [CXX, "-shared", "-o", tmp, nodes, *libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
-                  f"-L{PKG}", "-l:libmuon.so", "-Wl,-rpath,$ORIGIN"])
+    _run("link", [CXX, "-shared", "-o", tmp, obj, *libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
+                  f"-L{os.path.dirname(LIB)}", "-l:libmuon.so", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, NODES)
+
+
+def build(verbose: bool = False) -> str:
+    """libmuon.so, and _nodes.so where torch and a C++ compiler are there.  A _nodes.so that is not built raises, where it
+    could have been, once libmuon.so is in place; one of an earlier library does not stay beside it either way."""
+    if not os.path.exists(HIPCC) and shutil.which("hipcc") is None:
+        raise RuntimeError("hipcc not found")
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    without = _no_nodes()
+    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
+        nodes = None if without else ex.submit(_compile, NODES_SOURCE)
+        objs = list(ex.map(_compile, SOURCES))
+        tmp = LIB + ".tmp"
+        _run("link", [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+        built = False
+        try:
+            if nodes:
+                _link_nodes(nodes.result())
+                built = True
+        finally:
+            if not built and os.path.exists(NODES):
+                os.remove(NODES)
+    if without:
+        print(f"_nodes.so is left out: {without}.  The C ABI and the Muon step do not need it; layer_norm, rms_norm, gate, "
+              "balance_loss and the layers in four bits do.", file=sys.stderr)
     if verbose:
-        print(f"built {LIB} and {NODES}")
+        print(f"built {LIB}" + ("" if without else f" and {NODES}"))
     return LIB
 
 
