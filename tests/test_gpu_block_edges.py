@@ -3,10 +3,13 @@
 from __future__ import annotations
 
 import ctypes
+import itertools
 
 import pytest
 import torch
 
+import ops_reference
+from ops_reference import U32
 from test_gpu_mx import BF16, F32, NAN, both, muon, normal  # noqa: F401 (muon is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -27,6 +30,61 @@ def test_quantize_views_whose_strides_do_not_count(muon, dtype):  # noqa: F811
         assert q.shape == v.shape and q.k == want.k
         assert torch.equal(q.values, want.values) and torch.equal(q.scales, want.scales)
         assert muon.mx_dequantize(q).shape == v.shape
+
+
+def plain_linear(muon, x, q, b, r, act):  # noqa: F811
+    """(value, tolerance) in float64 on the GPU; ops_reference's count, with the sums of one contraction."""
+    xq = muon.mx_dequantize(muon.mx_quantize(x.t())).t().double()        # the form is checked bit by bit elsewhere
+    wq = muon.mx_dequantize(q).double()
+    z, size = xq @ wq, xq.abs() @ wq.abs()
+    if b is not None:
+        z, size = z + b.double(), size + b.double().abs()
+    y = ops_reference.act64(z, act)[0]
+    e = 1.2 * (x.shape[1] + 2) * U32 * size + 16 * U32 * z.abs()
+    if r is not None:
+        y = y + r.double()
+        e = e + U32 * y.abs()
+    return y, e + ops_reference.unit(x.dtype) * y.abs() + 1e-37
+
+
+# Tiles of 256 x 128 (the first two), of 128 x 128, and of 64 x 64; whole pieces of eight columns, and ragged ones.
+TILES = [(4100, 600, 4104), (2050, 200, 4099), (2040, 520, 2104), (2033, 130, 2101), (1000, 520, 2000), (130, 400, 333)]
+
+
+@both
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("m,k,n", TILES)
+def test_every_tile_with_activation_bias_and_residual(muon, m, k, n, act, dtype):  # noqa: F811
+    x, w = normal((m, k), dtype, 1, 1.5).cuda(), normal((k, n), dtype, 2, k ** -0.5).cuda()
+    b, r = normal((n,), dtype, 3).cuda(), normal((m, n + 8), dtype, 4).cuda()[:, :n]
+    q = muon.mx_quantize(w)
+    for bias, res in ((b, r), (None, r), (b, None)):
+        y = muon.mx_linear(x, q, bias, activation=act, residual=res)
+        want, tol = plain_linear(muon, x, q, bias, res, act)
+        assert ((y.double() - want).abs() <= tol).all(), (bias is None, res is None)
+
+
+@both
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("n", [2056, 1403])
+def test_experts_of_many_rows_with_activation_and_bias(muon, n, act, dtype):  # noqa: F811
+    """Groups over both large tiles, ragged and empty ones among them, and rows past the last."""
+    counts = [1500, 0, 2100, 900, 3, 1800] if n == 2056 else [300, 500, 0, 129, 700, 450]
+    k, offsets = 300, torch.tensor([0, *itertools.accumulate(counts)], dtype=torch.int32)
+    rows = int(offsets[-1]) + 40
+    x, w, b = normal((rows, k), dtype, 1), normal((len(counts), k, n), dtype, 2, k ** -0.5).cuda(), \
+        normal((len(counts), n), dtype, 3).cuda()
+    x[int(offsets[-1]):] = NAN
+    x = x.cuda()
+    q = muon.mx_quantize(w)
+    y = muon.mx_expert_linear(x, q, offsets.cuda(), b, activation=act)
+    for i in range(len(counts)):
+        lo, hi = offsets[i], offsets[i + 1]
+        if lo == hi:
+            continue
+        want, tol = plain_linear(muon, x[lo:hi], muon.MxWeight(q.values[i], q.scales[i], k), b[i], None, act)
+        assert ((y[lo:hi].double() - want).abs() <= tol).all(), i
+    assert torch.equal(y[int(offsets[-1]):], torch.zeros(40, n, dtype=dtype, device="cuda"))
 
 
 # ------------------------------------------------------------------ norms
