@@ -87,6 +87,58 @@ def test_experts_of_many_rows_with_activation_and_bias(muon, n, act, dtype):  # 
     assert torch.equal(y[int(offsets[-1]):], torch.zeros(40, n, dtype=dtype, device="cuda"))
 
 
+def inside(t, front, back, fill):
+    """A copy of t (1-D bytes) between guards of `fill`: (the whole buffer, the place of t)."""
+    whole = torch.full((front + t.numel() + back,), fill, dtype=torch.uint8, device="cuda")
+    whole[front:front + t.numel()] = t
+    return whole, whole[front:front + t.numel()]
+
+
+def as_bytes(t):
+    return t.contiguous().reshape(-1).view(torch.uint8)
+
+
+GUARD = 1 << 20
+
+
+@both
+@pytest.mark.parametrize("rows,n", [(8, 72), (40, 72), (700, 72), (1500, 1403), (3000, 2056)])
+@pytest.mark.parametrize("share", [None, (0.1, 0.85, 0.14), (0.3, 0.3, 0.3), (-0.01, 1e6, 0.1), (1.0, 1.0, 0.0), (0.0, 0.4, 0.9)], ids=str)
+def test_nothing_outside_the_tensors_is_written_or_used(muon, rows, n, share, dtype):  # noqa: F811
+    """y and the workspace between guards that must stay, x and the weight between NaN that must not come through, for
+    offsets that ascend, that do not, and that leave the tensors.  share: offsets 1 to 3 in rows (None: a plain layer)."""
+    from muon_newton_schulz_05_amd import block
+    lib, k, e = block.load_block(), 200, 3
+    x = normal((rows, k), dtype, 1).cuda()
+    lead = () if share is None else (e,)
+    q = muon.mx_quantize(normal((*lead, k, n), dtype, 2, 0.1).cuda())
+    d = block.MxDesc(muon.MUON_BF16 if dtype is BF16 else muon.MUON_F32, 0, e if lead else 0, 0, rows, k, n, k, 0, 0, 0)
+    need = ctypes.c_uint64(0)
+    assert lib.muon_mx_linear_workspace(ctypes.byref(d), ctypes.byref(need)) == 0
+    offsets = None if share is None else torch.tensor([0, *(max(-2 ** 31, min(2 ** 31 - 1, int(s * rows))) for s in share)],
+                                                      dtype=torch.int32).cuda()
+    y_size = rows * n * x.element_size()
+    # All bits set: NaN as a float, as a bfloat16 and as a scale.
+    xw, xv = inside(as_bytes(x), GUARD, GUARD, 255)
+    vw, vv = inside(as_bytes(q.values), GUARD, GUARD, 255)
+    sw, sv = inside(as_bytes(q.scales), GUARD, GUARD, 255)
+    yw, yv = inside(torch.zeros(y_size, dtype=torch.uint8, device="cuda"), GUARD, GUARD, 90)
+    ww, wv = inside(torch.full((need.value,), 255, dtype=torch.uint8, device="cuda"), GUARD, GUARD, 90)
+    rc = lib.muon_mx_linear(ctypes.byref(d), None if offsets is None else offsets.data_ptr(), xv.data_ptr(), vv.data_ptr(),
+                            sv.data_ptr(), None, None, yv.data_ptr(), wv.data_ptr() if need.value else None, need.value,
+                            torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0
+    for whole in (yw, ww):
+        assert (whole[:GUARD] == 90).all() and (whole[-GUARD:] == 90).all()
+    y = yv.view(dtype).view(rows, n)
+    assert y.isfinite().all()
+    if share is None:
+        assert torch.equal(y, muon.mx_linear(x, q))
+    elif share == (0.0, 0.4, 0.9):
+        assert torch.equal(y, muon.mx_expert_linear(x, q, offsets))
+
+
 # ------------------------------------------------------------------ norms
 
 
