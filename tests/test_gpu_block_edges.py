@@ -186,3 +186,43 @@ def test_a_normalised_gate_does_not_keep_the_logits(muon):  # noqa: F811
     del logits
     assert before - torch.cuda.memory_allocated() >= leaf.numel() * 4
     weights.sum().backward()
+
+
+# ------------------------------------------------------------------ capture
+
+
+def test_captured_autograd_over_inputs_that_change(muon):  # noqa: F811
+    """Each replay, its outputs spoilt and its inputs renewed beforehand, gives an eager pass's bits on the same values."""
+    shapes = {"x": (64, 200), "w": (200,), "b": (200,), "r": (64, 200), "router": (200, 16)}
+    leaves = {name: normal(s, F32, i).cuda().requires_grad_() for i, (name, s) in enumerate(shapes.items())}
+    dw, dloss, ds = normal((64, 4), F32, 9).cuda(), torch.tensor(0.3, device="cuda"), normal((64, 200), F32, 10).cuda()
+
+    def step(p):
+        y, s = muon.layer_norm(p["x"], p["w"], p["b"], residual=p["r"])
+        z = muon.linear(muon.rms_norm(y, p["w"]), p["router"])
+        dense, ids = muon.gate(z, 4, normalize=False)
+        even = muon.gate(z, 4).weights
+        loss, counts = muon.balance_loss(z, ids)
+        grads = torch.autograd.grad((dense, even, loss, s), tuple(p.values()), (dw, dw, dloss, ds))
+        return [*grads, dense.detach(), even.detach(), ids, loss.detach(), counts, s.detach()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(leaves)
+    for replay in range(4):
+        with torch.no_grad():
+            for i, t in enumerate(leaves.values()):
+                t.copy_(normal(t.shape, F32, 100 * replay + i + 20))
+            for t in out:
+                t.fill_(NAN) if t.dtype.is_floating_point else t.fill_(-7)
+        want = step({name: t.detach().clone().requires_grad_() for name, t in leaves.items()})
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(out, want)):
+            assert torch.equal(a, b), (replay, i)
