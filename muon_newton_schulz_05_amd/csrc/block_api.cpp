@@ -124,16 +124,19 @@ muon::MxArgs mx_args(const muon_mx_desc_t* d) {
   a.t = d->w_layout == 0;
   return a;
 }
-// A layer's product: its tile and split, and what it takes of the workspace.  Times in us, bf16, of a whole call:
+// A layer's product: its tile and split, and what it takes of the workspace.  Times in us, bf16, of a whole
+// call without bias, activation or residual, the weights from HBM; each pair is the kernel named first and the other:
 //  - Up to 4 rows (on average, of experts) the product takes x to four bits itself, where a launch ahead of it costs
-//    more than doing so in every workgroup.  x [4096, 16384]: 1 row 9.6 and 13.1, 4 rows 10.9 and 13.2, 8 rows 13.1 and
-//    13.5, 16 rows 17.0 and 13.4.
-//  - Up to 32 rows, or 16 an expert, the weight goes straight to registers (16 x 4096 x 16384: 14); from 64 on
-//    64 x 64 tiles are faster (64 x 4096 x 16384: 13.5 and 17.6; 64 experts [2048, 1408] with 32 rows each: 32 and 40).
-//  - 64 x 64 below 256 tiles of 128 x 128 (128 x 4096 x 16384: 16.5 and 32), and for up to 32 rows an expert.
-//  - 128 x 128 below 256 rows (64 experts with 128 each: 48 and 53) or 256 tiles of 256 x 128 (256 x 4096 x 16384: 18.7 and 45;
-//    1024 x 4096 x 4096: 19 and 38).
-//  - 256 x 128 above (8192 x 4096 x 16384: 325, with 128 x 128 373, with 64 x 64 461; 2048 x 4096 x 4096: 30 and 29).
+//    more than doing so in every workgroup.  x [4096, 16384]: 1 row 9.4 and 11.9, 4 rows 10.7 and 11.7, 5 rows 11.2 and 11.9,
+//    8 rows 13.3 and 11.7, 16 rows 18.7 and 12.1.
+//  - Up to 32 rows, or 16 an expert, the weight goes straight to registers (32 x 4096 x 16384: 12.8 and 13.4); from 64 on
+//    64 x 64 tiles are faster (64 x 4096 x 16384: 13.8 and 17.7; 64 experts [2048, 1408] with 32 rows each: 31 and 35, with 16
+//    each 28 either way).
+//  - 64 x 64 below 256 tiles of 128 x 128 (128 x 4096 x 16384: 16.8 and 30.6), and for up to 32 rows an expert.
+//  - 128 x 128 below 256 rows (64 experts with 128 each: 44 and 53) or 256 tiles of 256 x 128 (256 x 4096 x 16384: 19 and 43;
+//    1024 x 4096 x 4096: 19 and 41).
+//  - 256 x 128 above (8192 x 4096 x 16384: 327, with 128 x 128 389, with 64 x 64 511; with gelu, bias and residual 391 and 446;
+//    2048 x 4096 x 4096: 31.5 and 31).
 //    256 x 256 with one workgroup a unit was 4 - 7% faster without an activation or a residual and 4 - 8% slower with
 //    both, whose work nothing hides then.
 // Tiles that do not fill the card are split along the contraction, two chunks of 512 each at least.

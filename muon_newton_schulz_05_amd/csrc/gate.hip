@@ -12,10 +12,11 @@
 //    probabilities in registers, workgroups leave partial sums, the join adds them in order.  c_e are integer
 //    counts, exact in any order, so LDS atomics may make them.  dz_te = dloss E / T p_te (f_e - sum_i p_ti f_i).
 //
-// The logits are a few megabytes, and what bounds the kernels is the work between loads: per choice a maximum in the lane, log2 L
-// steps between lanes and the taking out of the key, per logit one exponential.  In us: gate 16384 x 64, top 8, bf16 5.9,
-// its gradient 4.8; 65536 x 256 35 and 21; balance loss of 65536 x 256, bf16, 17 and 6 - 9 for the join (one workgroup,
-// 512 KiB of sums), its gradient 23 (2.9 TB/s); 64 x 64 4 each.
+// What bounds them.  gate: per choice a maximum in the lane, log2 L steps between lanes and the taking out of the key, which
+// every lane repeats whether it held the choice or not.  balance loss: at most 256 workgroups of 16 waves, half of what the card
+// holds, with one exponential a logit between their loads, and a join by one workgroup; the gradient makes the softmax anew.  In
+// us: gate 16384 x 64, top 8, bf16 5.9, its gradient 4.9; 65536 x 256 33 and 15 (over all experts 24), float32 41 and
+// 20; balance loss of 65536 x 256, bf16, 17 and 8.5 for the join (512 KiB of sums), its gradient 23 (2.9 TB/s); 64 x 64 4 each.
 //
 // A masked token takes no part in anything, whatever its logits hold.  Logits of -inf are experts that cannot be
 // chosen: their probability is zero, and a row of nothing else has no choice and no probabilities.

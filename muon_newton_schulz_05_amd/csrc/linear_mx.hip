@@ -14,11 +14,12 @@
 //    eight waves takes every eighth chunk of 512 values for all rows, and they add up in order in LDS.
 //
 // What bounds it.  A loop of nothing but these instructions on random operands reaches 6.6 - 6.8 PFLOP/s under the card's
-// power limit (9.4 - 9.7 on zeros).  16384^3: 5.0 (1750 us), the matrix cores 72% busy at 1.68 GHz, so that what moves
-// operands takes its part of the power; 8192 x 16384 x 4096: 4.8 (230 us).  8192 x 4096 x 16384 with gelu, bias and
-// residual: 358 us, with the bias alone 283: with 32 slices a tile, starts and epilogues are 20 - 35% of the time, and only
+// power limit (9.4 - 9.7 on zeros).  Times of the product alone, medians of several sessions: 16384^3 1750 - 1855 us (4.7 - 5.0
+// PFLOP/s), the matrix cores 72% busy at 1.68 GHz, so that what moves operands takes its part of the power; 8192 x 16384 x 4096
+// 230 - 255 (4.3 - 4.8).  8192 x 4096 x 16384 with gelu, bias and residual 358 - 380, with the bias alone 283 - 312: with 32
+// slices a tile, starts and epilogues are 20 - 35% of the time, and only
 // partly behind another workgroup's products (y written and the residual read are 512 MiB).  Stores that pass the caches by took 6 - 16% off, and more than that
-// on top of the kernel that reads y next.  1 x 4096 x 16384: 9.2 us, the weight's 36 MB at 3.9 TB/s, start and end included.
+// on top of the kernel that reads y next.  1 x 4096 x 16384, the whole call: 9.4 us, the weight's 36 MB at 3.8 TB/s, start and end included.
 #include "gemm.h"
 #include "mx_device.h"
 

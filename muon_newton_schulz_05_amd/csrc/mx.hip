@@ -6,7 +6,9 @@
 // with an infinity or NaN has scale 255, which is NaN, and values of zero.  The matrix instructions take these scales
 // as they are.
 //
-// Bound by memory: a weight [4096, 16384] in bf16 takes 29 us (5.9 TB/s), back 28 (6.2), rows of [49152, 2048] 48 (5.3).
+// Bound by memory.  bf16, operands that come from HBM: a weight [4096, 16384] held [K, N] takes 38 us (4.4 TB/s over what is read
+// and written), held [N, K] 39, back 46 (3.7), rows of [49152, 2048] 54 (4.8), of [8192, 4096] 23 (3.7).  Operands that the
+// memory-side cache still holds: 29, 33, 27, 46 and 19.
 #include "mx_device.h"
 
 namespace muon {

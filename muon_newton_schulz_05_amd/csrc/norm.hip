@@ -207,8 +207,9 @@ __device__ __forceinline__ void load_sum(const A& a, int64_t row, int64_t col, i
   for (int i = 0; i < 8; ++i) v[i] += r[i];
 }
 
-// Rows longer than the registers of a workgroup hold: read three times (4096 x 16384 bf16, gradient: 233 us, 2.3 TB/s
-// over what it has to read once).
+// Rows longer than the registers of a workgroup hold: read three times, the gradient's twice and once more for the
+// sums over rows (4096 x 16384 bf16: 117 + 86 + 5 us, 1.9 TB/s over what it has to read and write once; with residual and ds 181 +
+// 124 + 5, 2.2 TB/s; rows of 8192, which one workgroup holds: 66 + 6 with both, 4.7).
 constexpr int kWide = 1024, kWideCols = 16384, kWideGradCols = 8192;
 constexpr int64_t kWideGrid = 1 << 20;  // a launch holds fewer than 2^32 threads
 
